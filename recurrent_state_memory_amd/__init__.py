@@ -17,10 +17,17 @@ Entry points (same names as the C ABI):
   returns (o, Sk_out, Sv_out)
 * ``gdr_perm_fwd``    -- the delta rule with partial-permutation transitions
   (include/gdr_perm.h), returns (o, S_out)
+* ``gdr_scan_fwd``, ``gdr_scan_bwd``, ``gdr_scan_step`` and their ``_gated``
+  forms -- the channelwise gated linear recurrence (include/gdr_scan.h)
+* ``gdr_norm_fwd``, ``gdr_norm_bwd`` -- layer norm (include/gdr_norm.h)
+* ``gdr_ckpt8_pack``, ``gdr_ckpt8_unpack`` -- activations kept in 8 bits for the
+  backward (include/gdr_ckpt8.h)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -143,6 +150,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.gdr_raven_fwd.restype = ctypes.c_int
     lib.gdr_perm_fwd.argtypes = [ctypes.POINTER(PermArgs), _vp]
     lib.gdr_perm_fwd.restype = ctypes.c_int
+    for name, struct in _CHANNELWISE.items():
+        getattr(lib, name).argtypes = [ctypes.POINTER(struct), _vp]
+        getattr(lib, name).restype = ctypes.c_int
+    for name, struct in _CHANNELWISE_WS.items():
+        getattr(lib, name).argtypes = [ctypes.POINTER(struct)]
+        getattr(lib, name).restype = ctypes.c_size_t
     lib.gdr_status_str.argtypes = [ctypes.c_int]
     lib.gdr_status_str.restype = ctypes.c_char_p
     lib.gdr_abi_version.argtypes = []
@@ -653,3 +666,445 @@ def gdr_perm_fwd(q, k, v, w, src, beta, *, S0=None, o=None, S_out=None, return_s
     a.S0, a.o, a.S_out = _ptr(S0), _ptr(o), _ptr(S_out)
     _check(call_perm_fwd(a, _stream(stream)))
     return o, S_out
+
+
+# ------------------------------------------------------------ channelwise operators
+GDR_SCAN_BLOCK = 32       # tokens between two saved states (include/gdr_scan.h)
+GDR_CKPT8_GROUP = 128     # values that share one exponent (include/gdr_ckpt8.h)
+
+
+class ScanArgs(ctypes.Structure):
+    """Mirror of ``gdr_scan_args`` (include/gdr_scan.h)."""
+    _fields_ = [
+        ("B", _i32), ("T", _i32), ("C", _i32), ("io_dtype", _i32),
+        ("x", _vp), ("alpha", _vp), ("decay_x", _vp), ("decay_a", _vp), ("gate_x", _vp),
+        ("normalise", _i32), ("reserved", _i32), ("h0", _vp), ("y", _vp), ("h_out", _vp),
+        ("ckpt", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    """Mirror of ``gdr_scan_bwd_args`` (include/gdr_scan.h)."""
+    _fields_ = [
+        ("B", _i32), ("T", _i32), ("C", _i32), ("io_dtype", _i32),
+        ("x", _vp), ("x_exp", _vp), ("alpha", _vp), ("decay_x", _vp), ("decay_a", _vp),
+        ("gate_x", _vp), ("normalise", _i32), ("reserved", _i32), ("h0", _vp), ("ckpt", _vp),
+        ("grad_y", _vp), ("grad_h", _vp), ("grad_x", _vp), ("grad_alpha", _vp),
+        ("grad_decay_x", _vp), ("grad_decay_a", _vp), ("grad_gate_x", _vp), ("grad_h0", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ScanStepArgs(ctypes.Structure):
+    """Mirror of ``gdr_scan_step_args`` (include/gdr_scan.h)."""
+    _fields_ = [
+        ("N", _i32), ("C", _i32), ("io_dtype", _i32), ("normalise", _i32),
+        ("x", _vp), ("alpha", _vp), ("decay_x", _vp), ("decay_a", _vp), ("gate_x", _vp),
+        ("h", _vp), ("h_out", _vp), ("y", _vp),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of ``gdr_norm_args`` (include/gdr_norm.h)."""
+    _fields_ = [
+        ("R", ctypes.c_int64), ("D", _i32), ("io_dtype", _i32), ("eps", ctypes.c_float),
+        ("reserved", _i32), ("x", _vp), ("weight", _vp), ("bias", _vp), ("y", _vp),
+        ("mean", _vp), ("rstd", _vp), ("x_code", _vp), ("x_exp", _vp),
+    ]
+
+
+class NormBwdArgs(ctypes.Structure):
+    """Mirror of ``gdr_norm_bwd_args`` (include/gdr_norm.h)."""
+    _fields_ = [
+        ("R", ctypes.c_int64), ("D", _i32), ("io_dtype", _i32),
+        ("x", _vp), ("x_exp", _vp), ("mean", _vp), ("rstd", _vp), ("weight", _vp),
+        ("grad_y", _vp), ("grad_x", _vp), ("grad_weight", _vp), ("grad_bias", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class Ckpt8PackArgs(ctypes.Structure):
+    """Mirror of ``gdr_ckpt8_pack_args`` (include/gdr_ckpt8.h)."""
+    _fields_ = [("R", ctypes.c_int64), ("D", _i32), ("io_dtype", _i32),
+                ("x", _vp), ("code", _vp), ("exp", _vp)]
+
+
+class Ckpt8UnpackArgs(ctypes.Structure):
+    """Mirror of ``gdr_ckpt8_unpack_args`` (include/gdr_ckpt8.h)."""
+    _fields_ = [("R", ctypes.c_int64), ("D", _i32), ("io_dtype", _i32),
+                ("code", _vp), ("exp", _vp), ("x", _vp)]
+
+
+_CHANNELWISE = {"gdr_scan_fwd": ScanArgs, "gdr_scan_bwd": ScanBwdArgs,
+                "gdr_scan_step": ScanStepArgs, "gdr_norm_fwd": NormArgs,
+                "gdr_norm_bwd": NormBwdArgs, "gdr_ckpt8_pack": Ckpt8PackArgs,
+                "gdr_ckpt8_unpack": Ckpt8UnpackArgs}
+_CHANNELWISE_WS = {"gdr_scan_fwd_workspace": ScanArgs, "gdr_scan_bwd_workspace": ScanBwdArgs,
+                   "gdr_norm_bwd_workspace": NormBwdArgs}
+
+
+def call_channelwise(name: str, args, stream=None) -> int:
+    """Raw call of a channelwise entry point (``gdr_scan_fwd``, ``gdr_scan_bwd``,
+    ``gdr_scan_step``, ``gdr_norm_fwd``, ``gdr_norm_bwd``, ``gdr_ckpt8_pack``,
+    ``gdr_ckpt8_unpack``) with its filled struct; returns the status code."""
+    s = stream if isinstance(stream, ctypes.c_void_p) else (
+        ctypes.c_void_p(0) if stream is None else _stream(stream))
+    return getattr(load_library(), name)(ctypes.byref(args), s)
+
+
+def _in(t, name, shape, dtype, dev):
+    """Device pointer of one argument after checking its shape, dtype, contiguity
+    and device (``_expect`` and ``_ptr`` in one, cheap enough for single-token calls)."""
+    if t is None or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        _expect(t, name, shape, dtype)
+    if t.device != dev:
+        if not t.is_cuda:
+            raise ValueError("gdr: tensors must live on the GPU")
+        raise ValueError(f"gdr: {name} is on {t.device}, expected {dev}")
+    return t.data_ptr()
+
+
+def _opt(t, name, shape, dtype, dev):
+    return None if t is None else _in(t, name, shape, dtype, dev)
+
+
+_NULL_CONTEXT = contextlib.nullcontext()
+
+
+def _on(dev, stream):
+    """Context in which a call on ``dev`` allocates and launches: the current
+    stream of ``dev``, or ``stream``, which must belong to it.  Outputs and
+    workspaces are allocated inside, so that the allocator ties them to the
+    stream that uses them."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError("gdr: tensors must live on the GPU")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"gdr: stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return _NULL_CONTEXT
+
+
+def _launch(entry, args, dev):
+    import torch
+    _check(entry(ctypes.byref(args), torch._C._cuda_getCurrentRawStream(dev.index)))
+
+
+def _workspace(need, workspace, dev):
+    """(pointer, bytes) of a workspace of ``need`` bytes, and the tensor that owns it."""
+    import torch
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif (workspace.dtype != torch.uint8 or workspace.numel() < need or workspace.device != dev
+          or not workspace.is_contiguous()):
+        raise ValueError(f"gdr: workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def _x8(x, lead, D, dev):
+    """Pointers of an 8-bit checkpoint (codes, exponents) of shape [*lead, D]."""
+    import torch
+    code, exp = x
+    return (_in(code, "x[0]", (*lead, D), torch.float8_e4m3fn, dev),
+            _in(exp, "x[1]", (*lead, -(-D // GDR_CKPT8_GROUP)), torch.uint8, dev))
+
+
+def _scan_fwd(x, alpha, decay_x, decay_a, gate_x, normalise, h0, y, h_out, ckpt, return_state, return_ckpt,
+              workspace, stream):
+    import torch
+    if x.dim() != 3:
+        raise ValueError("gdr: x must be [B,T,C]")
+    shape, io, f32, dev = x.shape, x.dtype, torch.float32, x.device
+    B, T, C = shape
+    a = ScanArgs(B, T, C, _io(x), _in(x, "x", shape, io, dev))
+    if alpha is not None:
+        a.alpha = _in(alpha, "alpha", shape, f32, dev)
+    else:
+        a.decay_x = _in(decay_x, "decay_x", shape, io, dev)
+        a.decay_a = _in(decay_a, "decay_a", (C,), f32, dev)
+        a.gate_x = _opt(gate_x, "gate_x", shape, io, dev)
+        a.normalise = int(bool(normalise))
+    a.h0 = _opt(h0, "h0", (B, C), f32, dev)
+    lib = load_library()
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty_like(x)
+        if h_out is None and return_state:
+            h_out = torch.empty((B, C), dtype=f32, device=dev)
+        cshape = (B, -(-T // GDR_SCAN_BLOCK), C)
+        if ckpt is None and return_ckpt:
+            ckpt = torch.empty(cshape, dtype=f32, device=dev)
+        a.y = _in(y, "y", shape, io, dev)
+        a.h_out = _opt(h_out, "h_out", (B, C), f32, dev)
+        a.ckpt = _opt(ckpt, "ckpt", cshape, f32, dev)
+        a.workspace, a.workspace_bytes, keep = _workspace(
+            lib.gdr_scan_fwd_workspace(ctypes.byref(a)), workspace, dev)
+        _launch(lib.gdr_scan_fwd, a, dev)
+    return y, h_out, ckpt
+
+
+def gdr_scan_fwd(x, alpha, *, h0=None, y=None, h_out=None, ckpt=None, return_state=True,
+                 return_ckpt=False, workspace=None, stream=None):
+    """Channelwise linear recurrence h_t = alpha_t h_{t-1} + x_t, y_t = h_t (see
+    ``gdr_scan_fwd`` in include/gdr_scan.h).
+
+    x [B,T,C] bf16 or fp32; alpha fp32 [B,T,C] in [0, 1] (0 starts anew); h0 fp32
+    [B,C] or None (zero).  Returns (y [B,T,C] like x, h_out fp32 [B,C], ckpt) --
+    h_out None unless ``return_state`` or given (it may be h0), ckpt fp32
+    [B,ceil(T/32),C] (the states before each 32 tokens, for the backward) None
+    unless ``return_ckpt`` or given.
+    """
+    if alpha is None:
+        raise ValueError("gdr: alpha is required")
+    return _scan_fwd(x, alpha, None, None, None, False, h0, y, h_out, ckpt, return_state, return_ckpt, workspace,
+                     stream)
+
+
+def gdr_scan_fwd_gated(x, decay_x, decay_a, *, gate_x=None, normalise=True, h0=None, y=None,
+                       h_out=None, ckpt=None, return_state=True, return_ckpt=False, workspace=None,
+                       stream=None):
+    """The recurrence with its gates computed in the kernel (include/gdr_scan.h):
+    u = decay_a softplus(decay_x), h_t = exp(-u_t) h_{t-1} + b_t x_t with
+    b = sigmoid(gate_x) (1 without gate_x), times sqrt(1 - exp(-2 u)) with ``normalise``.
+
+    x, decay_x, gate_x [B,T,C], all bf16 or all fp32; decay_a fp32 [C], >= 0; the
+    rest and the results as ``gdr_scan_fwd``.
+    """
+    if decay_x is None or decay_a is None:
+        raise ValueError("gdr: decay_x and decay_a are required")
+    return _scan_fwd(x, None, decay_x, decay_a, gate_x, normalise, h0, y, h_out, ckpt, return_state, return_ckpt,
+                     workspace, stream)
+
+
+def _scan_bwd(x, alpha, decay_x, decay_a, gate_x, normalise, grad_y, h0, grad_h, ckpt, need_grad_h0, workspace,
+              stream):
+    import torch
+    if grad_y.dim() != 3:
+        raise ValueError("gdr: grad_y must be [B,T,C]")
+    shape, io, f32, dev = grad_y.shape, grad_y.dtype, torch.float32, grad_y.device
+    B, T, C = shape
+    a = ScanBwdArgs(B, T, C, _io(grad_y))
+    if isinstance(x, tuple):
+        a.x, a.x_exp = _x8(x, (B, T), C, dev)
+    else:
+        a.x = _in(x, "x", shape, io, dev)
+    if alpha is not None:
+        a.alpha = _in(alpha, "alpha", shape, f32, dev)
+    else:
+        a.decay_x = _in(decay_x, "decay_x", shape, io, dev)
+        a.decay_a = _in(decay_a, "decay_a", (C,), f32, dev)
+        a.gate_x = _opt(gate_x, "gate_x", shape, io, dev)
+        a.normalise = int(bool(normalise))
+    if ckpt is not None and h0 is not None:
+        raise ValueError("gdr: pass either ckpt or h0, not both (ckpt holds the start state)")
+    a.h0 = _opt(h0, "h0", (B, C), f32, dev)
+    a.ckpt = _opt(ckpt, "ckpt", (B, -(-T // GDR_SCAN_BLOCK), C), f32, dev)
+    a.grad_y = _in(grad_y, "grad_y", shape, io, dev)
+    a.grad_h = _opt(grad_h, "grad_h", (B, C), f32, dev)
+    lib = load_library()
+    g = {}
+    with _on(dev, stream):
+        g["x"] = torch.empty(shape, dtype=io, device=dev)
+        a.grad_x = g["x"].data_ptr()
+        if alpha is not None:
+            g["alpha"] = torch.empty(shape, dtype=f32, device=dev)
+            a.grad_alpha = g["alpha"].data_ptr()
+        else:
+            g["decay_x"] = torch.empty(shape, dtype=io, device=dev)
+            g["decay_a"] = torch.empty((C,), dtype=f32, device=dev)
+            a.grad_decay_x, a.grad_decay_a = g["decay_x"].data_ptr(), g["decay_a"].data_ptr()
+            if gate_x is not None:
+                g["gate_x"] = torch.empty(shape, dtype=io, device=dev)
+                a.grad_gate_x = g["gate_x"].data_ptr()
+        if need_grad_h0:
+            g["h0"] = torch.empty((B, C), dtype=f32, device=dev)
+            a.grad_h0 = g["h0"].data_ptr()
+        a.workspace, a.workspace_bytes, keep = _workspace(
+            lib.gdr_scan_bwd_workspace(ctypes.byref(a)), workspace, dev)
+        _launch(lib.gdr_scan_bwd, a, dev)
+    return g
+
+
+def gdr_scan_bwd(x, alpha, grad_y, *, h0=None, grad_h=None, ckpt=None, need_grad_h0=True,
+                 workspace=None, stream=None):
+    """Gradients of ``gdr_scan_fwd`` (``gdr_scan_bwd`` in include/gdr_scan.h).
+
+    x, alpha and h0 as the forward's; grad_y [B,T,C] like x, grad_h fp32 [B,C] or
+    None.  ``ckpt`` (the forward's, in place of h0) saves the second run of the
+    recurrence.  x may be an 8-bit checkpoint, the tuple ``gdr_ckpt8_pack``
+    returned.  Returns a dict: x (like grad_y), alpha (fp32) and, when
+    ``need_grad_h0``, h0 (fp32).  The workspace (``gdr_scan_bwd_workspace``
+    bytes) is allocated here unless a large enough uint8 tensor is passed.
+    """
+    if alpha is None:
+        raise ValueError("gdr: alpha is required")
+    return _scan_bwd(x, alpha, None, None, None, False, grad_y, h0, grad_h, ckpt, need_grad_h0, workspace, stream)
+
+
+def gdr_scan_bwd_gated(x, decay_x, decay_a, grad_y, *, gate_x=None, normalise=True, h0=None, grad_h=None,
+                       ckpt=None, need_grad_h0=True, workspace=None, stream=None):
+    """Gradients of ``gdr_scan_fwd_gated``; arguments as there and as
+    ``gdr_scan_bwd``.  Returns a dict: x, decay_x and (with gate_x) gate_x like
+    grad_y, decay_a fp32 [C] and, when ``need_grad_h0``, h0 fp32 [B,C]."""
+    if decay_x is None or decay_a is None:
+        raise ValueError("gdr: decay_x and decay_a are required")
+    return _scan_bwd(x, None, decay_x, decay_a, gate_x, normalise, grad_y, h0, grad_h, ckpt, need_grad_h0, workspace,
+                     stream)
+
+
+def _scan_step(h, x, alpha, decay_x, decay_a, gate_x, normalise, h_out, y, stream):
+    import torch
+    if x.dim() != 2:
+        raise ValueError("gdr: x must be [N,C]")
+    shape, io, f32, dev = x.shape, x.dtype, torch.float32, x.device
+    N, C = shape
+    code_io = _io(x)
+    if h_out is None:
+        h_out = h
+    hp = _in(h, "h", shape, f32, dev)
+    xp = _in(x, "x", shape, io, dev)
+    ho = hp if h_out is h else _in(h_out, "h_out", shape, f32, dev)
+    if alpha is not None:
+        gates = (_in(alpha, "alpha", shape, f32, dev), None, None, None)
+    else:
+        gates = (None, _in(decay_x, "decay_x", shape, io, dev), _in(decay_a, "decay_a", (C,), f32, dev),
+                 _opt(gate_x, "gate_x", shape, io, dev))
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty_like(x)
+        a = ScanStepArgs(N, C, code_io, int(bool(normalise)), xp, *gates, hp, ho, _in(y, "y", shape, io, dev))
+        _launch(load_library().gdr_scan_step, a, dev)
+    return y
+
+
+def gdr_scan_step(h, x, alpha, *, h_out=None, y=None, stream=None):
+    """One token of ``gdr_scan_fwd`` on N states (``gdr_scan_step`` in
+    include/gdr_scan.h).  h [N,C] fp32, overwritten unless ``h_out`` is given;
+    x [N,C] bf16 or fp32, alpha fp32 [N,C].  Returns y [N,C] like x."""
+    if alpha is None:
+        raise ValueError("gdr: alpha is required")
+    return _scan_step(h, x, alpha, None, None, None, False, h_out, y, stream)
+
+
+def gdr_scan_step_gated(h, x, decay_x, decay_a, *, gate_x=None, normalise=True, h_out=None, y=None,
+                        stream=None):
+    """One token of ``gdr_scan_fwd_gated`` on N states: x, decay_x, gate_x [N,C],
+    decay_a fp32 [C], the rest as ``gdr_scan_step``."""
+    if decay_x is None or decay_a is None:
+        raise ValueError("gdr: decay_x and decay_a are required")
+    return _scan_step(h, x, None, decay_x, decay_a, gate_x, normalise, h_out, y, stream)
+
+
+def gdr_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, return_ckpt8=False, stream=None):
+    """Layer norm over the last dimension (see ``gdr_norm_fwd`` in include/gdr_norm.h).
+
+    x [...,D] bf16 or fp32; weight, bias fp32 [D] or None.  Returns (y like x,
+    mean, rstd, ckpt8): the statistics fp32 [...], and with ``return_ckpt8`` the
+    8-bit copy of x for the backward (the tuple of ``gdr_ckpt8_pack``), else None.
+    """
+    import torch
+    if x.dim() < 1:
+        raise ValueError("gdr: x must be [...,D]")
+    shape, io, f32, dev = x.shape, x.dtype, torch.float32, x.device
+    lead, D = shape[:-1], shape[-1]
+    R, code_io = math.prod(lead), _io(x)
+    xp = _in(x, "x", shape, io, dev)
+    wp = _opt(weight, "weight", (D,), f32, dev)
+    bp = _opt(bias, "bias", (D,), f32, dev)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty_like(x)
+        yp = _in(y, "y", shape, io, dev)
+        mean = torch.empty(lead, dtype=f32, device=dev)
+        rstd = torch.empty(lead, dtype=f32, device=dev)
+        code, kept = (None, None), None
+        if return_ckpt8:
+            kept = (torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev),
+                    torch.empty((*lead, -(-D // GDR_CKPT8_GROUP)), dtype=torch.uint8, device=dev))
+            code = kept[0].data_ptr(), kept[1].data_ptr()
+        a = NormArgs(R, D, code_io, eps, 0, xp, wp, bp, yp, mean.data_ptr(), rstd.data_ptr(), *code)
+        _launch(load_library().gdr_norm_fwd, a, dev)
+    return y, mean, rstd, kept
+
+
+def gdr_norm_bwd(grad_y, x, mean, rstd, weight=None, *, need_grad_weight=True, need_grad_bias=True,
+                 workspace=None, stream=None):
+    """Gradients of ``gdr_norm_fwd`` (``gdr_norm_bwd`` in include/gdr_norm.h).
+
+    grad_y [...,D]; x like it, or the forward's ckpt8 tuple; mean, rstd and weight
+    as the forward's.  Returns a dict: x like grad_y, and weight and bias fp32 [D]
+    unless not needed.  The workspace (``gdr_norm_bwd_workspace`` bytes) is
+    allocated here unless a large enough uint8 tensor is passed.
+    """
+    import torch
+    if grad_y.dim() < 1:
+        raise ValueError("gdr: grad_y must be [...,D]")
+    shape, io, f32, dev = grad_y.shape, grad_y.dtype, torch.float32, grad_y.device
+    lead, D = shape[:-1], shape[-1]
+    a = NormBwdArgs(math.prod(lead), D, _io(grad_y))
+    if isinstance(x, tuple):
+        a.x, a.x_exp = _x8(x, lead, D, dev)
+    else:
+        a.x = _in(x, "x", shape, io, dev)
+    a.mean, a.rstd = _in(mean, "mean", lead, f32, dev), _in(rstd, "rstd", lead, f32, dev)
+    a.weight = _opt(weight, "weight", (D,), f32, dev)
+    a.grad_y = _in(grad_y, "grad_y", shape, io, dev)
+    lib = load_library()
+    g = {}
+    with _on(dev, stream):
+        g["x"] = torch.empty(shape, dtype=io, device=dev)
+        a.grad_x = g["x"].data_ptr()
+        if need_grad_weight:
+            g["weight"] = torch.empty((D,), dtype=f32, device=dev)
+            a.grad_weight = g["weight"].data_ptr()
+        if need_grad_bias:
+            g["bias"] = torch.empty((D,), dtype=f32, device=dev)
+            a.grad_bias = g["bias"].data_ptr()
+        a.workspace, a.workspace_bytes, keep = _workspace(
+            lib.gdr_norm_bwd_workspace(ctypes.byref(a)), workspace, dev)
+        _launch(lib.gdr_norm_bwd, a, dev)
+    return g
+
+
+def gdr_ckpt8_pack(x, *, stream=None):
+    """8-bit checkpoint of an activation (``gdr_ckpt8_pack`` in include/gdr_ckpt8.h):
+    x [...,D] bf16 or fp32 -> (codes float8_e4m3fn [...,D], exponents uint8
+    [...,ceil(D/128)]), each code standing for code * 2^(exponent - 127)."""
+    import torch
+    if x.dim() < 1:
+        raise ValueError("gdr: x must be [...,D]")
+    shape, dev = x.shape, x.device
+    lead, D = shape[:-1], shape[-1]
+    code_io = _io(x)
+    xp = _in(x, "x", shape, x.dtype, dev)
+    with _on(dev, stream):
+        code = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+        exp = torch.empty((*lead, -(-D // GDR_CKPT8_GROUP)), dtype=torch.uint8, device=dev)
+        a = Ckpt8PackArgs(math.prod(lead), D, code_io, xp, code.data_ptr(), exp.data_ptr())
+        _launch(load_library().gdr_ckpt8_pack, a, dev)
+    return code, exp
+
+
+def gdr_ckpt8_unpack(code, exp, *, dtype=None, x=None, stream=None):
+    """The values of an 8-bit checkpoint (``gdr_ckpt8_unpack`` in include/gdr_ckpt8.h),
+    in ``dtype`` (bf16 by default, or fp32), written to ``x`` when given."""
+    import torch
+    if code.dim() < 1:
+        raise ValueError("gdr: the codes must be [...,D]")
+    shape, dev = code.shape, code.device
+    lead, D = shape[:-1], shape[-1]
+    if dtype is None:
+        dtype = torch.bfloat16 if x is None else x.dtype
+    cp = _in(code, "code", shape, torch.float8_e4m3fn, dev)
+    ep = _in(exp, "exp", (*lead, -(-D // GDR_CKPT8_GROUP)), torch.uint8, dev)
+    with _on(dev, stream):
+        if x is None:
+            x = torch.empty(shape, dtype=dtype, device=dev)
+        a = Ckpt8UnpackArgs(math.prod(lead), D, _io(x), cp, ep, _in(x, "x", shape, dtype, dev))
+        _launch(load_library().gdr_ckpt8_unpack, a, dev)
+    return x
