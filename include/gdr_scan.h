@@ -20,7 +20,8 @@
  * exact reset (it starts a new sequence packed behind another), alpha = 1 with
  * x = 0 leaves the state as it is (padding).  NaN and Inf propagate.
  *
- * Sizes: any B, C and T >= 1, B * T * C < 2^40, C <= 2^18.  Every pointer is
+ * Sizes: any B, C and T >= 1 with B * T * C < 2^40, C <= 2^18 and
+ * B * ceil(C/64) * ceil(T/256) < 2^23.  Every pointer is
  * aligned to its element; rows whose C is a multiple of 4, in buffers aligned
  * to 4 elements, move 4 channels at a time.  Outputs overlap neither inputs nor
  * each other (GDR_ERR_ARG), except that h_out may equal h0 (and the step's
@@ -73,7 +74,8 @@ gdr_status gdr_scan_fwd(const gdr_scan_args *args, void *stream);
  *   dL/du = G a (b x a / (1 - a^2) [if normalise] - h_{t-1}),
  *   grad_decay_x = dL/du decay_a sigmoid(decay_x),
  *   grad_decay_a = sum over (b, t) of dL/du softplus(decay_x).
- * The quotient is taken as 0 where 1 - a^2 is 0 (a decay that has underflowed).
+ * The quotient is taken as 0 where 1 - a^2 is below 2^-120 (the term vanishes with
+ * its root; at decay_a = 0 it has no limit).
  * States inside a block of 32 tokens are computed again from ckpt (as
  * gdr_scan_fwd wrote it); without ckpt the whole recurrence is run again from
  * h0, and ckpt and h0 are not given together.  x may be 8-bit: then x_exp holds

@@ -1,134 +1,320 @@
 // scan_bwd.hip -- gradients of the channelwise gated linear recurrence, gfx950.
 //
-// One thread per (batch row, channel).  Blocks of 32 tokens are taken from the
-// last to the first: the states inside a block are computed again from its
-// start state, then G_t = grad_y_t + a_{t+1} G_{t+1} runs backwards through it.
-#include "chan_device.h"
+// The tile and its joins: scan_tile.h.  States run forwards inside each wave's
+// block of 32 tokens from the block's saved state; K_t = a_t G_t, what a token
+// hands to the one before it, runs backwards over the whole sequence, handed from
+// tile to tile with the last tiles first.  G_t = grad_y_t + K_{t+1}, so a run of
+// tokens takes K to P K + Q with P the same product of decays.
+//
+// A thread keeps a and v = b x of its 32 elements; what the gradients need besides
+// (the softplus, the sigmoids, 1 - a^2) is evaluated again from the inputs' raw
+// registers, which costs less than the registers to keep it would.
+//
+// grad_decay_a sums over all tokens: registers, lane groups, waves (one LDS pass
+// in a fixed order), then one partial row per tile that sum_kernel adds up, again
+// in a fixed order.
 #include "scan_gate.h"
-#include "scan_kernels.h"
+#include "scan_tile.h"
 
 namespace gdr {
 namespace scan {
 
-using chan::ld;
-using chan::st;
+// Below this, 1 - a^2 counts as 0: the term it divides vanishes with its root.
+constexpr float kLeastM = 0x1p-120f;
 
-struct Gates {
-  float a, s, m, sp, sig;   // decay, input gate, 1 - a^2, softplus, sigmoid(decay_x)
+struct BwdP {
+  int B, T, C, normalise;
+  int nchain, nct, nt;
+  const void* x;
+  const uint8_t* x_exp;
+  const float* alpha;
+  const void* decay_x;
+  const float* decay_a;
+  const void* gate_x;
+  const float* ckpt;
+  const void* grad_y;
+  const float* grad_h;
+  void* grad_x;
+  float* grad_alpha;
+  void* grad_decay_x;
+  void* grad_gate_x;
+  float* grad_h0;
+  float* part;       // [tiles of a chain * B][C] partial sums of grad_decay_a
+  Chains ch;
 };
 
-template <typename T>
-__device__ inline Gates gates(const gdr_scan_bwd_args& p, float A, size_t i) {
-  Gates g{0.f, 1.f, 1.f, 0.f, 0.f};
-  if (p.alpha) {
-    g.a = p.alpha[i];
-    return g;
-  }
-  float w;
-  const float d = ld((const T*)p.decay_x + i);
-  g.sp = softplus(d, w);
-  const float r = __builtin_amdgcn_rcpf(1.f + w);
-  g.sig = d > 0.f ? r : w * r;
-  g.a = exp_fast(-A * g.sp);
-  if (p.gate_x) g.s = sigmoid(ld((const T*)p.gate_x + i));
-  if (p.normalise) g.m = one_minus_sq(A * g.sp, g.a);
-  return g;
-}
+template <typename T, typename X, int KIND, bool VEC>
+__global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(BwdP p) {
+  constexpr bool kCodes = !__is_same(X, T);
+  __shared__ float2 run[kWaves][kTileC];    // (P, Q) of each wave
+  __shared__ float from[kWaves][kTileC];    // K behind each wave; then the waves' sums
+  const Place q = take_place(p.C, p.nchain, p.nct, p.ch.ticket);
+  const int tile = p.nt - 1 - q.tt;         // the last tokens come first
+  const int C = p.C, t0 = tile * kTileT;
+  const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);
+  const int r0 = q.wave * GDR_SCAN_BLOCK + q.grp * S;
+  const size_t base = ((size_t)q.b * p.T + t0) * C;
+  const int e0 = r0 * C + q.c;
+  const int ox = q.nv > 0 ? e0 * size_of<X> : kNoLane, ot = q.nv > 0 ? e0 * size_of<T> : kNoLane;
+  const int oa = q.nv > 0 ? e0 * 4 : kNoLane;
+  const uint32_t tbytes = rows * C * size_of<T>;
 
-template <typename T>
-__device__ inline float load_x(const gdr_scan_bwd_args& p, size_t row, int c) {
-  const size_t i = row * p.C + c;
-  if (!p.x_exp) return ld((const T*)p.x + i);
-  return chan::code1_f32(((const uint8_t*)p.x)[i]) * chan::scale_of(p.x_exp[row * ((p.C + 127) / 128) + c / 128]);
-}
-
-template <typename T>
-__global__ __launch_bounds__(64) void ckpt_kernel(gdr_scan_bwd_args p, float* ckpt) {
-  const size_t n = (size_t)blockIdx.x * 64 + threadIdx.x;
-  if (n >= (size_t)p.B * p.C) return;
-  const int b = (int)(n / p.C), c = (int)(n % p.C);
-  const float A = p.alpha ? 0.f : p.decay_a[c];
-  float h = p.h0 ? p.h0[n] : 0.f;
-  for (int t = 0; t < p.T; ++t) {
-    const size_t row = (size_t)b * p.T + t;
-    if (t % GDR_SCAN_BLOCK == 0) ckpt[((size_t)b * blocks_of(p.T) + t / GDR_SCAN_BLOCK) * p.C + c] = h;
-    const Gates g = gates<T>(p, A, row * p.C + c);
-    h = fmaf(g.a, h, load_x<T>(p, row, c) * g.s * __builtin_amdgcn_sqrtf(g.m));
-  }
-}
-
-template <typename T>
-__global__ __launch_bounds__(64) void scan_bwd_kernel(gdr_scan_bwd_args p, const float* ckpt, float* ga) {
-  const size_t n = (size_t)blockIdx.x * 64 + threadIdx.x;
-  if (n >= (size_t)p.B * p.C) return;
-  const int b = (int)(n / p.C), c = (int)(n % p.C);
-  const float A = p.alpha ? 0.f : p.decay_a[c];
-  float K = p.grad_h ? p.grad_h[n] : 0.f, sum = 0.f;
-  for (int j = (int)blocks_of(p.T) - 1; j >= 0; --j) {
-    const int t0 = j * GDR_SCAN_BLOCK, t1 = t0 + GDR_SCAN_BLOCK < p.T ? t0 + GDR_SCAN_BLOCK : p.T;
-    float prev[GDR_SCAN_BLOCK];
-    float h = ckpt[((size_t)b * blocks_of(p.T) + j) * p.C + c];
-    for (int t = t0; t < t1; ++t) {
-      const size_t row = (size_t)b * p.T + t;
-      const Gates g = gates<T>(p, A, row * p.C + c);
-      prev[t - t0] = h;
-      h = fmaf(g.a, h, load_x<T>(p, row, c) * g.s * __builtin_amdgcn_sqrtf(g.m));
+  typename Four<X>::R rx[S];
+  typename Four<T>::R ry[S];
+  Four<float>::R ra[KIND == 0 ? S : 1];
+  typename Four<T>::R rd[KIND == 0 ? 1 : S], rg[KIND == 2 ? S : 1];
+  float xs[kCodes ? S : 1];
+  {
+    const rsrc_t bx = buffer((const char*)p.x + base * size_of<X>, rows * C * size_of<X>);
+    const rsrc_t by = buffer((const T*)p.grad_y + base, tbytes);
+    if constexpr (KIND == 0) {
+      const rsrc_t ba = buffer(p.alpha + base, rows * C * 4);
+#pragma unroll
+      for (int i = 0; i < S; ++i) ra[i] = Four<float>::template load<VEC>(ba, oa + i * C * 4, q.nv);
+    } else {
+      const rsrc_t bd = buffer((const T*)p.decay_x + base, tbytes);
+#pragma unroll
+      for (int i = 0; i < S; ++i) rd[i] = Four<T>::template load<VEC>(bd, ot + i * C * size_of<T>, q.nv);
     }
-    for (int t = t1 - 1; t >= t0; --t) {
-      const size_t row = (size_t)b * p.T + t, i = row * p.C + c;
-      const Gates g = gates<T>(p, A, i);
-      const float G = K + ld((const T*)p.grad_y + i), bb = g.s * __builtin_amdgcn_sqrtf(g.m);
-      st((T*)p.grad_x + i, bb * G);
-      if (p.alpha) {
-        p.grad_alpha[i] = G * prev[t - t0];
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
+      ry[i] = Four<T>::template load<VEC>(by, ot + i * C * size_of<T>, q.nv);
+    }
+    if constexpr (KIND == 2) {
+      const rsrc_t bg = buffer((const T*)p.gate_x + base, tbytes);
+#pragma unroll
+      for (int i = 0; i < S; ++i) rg[i] = Four<T>::template load<VEC>(bg, ot + i * C * size_of<T>, q.nv);
+    }
+    if constexpr (kCodes) {
+      const int ng = (C + 127) / 128;
+      const rsrc_t be = buffer(p.x_exp + ((size_t)q.b * p.T + t0) * ng, rows * ng);
+      const int oe = q.nv > 0 ? r0 * ng + q.c / 128 : kNoLane;
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        xs[i] = chan::scale_of(__builtin_amdgcn_raw_buffer_load_b8(be, oe + i * ng, 0, 0));
+    }
+  }
+  float A[V], h0[V];
+  const size_t nb = blocks_of(p.T), block = (size_t)tile * kWaves + q.wave;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    A[k] = KIND != 0 && k < q.nv ? p.decay_a[q.c + k] : 0.f;
+    h0[k] = k < q.nv && block < nb ? p.ckpt[((size_t)q.b * nb + block) * C + q.c + k] : 0.f;
+  }
+  const int cc = q.c0 + q.lane;
+  float k_in = 0.f;
+  if (q.wave == 0 && q.tt == 0 && p.grad_h && cc < C) k_in = p.grad_h[(size_t)q.b * C + cc];
+
+  // a and v; (P, H) forwards and (P, Q) backwards over the thread's run
+  float a[S][V], v[S][V], P[V], H[V], Q[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    P[k] = 1.f;
+    H[k] = Q[k] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float x = Four<X>::get(rx[i], k);
+      if constexpr (kCodes) x *= xs[i];
+      if constexpr (KIND == 0) {
+        a[i][k] = Four<float>::get(ra[i], k);
       } else {
-        const float v = bb * load_x<T>(p, row, c);
-        if (p.gate_x) st((T*)p.grad_gate_x + i, G * v * (1.f - g.s));
-        float in = -prev[t - t0];
-        if (p.normalise && g.m > 0.f) in += v * g.a / g.m;
-        const float du = G * g.a * in;
-        st((T*)p.grad_decay_x + i, du * A * g.sig);
-        sum += du * g.sp;
+        float w;
+        const float u = A[k] * softplus(Four<T>::get(rd[i], k), w);
+        a[i][k] = exp_fast(-u);
+        if constexpr (KIND == 2) x *= sigmoid(Four<T>::get(rg[i], k));
+        if (p.normalise) x *= __builtin_amdgcn_sqrtf(one_minus_sq(u, a[i][k]));
       }
-      K = g.a * G;
+      v[i][k] = x;
+    }
+    if (r0 + i >= rows) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        a[i][k] = 1.f;
+        v[i][k] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      P[k] *= a[i][k];
+      H[k] = fmaf(a[i][k], H[k], v[i][k]);
     }
   }
-  if (p.grad_h0) p.grad_h0[n] = K;
-  if (ga) ga[n] = sum;
+#pragma unroll
+  for (int i = S - 1; i >= 0; --i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) Q[k] = a[i][k] * (Four<T>::get(ry[i], k) + Q[k]);
+  float h[V], Pb[V], Qb[V];
+  {
+    float Pf[V], Pe[V], He[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) Pf[k] = P[k];
+    join_groups<true>(Pf, H, Pe, He, q.grp);
+#pragma unroll
+    for (int k = 0; k < V; ++k) h[k] = fmaf(Pe[k], h0[k], He[k]);   // the state before the run
+  }
+  join_groups<false>(P, Q, Pb, Qb, q.grp);
+  if (q.grp == 0) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) run[q.wave][q.cl + k] = float2{P[k], Q[k]};
+  }
+  __syncthreads();
+  if (q.wave == 0) {
+    float2 r[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) r[w] = w < q.nw ? run[w][q.lane] : float2{1.f, 0.f};
+    uint64_t* slot = p.ch.slots + (size_t)q.chain * kTileC + q.lane;
+    if (q.tt > 0) k_in = wait_for(slot, q.tt);
+    float kk[kWaves + 1];
+    kk[kWaves] = k_in;
+#pragma unroll
+    for (int w = kWaves - 1; w >= 0; --w) kk[w] = fmaf(r[w].x, kk[w + 1], r[w].y);
+    if (q.tt + 1 < p.nt) hand_over(slot, kk[0], q.tt + 1);
+    else if (p.grad_h0 && cc < C) p.grad_h0[(size_t)q.b * C + cc] = kk[0];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) from[w][q.lane] = kk[w + 1];
+  }
+  __syncthreads();
+  float K[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) K[k] = fmaf(Pb[k], from[q.wave][q.cl + k], Qb[k]);
+  float prev[S][V];
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      prev[i][k] = h[k];
+      h[k] = fmaf(a[i][k], h[k], v[i][k]);
+    }
+  const rsrc_t gx = buffer((const T*)p.grad_x + base, tbytes);
+  const rsrc_t gd = KIND == 0 ? buffer(p.grad_alpha + base, rows * C * 4) : buffer((const T*)p.grad_decay_x + base, tbytes);
+  const rsrc_t gg = KIND == 2 ? buffer((const T*)p.grad_gate_x + base, tbytes) : gx;
+  float sum[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) sum[k] = 0.f;
+#pragma unroll
+  for (int i = S - 1; i >= 0; --i) {
+    float ox_[V], od[V], og[V];
+    if constexpr (KIND != 0) forget(rd[i]);
+    if constexpr (KIND == 2) forget(rg[i]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float G = Four<T>::get(ry[i], k) + K[k];
+      const float ak = a[i][k];
+      K[k] = ak * G;
+      if constexpr (KIND == 0) {
+        ox_[k] = G;
+        od[k] = G * prev[i][k];
+      } else {
+        const float d = Four<T>::get(rd[i], k);
+        float w;
+        const float sp = softplus(d, w), rw = __builtin_amdgcn_rcpf(1.f + w);
+        float b = 1.f, in = -prev[i][k];
+        if constexpr (KIND == 2) {
+          const float s = sigmoid(Four<T>::get(rg[i], k));
+          b = s;
+          og[k] = G * v[i][k] * (1.f - s);
+        }
+        if (p.normalise) {
+          const float m = one_minus_sq(A[k] * sp, ak);
+          b *= __builtin_amdgcn_sqrtf(m);
+          in += m > kLeastM ? v[i][k] * ak * __builtin_amdgcn_rcpf(m) : 0.f;
+        }
+        ox_[k] = b * G;
+        const float du = r0 + i < rows ? K[k] * in : 0.f;
+        sum[k] = fmaf(du, sp, sum[k]);
+        od[k] = du * A[k] * (d > 0.f ? rw : w * rw);
+      }
+    }
+    Four<T>::template store<VEC>(gx, ot + i * C * size_of<T>, q.nv, ox_);
+    if constexpr (KIND == 0) Four<float>::template store<VEC>(gd, oa + i * C * 4, q.nv, od);
+    else Four<T>::template store<VEC>(gd, ot + i * C * size_of<T>, q.nv, od);
+    if constexpr (KIND == 2) Four<T>::template store<VEC>(gg, ot + i * C * size_of<T>, q.nv, og);
+  }
+  if constexpr (KIND != 0) {
+#pragma unroll
+    for (int dist = kSide; dist < 64; dist *= 2)
+#pragma unroll
+      for (int k = 0; k < V; ++k) sum[k] += __shfl_xor(sum[k], dist);
+    __syncthreads();   // `from` has been read
+    if (q.grp == 0) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) from[q.wave][q.cl + k] = sum[k];
+    }
+    __syncthreads();
+    if (q.wave == 0 && cc < C) {
+      float s = 0.f;
+      for (int w = 0; w < q.nw; ++w) s += from[w][q.lane];
+      p.part[((size_t)tile * p.B + q.b) * C + cc] = s;
+    }
+  }
 }
 
-__global__ __launch_bounds__(64) void sum_rows_kernel(const float* part, float* out, int rows, int C) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= C) return;
-  float s = 0.f;
-  for (int r = 0; r < rows; ++r) s += part[(size_t)r * C + c];
-  out[c] = s;
+// grad_decay_a[c]: 16 threads per channel take every 16th partial row, then join.
+__global__ __launch_bounds__(1024) void sum_kernel(const float* part, float* out, int rows, int C) {
+  __shared__ float s[16][64];
+  const int l = threadIdx.x & 63, y = threadIdx.x >> 6, c = blockIdx.x * 64 + l;
+  float t = 0.f;
+  if (c < C)
+    for (int r = y; r < rows; r += 16) t += part[(size_t)r * C + c];
+  s[y][l] = t;
+  __syncthreads();
+  if (y == 0 && c < C) {
+    for (int k = 1; k < 16; ++k) t += s[k][l];
+    out[c] = t;
+  }
 }
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t bwd_workspace(int B, int T, int C, bool gated, bool ckpt) {
-  return (ckpt ? 0 : align256((size_t)B * blocks_of(T) * C * 4)) + (gated ? align256((size_t)B * C * 4) : 0);
+  return align256(chain_bytes(B, T, C)) + (ckpt ? 0 : align256((size_t)B * blocks_of(T) * C * 4)) +
+         (gated ? align256(tiles_t(T) * B * C * 4) : 0);
 }
 
-template <typename T>
-static void launch(const gdr_scan_bwd_args& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((size_t)a.B * a.C + 63) / 64));
-  char* ws = (char*)a.workspace;
-  const float* ckpt = a.ckpt;
-  if (!ckpt) {
-    hipLaunchKernelGGL(ckpt_kernel<T>, grid, dim3(64), 0, s, a, (float*)ws);
-    ckpt = (const float*)ws;
-    ws += align256((size_t)a.B * blocks_of(a.T) * a.C * 4);
-  }
-  float* ga = a.alpha ? nullptr : (float*)ws;
-  hipLaunchKernelGGL(scan_bwd_kernel<T>, grid, dim3(64), 0, s, a, ckpt, ga);
-  if (ga) hipLaunchKernelGGL(sum_rows_kernel, dim3((a.C + 63) / 64), dim3(64), 0, s, ga, a.grad_decay_a, a.B, a.C);
+template <typename T, typename X, int KIND>
+static hipError_t launch_v(const BwdP& p, bool vec, hipStream_t s) {
+  const int nw = p.nt > 1 ? kWaves : (int)blocks_of(p.T);
+  const dim3 grid((unsigned)((size_t)p.nchain * p.nt)), block(64 * nw);
+  if (vec) hipLaunchKernelGGL((scan_bwd_kernel<T, X, KIND, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((scan_bwd_kernel<T, X, KIND, false>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, typename X>
+static hipError_t launch_kind(const BwdP& p, bool vec, hipStream_t s) {
+  if (p.alpha) return launch_v<T, X, 0>(p, vec, s);
+  return p.gate_x ? launch_v<T, X, 2>(p, vec, s) : launch_v<T, X, 1>(p, vec, s);
 }
 
 hipError_t launch_scan_bwd(const gdr_scan_bwd_args& a, hipStream_t s) {
-  if (a.io_dtype == GDR_BF16) launch<__bf16>(a, s);
-  else launch<float>(a, s);
+  char* ws = (char*)a.workspace;
+  char* rest = ws + align256(chain_bytes(a.B, a.T, a.C));
+  const float* ckpt = a.ckpt;
+  if (!ckpt) {
+    const hipError_t e = launch_ckpt(a, (float*)rest, ws, s);
+    if (e != hipSuccess) return e;
+    ckpt = (const float*)rest;
+    rest += align256((size_t)a.B * blocks_of(a.T) * a.C * 4);
+  }
+  BwdP p{a.B, a.T, a.C, a.normalise, (int)chains_of(a.B, a.C), (a.C + kTileC - 1) / kTileC, (int)tiles_t(a.T),
+         a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, ckpt, a.grad_y, a.grad_h, a.grad_x, a.grad_alpha,
+         a.grad_decay_x, a.grad_gate_x, a.grad_h0, a.alpha ? nullptr : (float*)rest, {}};
+  hipError_t e = reset_chains(ws, a.B, a.T, a.C, &p.ch, s);
+  if (e != hipSuccess) return e;
+  const size_t io = a.io_dtype == GDR_BF16 ? 2 : 4;
+  const bool vec = a.C % 4 == 0 && vec4_ok(a.x, a.x_exp ? 1 : io) && vec4_ok(a.alpha, 4) && vec4_ok(a.decay_x, io) &&
+                   vec4_ok(a.gate_x, io) && vec4_ok(a.grad_y, io) && vec4_ok(a.grad_x, io) && vec4_ok(a.grad_alpha, 4) &&
+                   vec4_ok(a.grad_decay_x, io) && vec4_ok(a.grad_gate_x, io);
+  if (a.io_dtype == GDR_BF16)
+    e = a.x_exp ? launch_kind<__bf16, Code8>(p, vec, s) : launch_kind<__bf16, __bf16>(p, vec, s);
+  else
+    e = a.x_exp ? launch_kind<float, Code8>(p, vec, s) : launch_kind<float, float>(p, vec, s);
+  if (e != hipSuccess || a.alpha) return e;
+  hipLaunchKernelGGL(sum_kernel, dim3((a.C + 63) / 64), dim3(1024), 0, s, p.part, a.grad_decay_a, p.nt * a.B, a.C);
   return hipGetLastError();
 }
 

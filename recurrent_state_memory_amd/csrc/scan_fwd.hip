@@ -1,15 +1,171 @@
 // scan_fwd.hip -- channelwise gated linear recurrence, forward and step, gfx950.
 //
-// One thread per (batch row, channel) walks the tokens in order.
-#include "chan_device.h"
+// The tile, its joins and the hand-over between tiles: scan_tile.h.  A thread
+// keeps a and v = b x of its 32 elements in registers between forming (P, H) of
+// its run and writing the outputs, so gates are evaluated once.
 #include "scan_gate.h"
-#include "scan_kernels.h"
+#include "scan_tile.h"
 
 namespace gdr {
 namespace scan {
 
 using chan::ld;
 using chan::st;
+
+struct FwdP {
+  int B, T, C, normalise;
+  int nchain, nct, nt;   // chains, channel tiles of a row, tiles of a chain
+  const void* x;
+  const uint8_t* x_exp;
+  const float* alpha;
+  const void* decay_x;
+  const float* decay_a;
+  const void* gate_x;
+  const float* h0;
+  void* y;
+  float* h_out;
+  float* ckpt;
+  Chains ch;
+};
+
+// KIND: 0 alpha given, 1 decay from its pre-activation, 2 with an input gate too.
+// X: the type x is read in (T, or Code8).
+template <typename T, typename X, int KIND, bool VEC>
+__global__ __launch_bounds__(64 * kWaves) void scan_fwd_kernel(FwdP p) {
+  constexpr bool kCodes = !__is_same(X, T);
+  __shared__ float2 run[kWaves][kTileC];    // (P, H) of each wave
+  __shared__ float from[kWaves][kTileC];    // the state before each wave
+  const Place q = take_place(p.C, p.nchain, p.nct, p.ch.ticket);
+  const int C = p.C, t0 = q.tt * kTileT;
+  const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);   // of the tile that exist
+  const int r0 = q.wave * GDR_SCAN_BLOCK + q.grp * S;      // the thread's first row
+  const size_t base = ((size_t)q.b * p.T + t0) * C;
+  const int e0 = r0 * C + q.c;                             // its first element from base
+
+  typename Four<X>::R rx[S];
+  Four<float>::R ra[KIND == 0 ? S : 1];
+  typename Four<T>::R rd[KIND == 0 ? 1 : S], rg[KIND == 2 ? S : 1];
+  float xs[kCodes ? S : 1];
+  {
+    const rsrc_t bx = buffer((const char*)p.x + base * size_of<X>, rows * C * size_of<X>);
+    const int ox = q.nv > 0 ? e0 * size_of<X> : kNoLane, ot = q.nv > 0 ? e0 * size_of<T> : kNoLane;
+    if constexpr (KIND == 0) {
+      const rsrc_t ba = buffer(p.alpha + base, rows * C * 4);
+      const int oa = q.nv > 0 ? e0 * 4 : kNoLane;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        ra[i] = Four<float>::template load<VEC>(ba, oa + i * C * 4, q.nv);
+        rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
+      }
+    } else {
+      const rsrc_t bd = buffer((const T*)p.decay_x + base, rows * C * size_of<T>);
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        rd[i] = Four<T>::template load<VEC>(bd, ot + i * C * size_of<T>, q.nv);
+        rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
+      }
+      if constexpr (KIND == 2) {
+        const rsrc_t bg = buffer((const T*)p.gate_x + base, rows * C * size_of<T>);
+#pragma unroll
+        for (int i = 0; i < S; ++i) rg[i] = Four<T>::template load<VEC>(bg, ot + i * C * size_of<T>, q.nv);
+      }
+    }
+    if constexpr (kCodes) {   // four neighbouring channels share a group of 128
+      const int ng = (C + 127) / 128;
+      const rsrc_t be = buffer(p.x_exp + ((size_t)q.b * p.T + t0) * ng, rows * ng);
+      const int oe = q.nv > 0 ? r0 * ng + q.c / 128 : kNoLane;
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        xs[i] = chan::scale_of(__builtin_amdgcn_raw_buffer_load_b8(be, oe + i * ng, 0, 0));
+    }
+  }
+  float A[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) A[k] = KIND != 0 && k < q.nv ? p.decay_a[q.c + k] : 0.f;
+  // the first tile's start state, asked for early by the wave that carries it
+  const int cc = q.c0 + q.lane;
+  float h_in = 0.f;
+  if (q.wave == 0 && q.tt == 0 && p.h0 && cc < C) h_in = p.h0[(size_t)q.b * C + cc];
+
+  float a[S][V], v[S][V], P[V], H[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    P[k] = 1.f;
+    H[k] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float x = Four<X>::get(rx[i], k);
+      if constexpr (kCodes) x *= xs[i];
+      if constexpr (KIND == 0) {
+        a[i][k] = Four<float>::get(ra[i], k);
+      } else {
+        float w;
+        const float u = A[k] * softplus(Four<T>::get(rd[i], k), w);
+        a[i][k] = exp_fast(-u);
+        if constexpr (KIND == 2) x *= sigmoid(Four<T>::get(rg[i], k));
+        if (p.normalise) x *= __builtin_amdgcn_sqrtf(one_minus_sq(u, a[i][k]));
+      }
+      v[i][k] = x;
+    }
+    if (r0 + i >= rows) {   // behind the last token: the state stays
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        a[i][k] = 1.f;
+        v[i][k] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      P[k] *= a[i][k];
+      H[k] = fmaf(a[i][k], H[k], v[i][k]);
+    }
+  }
+  float Pe[V], He[V];
+  join_groups<true>(P, H, Pe, He, q.grp);
+  if (q.grp == kGroups - 1) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) run[q.wave][q.cl + k] = float2{P[k], H[k]};
+  }
+  __syncthreads();
+  if (q.wave == 0) {
+    float2 r[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) r[w] = w < q.nw ? run[w][q.lane] : float2{1.f, 0.f};
+    uint64_t* slot = p.ch.slots + (size_t)q.chain * kTileC + q.lane;
+    if (q.tt > 0) h_in = wait_for(slot, q.tt);
+    float h[kWaves + 1];
+    h[0] = h_in;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) h[w + 1] = fmaf(r[w].x, h[w], r[w].y);
+    if (q.tt + 1 < p.nt) hand_over(slot, h[kWaves], q.tt + 1);
+    else if (p.h_out && cc < C) p.h_out[(size_t)q.b * C + cc] = h[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) from[w][q.lane] = h[w];
+    if (p.ckpt && cc < C) {
+      const size_t nb = blocks_of(p.T), j0 = (size_t)q.tt * kWaves;
+      float* ck = p.ckpt + ((size_t)q.b * nb + j0) * C + cc;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        if (w * GDR_SCAN_BLOCK < rows) ck[(size_t)w * C] = h[w];
+    }
+  }
+  if (!p.y) return;   // the states were all that was wanted (uniform)
+  __syncthreads();
+  const rsrc_t by = buffer((const T*)p.y + base, rows * C * size_of<T>);
+  const int oy = q.nv > 0 ? e0 * size_of<T> : kNoLane;
+  float h[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) h[k] = fmaf(Pe[k], from[q.wave][q.cl + k], He[k]);
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) h[k] = fmaf(a[i][k], h[k], v[i][k]);
+    Four<T>::template store<VEC>(by, oy + i * C * size_of<T>, q.nv, h);
+  }
+}
 
 template <typename T>
 __device__ inline void coefficients(const float* alpha, const void* decay_x, const void* gate_x, float A, int normalise,
@@ -27,25 +183,6 @@ __device__ inline void coefficients(const float* alpha, const void* decay_x, con
 }
 
 template <typename T>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(gdr_scan_args p) {
-  const size_t n = (size_t)blockIdx.x * 64 + threadIdx.x;
-  if (n >= (size_t)p.B * p.C) return;
-  const int b = (int)(n / p.C), c = (int)(n % p.C);
-  const float A = p.alpha ? 0.f : p.decay_a[c];
-  const size_t nb = blocks_of(p.T);
-  float h = p.h0 ? p.h0[n] : 0.f;
-  for (int t = 0; t < p.T; ++t) {
-    const size_t i = ((size_t)b * p.T + t) * p.C + c;
-    if (p.ckpt && t % GDR_SCAN_BLOCK == 0) p.ckpt[((size_t)b * nb + t / GDR_SCAN_BLOCK) * p.C + c] = h;
-    float a, v;
-    coefficients<T>(p.alpha, p.decay_x, p.gate_x, A, p.normalise, i, ld((const T*)p.x + i), a, v);
-    h = fmaf(a, h, v);
-    st((T*)p.y + i, h);
-  }
-  if (p.h_out) p.h_out[n] = h;
-}
-
-template <typename T>
 __global__ __launch_bounds__(256) void scan_step_kernel(gdr_scan_step_args p) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (size_t)p.N * p.C) return;
@@ -57,13 +194,66 @@ __global__ __launch_bounds__(256) void scan_step_kernel(gdr_scan_step_args p) {
   st((T*)p.y + i, h);
 }
 
-size_t fwd_workspace(int, int, int) { return 0; }
+// The chains' words hold no count yet, and the ticket starts at 0.
+__global__ __launch_bounds__(256) void reset_kernel(uint32_t* ticket, uint64_t* slots, uint32_t n) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i == 0) *ticket = 0u;
+  if (i < n) slots[i] = 0u;
+}
+
+size_t chain_bytes(int B, int T, int C) { return tiles_t(T) > 1 ? 256 + chains_of(B, C) * kTileC * 8 : 0; }
+
+size_t fwd_workspace(int B, int T, int C) { return chain_bytes(B, T, C); }
+
+hipError_t reset_chains(void* workspace, int B, int T, int C, Chains* out, hipStream_t s) {
+  *out = Chains{nullptr, nullptr};
+  if (tiles_t(T) <= 1) return hipSuccess;
+  out->ticket = (uint32_t*)workspace;
+  out->slots = (uint64_t*)((char*)workspace + 256);
+  const uint32_t n = (uint32_t)(chains_of(B, C) * kTileC);   // < 2^29: fewer than 2^23 chains
+  hipLaunchKernelGGL(reset_kernel, dim3((n + 255) / 256), dim3(256), 0, s, out->ticket, out->slots, n);
+  return hipGetLastError();
+}
+
+template <typename T, typename X, int KIND>
+static hipError_t launch_v(const FwdP& p, bool vec, hipStream_t s) {
+  const int nw = p.nt > 1 ? kWaves : (int)blocks_of(p.T);
+  const dim3 grid((unsigned)((size_t)p.nchain * p.nt)), block(64 * nw);
+  if (vec) hipLaunchKernelGGL((scan_fwd_kernel<T, X, KIND, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((scan_fwd_kernel<T, X, KIND, false>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T, typename X>
+static hipError_t launch_kind(const FwdP& p, bool vec, hipStream_t s) {
+  if (p.alpha) return launch_v<T, X, 0>(p, vec, s);
+  return p.gate_x ? launch_v<T, X, 2>(p, vec, s) : launch_v<T, X, 1>(p, vec, s);
+}
+
+static hipError_t launch(FwdP& p, int io_dtype, void* workspace, hipStream_t s) {
+  p.nct = (p.C + kTileC - 1) / kTileC;
+  p.nchain = (int)chains_of(p.B, p.C);
+  p.nt = (int)tiles_t(p.T);
+  const hipError_t e = reset_chains(workspace, p.B, p.T, p.C, &p.ch, s);
+  if (e != hipSuccess) return e;
+  const size_t io = io_dtype == GDR_BF16 ? 2 : 4;
+  const bool vec = p.C % 4 == 0 && vec4_ok(p.x, p.x_exp ? 1 : io) && vec4_ok(p.alpha, 4) && vec4_ok(p.decay_x, io) &&
+                   vec4_ok(p.gate_x, io) && vec4_ok(p.y, io);
+  if (io_dtype == GDR_BF16)
+    return p.x_exp ? launch_kind<__bf16, Code8>(p, vec, s) : launch_kind<__bf16, __bf16>(p, vec, s);
+  return p.x_exp ? launch_kind<float, Code8>(p, vec, s) : launch_kind<float, float>(p, vec, s);
+}
 
 hipError_t launch_scan_fwd(const gdr_scan_args& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((size_t)a.B * a.C + 63) / 64));
-  if (a.io_dtype == GDR_BF16) hipLaunchKernelGGL(scan_fwd_kernel<__bf16>, grid, dim3(64), 0, s, a);
-  else hipLaunchKernelGGL(scan_fwd_kernel<float>, grid, dim3(64), 0, s, a);
-  return hipGetLastError();
+  FwdP p{a.B, a.T, a.C, a.normalise, 0, 0, 0, a.x, nullptr, a.alpha, a.decay_x, a.decay_a, a.gate_x, a.h0, a.y, a.h_out,
+         a.ckpt, {}};
+  return launch(p, a.io_dtype, a.workspace, s);
+}
+
+hipError_t launch_ckpt(const gdr_scan_bwd_args& a, float* ckpt, void* workspace, hipStream_t s) {
+  FwdP p{a.B, a.T, a.C, a.normalise, 0, 0, 0, a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, a.h0, nullptr,
+         nullptr, ckpt, {}};
+  return launch(p, a.io_dtype, workspace, s);
 }
 
 hipError_t launch_scan_step(const gdr_scan_step_args& a, hipStream_t s) {

@@ -45,8 +45,8 @@ static char* at(int i) { return reinterpret_cast<char*>((uintptr_t)(i + 1) << 44
 int main() {
   // the largest sizes that the checks let through, and the first that they do not
   gdr_scan_args f{};
-  f.B = (1 << 22) - 1;
-  f.T = 1;
+  f.B = 1;
+  f.T = (1 << 22) - 1;
   f.C = 1 << 18;
   f.io_dtype = GDR_F32;
   f.x = at(0);
@@ -54,9 +54,13 @@ int main() {
   f.y = at(2);
   f.workspace = at(3);
   f.workspace_bytes = 4096;
-  EXPECT(gdr_scan_fwd(&f, nullptr), GDR_OK);
-  f.B = 1 << 22;
+  EXPECT(gdr_scan_fwd(&f, nullptr), GDR_ERR_UNSUPPORTED);   // tiles
+  f.T = 1 << 22;
   EXPECT(gdr_scan_fwd(&f, nullptr), GDR_ERR_SHAPE);
+  f.T = 256 * 2047;
+  EXPECT(gdr_scan_fwd(&f, nullptr), GDR_OK);
+  f.T += 1;
+  EXPECT(gdr_scan_fwd(&f, nullptr), GDR_ERR_UNSUPPORTED);
   f.B = f.T = f.C = 2147483647;
   EXPECT(gdr_scan_fwd(&f, nullptr), GDR_ERR_UNSUPPORTED);
   f.C = 1;
