@@ -1,76 +1,115 @@
 // ckpt8.hip -- 8-bit activation checkpoints: pack and unpack, gfx950.
 //
-// One wave per group of up to 128 values, two values per lane.
+// A group of 128 values is 16 lanes of 8 bf16 values or 32 lanes of 4 fp32 ones,
+// 16 bytes a lane; lanes are numbered over all groups of all rows, so short rows
+// waste no wave.  Both directions are bound by HBM.
 #include "chan_device.h"
 #include "norm_kernels.h"
 
 namespace gdr {
 namespace ckpt8 {
 
-using chan::ld;
-using chan::st;
+using chan::Codes;
+using chan::raw4;
+using chan::Run;
+
+constexpr int kMany = 4;   // groups a lane has under way at once
+
+// A lane's run of one group.
+struct Spot {
+  size_t row;
+  int c0, n;   // first column, values that exist (none: <= 0)
+};
+template <int N>
+__device__ inline Spot spot_of(size_t g, size_t groups, int per_row, int D) {
+  constexpr int kLanes = GDR_CKPT8_GROUP / N;
+  if (g >= groups) return Spot{0, 0, 0};
+  const size_t row = per_row == 1 ? g : g / per_row;
+  const int c0 = (int)(g - row * per_row) * GDR_CKPT8_GROUP + (int)(threadIdx.x % kLanes) * N;
+  return Spot{row, c0, D - c0};
+}
 
 template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(gdr_ckpt8_pack_args p) {
-  const int G = (p.D + 127) / 128, l = threadIdx.x & 63;
-  const size_t n = (size_t)p.R * G;
-  for (size_t g = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6); g < n; g += (size_t)gridDim.x * 4) {
-    const size_t row = g / G;
-    const int c0 = (int)(g % G) * 128;
-    float v[2];
-    uint32_t m = 0;
+__global__ __launch_bounds__(256) void pack_kernel(gdr_ckpt8_pack_args p, size_t groups, int per_row) {
+  constexpr int N = Run<T>::N, kLanes = GDR_CKPT8_GROUP / N, kPer = 256 / kLanes;
+  const size_t step = (size_t)gridDim.x * kPer;
+  for (size_t g0 = (size_t)blockIdx.x * kPer + threadIdx.x / kLanes; g0 < groups; g0 += kMany * step) {
+    Spot q[kMany];
+    raw4 r[kMany];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = c0 + l + 64 * k;
-      v[k] = c < p.D ? ld((const T*)p.x + row * p.D + c) : 0.f;
-      const uint32_t b = chan::finite_mag_bits(v[k]);
-      m = b > m ? b : m;
+    for (int i = 0; i < kMany; ++i) {
+      q[i] = spot_of<N>(g0 + i * step, groups, per_row, p.D);
+      r[i] = Run<T>::load((const T*)p.x + q[i].row * p.D + q[i].c0, q[i].n);
     }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const uint32_t o = __shfl_xor(m, off);
-      m = o > m ? o : m;
-    }
-    const int e = chan::ckpt8_exponent(m);
-    const float inv = chan::inv_scale_of(e);
+    for (int i = 0; i < kMany; ++i) {
+      float v[N];
+      uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = c0 + l + 64 * k;
-      if (c < p.D) p.code[row * p.D + c] = chan::pack1_e4m3(v[k] * inv);
+      for (int k = 0; k < N; ++k) {
+        v[k] = Run<T>::get(r[i], k);
+        const uint32_t b = chan::finite_mag_bits(v[k]);
+        m = b > m ? b : m;
+      }
+      m = chan::lane_max<kLanes>(m);
+      const int e = chan::ckpt8_exponent(m);
+      Codes<N>::store(p.code + q[i].row * p.D + q[i].c0, q[i].n, Codes<N>::pack(v, chan::inv_scale_of(e)));
+      if (threadIdx.x % kLanes == 0 && q[i].n > 0) p.exp[g0 + i * step] = (uint8_t)e;
     }
-    if (l == 0) p.exp[g] = (uint8_t)e;
   }
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void unpack_kernel(gdr_ckpt8_unpack_args p) {
-  const int G = (p.D + 127) / 128, l = threadIdx.x & 63;
-  const size_t n = (size_t)p.R * G;
-  for (size_t g = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6); g < n; g += (size_t)gridDim.x * 4) {
-    const size_t row = g / G;
-    const float sc = chan::scale_of(p.exp[g]);
+__global__ __launch_bounds__(256) void unpack_kernel(gdr_ckpt8_unpack_args p, size_t groups, int per_row) {
+  constexpr int N = Run<T>::N, kLanes = GDR_CKPT8_GROUP / N, kPer = 256 / kLanes;
+  const size_t step = (size_t)gridDim.x * kPer;
+  for (size_t g0 = (size_t)blockIdx.x * kPer + threadIdx.x / kLanes; g0 < groups; g0 += kMany * step) {
+    Spot q[kMany];
+    typename Codes<N>::R r[kMany];
+    uint8_t e[kMany];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = (int)(g % G) * 128 + l + 64 * k;
-      if (c < p.D) st((T*)p.x + row * p.D + c, chan::code1_f32(p.code[row * p.D + c]) * sc);
+    for (int i = 0; i < kMany; ++i) {
+      q[i] = spot_of<N>(g0 + i * step, groups, per_row, p.D);
+      r[i] = Codes<N>::load(p.code + q[i].row * p.D + q[i].c0, q[i].n);
+      e[i] = q[i].n > 0 ? p.exp[g0 + i * step] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kMany; ++i) {
+      float v[N];
+      Codes<N>::unpack(r[i], v);
+      const float sc = chan::scale_of(e[i]);
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] *= sc;
+      Run<T>::store((T*)p.x + q[i].row * p.D + q[i].c0, q[i].n, v);
     }
   }
 }
 
-static unsigned grid_of(int64_t R, int D) {
-  const size_t n = ((size_t)R * ((D + 127) / 128) + 3) / 4;
-  return (unsigned)(n < 65536 ? n : 65536);
+struct Grid {
+  size_t groups;
+  int per_row;
+  dim3 blocks;
+};
+static Grid grid_of(int64_t R, int D, int n) {
+  Grid g;
+  g.per_row = (D + GDR_CKPT8_GROUP - 1) / GDR_CKPT8_GROUP;
+  g.groups = (size_t)R * g.per_row;
+  const size_t per = 256 / (GDR_CKPT8_GROUP / n), want = (g.groups + per * kMany - 1) / (per * kMany);
+  g.blocks = dim3((unsigned)(want < 8192 ? want : 8192));
+  return g;
 }
 
 hipError_t launch_pack(const gdr_ckpt8_pack_args& a, hipStream_t s) {
-  if (a.io_dtype == GDR_BF16) hipLaunchKernelGGL(pack_kernel<__bf16>, dim3(grid_of(a.R, a.D)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(pack_kernel<float>, dim3(grid_of(a.R, a.D)), dim3(256), 0, s, a);
+  const Grid g = grid_of(a.R, a.D, a.io_dtype == GDR_BF16 ? 8 : 4);
+  if (a.io_dtype == GDR_BF16) hipLaunchKernelGGL(pack_kernel<__bf16>, g.blocks, dim3(256), 0, s, a, g.groups, g.per_row);
+  else hipLaunchKernelGGL(pack_kernel<float>, g.blocks, dim3(256), 0, s, a, g.groups, g.per_row);
   return hipGetLastError();
 }
 
 hipError_t launch_unpack(const gdr_ckpt8_unpack_args& a, hipStream_t s) {
-  if (a.io_dtype == GDR_BF16) hipLaunchKernelGGL(unpack_kernel<__bf16>, dim3(grid_of(a.R, a.D)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(unpack_kernel<float>, dim3(grid_of(a.R, a.D)), dim3(256), 0, s, a);
+  const Grid g = grid_of(a.R, a.D, a.io_dtype == GDR_BF16 ? 8 : 4);
+  if (a.io_dtype == GDR_BF16) hipLaunchKernelGGL(unpack_kernel<__bf16>, g.blocks, dim3(256), 0, s, a, g.groups, g.per_row);
+  else hipLaunchKernelGGL(unpack_kernel<float>, g.blocks, dim3(256), 0, s, a, g.groups, g.per_row);
   return hipGetLastError();
 }
 
