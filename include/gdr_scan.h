@@ -21,7 +21,7 @@
  * x = 0 leaves the state as it is (padding).  NaN and Inf propagate.
  *
  * Sizes: any B, C and T >= 1 with B * T * C < 2^40, C <= 2^18 and
- * B * ceil(C/64) * ceil(T/256) < 2^23.  Every pointer is
+ * B * ceil(C/64) * ceil(T/128) < 2^23.  Every pointer is
  * aligned to its element; rows whose C is a multiple of 4, in buffers aligned
  * to 4 elements, move 4 channels at a time.  Outputs overlap neither inputs nor
  * each other (GDR_ERR_ARG), except that h_out may equal h0 (and the step's

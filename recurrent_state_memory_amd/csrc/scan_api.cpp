@@ -32,7 +32,7 @@ gdr_status check_fwd(const gdr_scan_args* a) {
   if (!a) return GDR_ERR_NULL;
   gdr_status st = check_sizes(a->B, a->T, a->C, a->io_dtype);
   if (st != GDR_OK) return st;
-  if (gdr::scan::tiles_of(a->B, a->T, a->C) >= gdr::scan::kMaxTiles) return GDR_ERR_UNSUPPORTED;
+  if (gdr::scan::too_many_tiles(a->B, a->T, a->C)) return GDR_ERR_UNSUPPORTED;
   if (!a->x || !a->y) return GDR_ERR_NULL;
   if (a->reserved != 0) return GDR_ERR_ARG;
   st = check_decay(a->alpha, a->decay_x, a->decay_a, a->gate_x, a->normalise);
@@ -52,7 +52,7 @@ gdr_status check_bwd(const gdr_scan_bwd_args* a) {
   if (!a) return GDR_ERR_NULL;
   gdr_status st = check_sizes(a->B, a->T, a->C, a->io_dtype);
   if (st != GDR_OK) return st;
-  if (gdr::scan::tiles_of(a->B, a->T, a->C) >= gdr::scan::kMaxTiles) return GDR_ERR_UNSUPPORTED;
+  if (gdr::scan::too_many_tiles(a->B, a->T, a->C)) return GDR_ERR_UNSUPPORTED;
   if (!a->x || !a->grad_y || !a->grad_x) return GDR_ERR_NULL;
   if (a->reserved != 0) return GDR_ERR_ARG;
   st = check_decay(a->alpha, a->decay_x, a->decay_a, a->gate_x, a->normalise);

@@ -6,9 +6,9 @@
 // tile to tile with the last tiles first.  G_t = grad_y_t + K_{t+1}, so a run of
 // tokens takes K to P K + Q with P the same product of decays.
 //
-// A thread keeps a and v = b x of its 32 elements; what the gradients need besides
-// (the softplus, the sigmoids, 1 - a^2) is evaluated again from the inputs' raw
-// registers, which costs less than the registers to keep it would.
+// A thread keeps a, b and the softplus of its 32 elements; what the gradients need
+// besides (the two sigmoids; 1 / (1 - a^2) = (s / b)^2) is evaluated again from the
+// inputs' raw registers, which costs less than the registers to keep it would.
 //
 // grad_decay_a sums over all tokens: registers, lane groups, waves (one LDS pass
 // in a fixed order), then one partial row per tile that sum_kernel adds up, again
@@ -19,8 +19,8 @@
 namespace gdr {
 namespace scan {
 
-// Below this, 1 - a^2 counts as 0: the term it divides vanishes with its root.
-constexpr float kLeastM = 0x1p-120f;
+// Below this, sqrt(1 - a^2) counts as 0: the term it divides vanishes with it.
+constexpr float kLeastB = 0x1p-60f;
 
 struct BwdP {
   int B, T, C, normalise;
@@ -43,14 +43,13 @@ struct BwdP {
   Chains ch;
 };
 
-template <typename T, typename X, int KIND, bool VEC>
-__global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(BwdP p) {
+template <typename T, typename X, int KIND, bool NORM, bool VEC>
+__global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
   constexpr bool kCodes = !__is_same(X, T);
-  __shared__ float2 run[kWaves][kTileC];    // (P, Q) of each wave
-  __shared__ float from[kWaves][kTileC];    // K behind each wave; then the waves' sums
+  __shared__ Joins<kBwdWaves> j;   // of the maps of K: later tokens first
   const Place q = take_place(p.C, p.nchain, p.nct, p.ch.ticket);
   const int tile = p.nt - 1 - q.tt;         // the last tokens come first
-  const int C = p.C, t0 = tile * kTileT;
+  const int C = p.C, t0 = tile * kBwdWaves * GDR_SCAN_BLOCK;
   const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);
   const int r0 = q.wave * GDR_SCAN_BLOCK + q.grp * S;
   const size_t base = ((size_t)q.b * p.T + t0) * C;
@@ -95,19 +94,29 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(BwdP p) {
         xs[i] = chan::scale_of(__builtin_amdgcn_raw_buffer_load_b8(be, oe + i * ng, 0, 0));
     }
   }
-  float A[V], h0[V];
-  const size_t nb = blocks_of(p.T), block = (size_t)tile * kWaves + q.wave;
+  float scale[V], h0[V];
+  const size_t nb = blocks_of(p.T), block = (size_t)tile * kBwdWaves + q.wave;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    A[k] = KIND != 0 && k < q.nv ? p.decay_a[q.c + k] : 0.f;
+    scale[k] = KIND != 0 && k < q.nv ? p.decay_a[q.c + k] : 0.f;
     h0[k] = k < q.nv && block < nb ? p.ckpt[((size_t)q.b * nb + block) * C + q.c + k] : 0.f;
   }
   const int cc = q.c0 + q.lane;
+  const int pos = q.nw - 1 - q.wave;        // the wave's place in the order of joining
   float k_in = 0.f;
-  if (q.wave == 0 && q.tt == 0 && p.grad_h && cc < C) k_in = p.grad_h[(size_t)q.b * C + cc];
+  if (q.wave == 0 && q.tt < kSuper && p.grad_h && cc < C) k_in = p.grad_h[(size_t)q.b * C + cc];
 
-  // a and v; (P, H) forwards and (P, Q) backwards over the thread's run
-  float a[S][V], v[S][V], P[V], H[V], Q[V];
+  // a and b; (P, H) forwards and (P, Q) backwards over the thread's run
+  float a[S][V], b[KIND == 2 || NORM ? S : 1][V], sp[KIND == 0 ? 1 : S][V], P[V], H[V], Q[V];
+  const auto x_at = [&](int i, int k) {
+    const float x = Four<X>::get(rx[i], k);
+    if constexpr (kCodes) return x * xs[i];
+    return x;
+  };
+  const auto v_at = [&](int i, int k) {
+    if constexpr (KIND == 2 || NORM) return b[i][k] * x_at(i, k);
+    return x_at(i, k);
+  };
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     P[k] = 1.f;
@@ -117,30 +126,32 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(BwdP p) {
   for (int i = 0; i < S; ++i) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      float x = Four<X>::get(rx[i], k);
-      if constexpr (kCodes) x *= xs[i];
       if constexpr (KIND == 0) {
         a[i][k] = Four<float>::get(ra[i], k);
       } else {
-        float w;
-        const float u = A[k] * softplus(Four<T>::get(rd[i], k), w);
-        a[i][k] = exp_fast(-u);
-        if constexpr (KIND == 2) x *= sigmoid(Four<T>::get(rg[i], k));
-        if (p.normalise) x *= __builtin_amdgcn_sqrtf(one_minus_sq(u, a[i][k]));
+        const Scale A(scale[k]);
+        sp[i][k] = softplus(Four<T>::get(rd[i], k));
+        a[i][k] = decay(A, sp[i][k]);
+        if constexpr (KIND == 2) b[i][k] = sigmoid(Four<T>::get(rg[i], k));
+        if constexpr (NORM) {
+          const float n = __builtin_amdgcn_sqrtf(one_minus_sq(A, sp[i][k], a[i][k]));
+          b[i][k] = KIND == 2 ? b[i][k] * n : n;
+        }
       }
-      v[i][k] = x;
     }
+    // behind the last token the state stays: x and grad_y read as 0 there, and a
+    // softplus of 0 keeps the row out of grad_decay_a
     if (r0 + i >= rows) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         a[i][k] = 1.f;
-        v[i][k] = 0.f;
+        if constexpr (KIND != 0) sp[i][k] = 0.f;
       }
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       P[k] *= a[i][k];
-      H[k] = fmaf(a[i][k], H[k], v[i][k]);
+      H[k] = fmaf(a[i][k], H[k], v_at(i, k));
     }
   }
 #pragma unroll
@@ -159,44 +170,46 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(BwdP p) {
   join_groups<false>(P, Q, Pb, Qb, q.grp);
   if (q.grp == 0) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) run[q.wave][q.cl + k] = float2{P[k], Q[k]};
+    for (int k = 0; k < V; ++k) j.run[pos][q.cl + k] = float2{P[k], Q[k]};
   }
-  __syncthreads();
-  if (q.wave == 0) {
-    float2 r[kWaves];
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) r[w] = w < q.nw ? run[w][q.lane] : float2{1.f, 0.f};
-    uint64_t* slot = p.ch.slots + (size_t)q.chain * kTileC + q.lane;
-    if (q.tt > 0) k_in = wait_for(slot, q.tt);
-    float kk[kWaves + 1];
-    kk[kWaves] = k_in;
-#pragma unroll
-    for (int w = kWaves - 1; w >= 0; --w) kk[w] = fmaf(r[w].x, kk[w + 1], r[w].y);
-    if (q.tt + 1 < p.nt) hand_over(slot, kk[0], q.tt + 1);
-    else if (p.grad_h0 && cc < C) p.grad_h0[(size_t)q.b * C + cc] = kk[0];
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) from[w][q.lane] = kk[w + 1];
-  }
-  __syncthreads();
+  float k_end;
+  join_tiles(j, p.ch, q, p.nt, pos, k_in, k_end);
+  if (p.grad_h0 && q.tt + 1 == p.nt && q.wave == 0 && cc < C) p.grad_h0[(size_t)q.b * C + cc] = k_end;
   float K[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) K[k] = fmaf(Pb[k], from[q.wave][q.cl + k], Qb[k]);
-  float prev[S][V];
-#pragma unroll
-  for (int i = 0; i < S; ++i)
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      prev[i][k] = h[k];
-      h[k] = fmaf(a[i][k], h[k], v[i][k]);
-    }
+  for (int k = 0; k < V; ++k) K[k] = fmaf(Pb[k], j.from[pos][q.cl + k], Qb[k]);
   const rsrc_t gx = buffer((const T*)p.grad_x + base, tbytes);
   const rsrc_t gd = KIND == 0 ? buffer(p.grad_alpha + base, rows * C * 4) : buffer((const T*)p.grad_decay_x + base, tbytes);
   const rsrc_t gg = KIND == 2 ? buffer((const T*)p.grad_gate_x + base, tbytes) : gx;
   float sum[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) sum[k] = 0.f;
+  // the states before each token are held for half of the run at a time
+  constexpr int HS = S / 2;
 #pragma unroll
-  for (int i = S - 1; i >= 0; --i) {
+  for (int half = 1; half >= 0; --half) {
+  float prev[HS][V];
+#pragma unroll
+  for (int i = 0; i < (half + 1) * HS; ++i) {
+    forget(rx[i]);
+    forget(ry[i]);
+  }
+  {
+    float t[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) t[k] = h[k];
+#pragma unroll
+    for (int i = 0; i < (half + 1) * HS - 1; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (i >= half * HS) prev[i - half * HS][k] = t[k];
+        t[k] = fmaf(a[i][k], t[k], v_at(i, k));
+      }
+#pragma unroll
+    for (int k = 0; k < V; ++k) prev[HS - 1][k] = t[k];
+  }
+#pragma unroll
+  for (int i = (half + 1) * HS - 1; i >= half * HS; --i) {
     float ox_[V], od[V], og[V];
     if constexpr (KIND != 0) forget(rd[i]);
     if constexpr (KIND == 2) forget(rg[i]);
@@ -207,26 +220,23 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(BwdP p) {
       K[k] = ak * G;
       if constexpr (KIND == 0) {
         ox_[k] = G;
-        od[k] = G * prev[i][k];
+        od[k] = G * prev[i - half * HS][k];
       } else {
-        const float d = Four<T>::get(rd[i], k);
-        float w;
-        const float sp = softplus(d, w), rw = __builtin_amdgcn_rcpf(1.f + w);
-        float b = 1.f, in = -prev[i][k];
+        float in = -prev[i - half * HS][k], sg = 1.f;
+        ox_[k] = G;
+        if constexpr (KIND == 2 || NORM) ox_[k] *= b[i][k];
         if constexpr (KIND == 2) {
-          const float s = sigmoid(Four<T>::get(rg[i], k));
-          b = s;
-          og[k] = G * v[i][k] * (1.f - s);
+          sg = sigmoid(Four<T>::get(rg[i], k));
+          og[k] = G * v_at(i, k) * (1.f - sg);
         }
-        if (p.normalise) {
-          const float m = one_minus_sq(A[k] * sp, ak);
-          b *= __builtin_amdgcn_sqrtf(m);
-          in += m > kLeastM ? v[i][k] * ak * __builtin_amdgcn_rcpf(m) : 0.f;
+        if constexpr (NORM) {   // v a / m = x a s^2 / b
+          const float t = x_at(i, k) * ak * __builtin_amdgcn_rcpf(b[i][k]);
+          in += b[i][k] > kLeastB * sg ? (KIND == 2 ? t * sg * sg : t) : 0.f;
         }
-        ox_[k] = b * G;
-        const float du = r0 + i < rows ? K[k] * in : 0.f;
-        sum[k] = fmaf(du, sp, sum[k]);
-        od[k] = du * A[k] * (d > 0.f ? rw : w * rw);
+        const float du = K[k] * in;
+        sum[k] = fmaf(du, sp[i][k], sum[k]);
+        const float d = Four<T>::get(rd[i], k), w = exp_neg_abs(d), r = __builtin_amdgcn_rcpf(1.f + w);
+        od[k] = du * scale[k] * (d > 0.f ? r : w * r);
       }
     }
     Four<T>::template store<VEC>(gx, ot + i * C * size_of<T>, q.nv, ox_);
@@ -234,20 +244,21 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_kernel(BwdP p) {
     else Four<T>::template store<VEC>(gd, ot + i * C * size_of<T>, q.nv, od);
     if constexpr (KIND == 2) Four<T>::template store<VEC>(gg, ot + i * C * size_of<T>, q.nv, og);
   }
+  }
   if constexpr (KIND != 0) {
 #pragma unroll
     for (int dist = kSide; dist < 64; dist *= 2)
 #pragma unroll
       for (int k = 0; k < V; ++k) sum[k] += __shfl_xor(sum[k], dist);
-    __syncthreads();   // `from` has been read
+    // a row of `from` has been read by its own wave alone
     if (q.grp == 0) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) from[q.wave][q.cl + k] = sum[k];
+      for (int k = 0; k < V; ++k) j.from[pos][q.cl + k] = sum[k];
     }
     __syncthreads();
     if (q.wave == 0 && cc < C) {
       float s = 0.f;
-      for (int w = 0; w < q.nw; ++w) s += from[w][q.lane];
+      for (int w = 0; w < q.nw; ++w) s += j.from[w][q.lane];
       p.part[((size_t)tile * p.B + q.b) * C + cc] = s;
     }
   }
@@ -270,29 +281,36 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float* part, float* out
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-size_t bwd_workspace(int B, int T, int C, bool gated, bool ckpt) {
-  return align256(chain_bytes(B, T, C)) + (ckpt ? 0 : align256((size_t)B * blocks_of(T) * C * 4)) +
-         (gated ? align256(tiles_t(T) * B * C * 4) : 0);
+// Room of the hand-over words, first the recomputed forward's, then the backward's.
+static size_t chains_room(int B, int T, int C) {
+  const size_t f = chain_bytes(B, T, C, kFwdWaves), b = chain_bytes(B, T, C, kBwdWaves);
+  return align256(f > b ? f : b);
 }
 
-template <typename T, typename X, int KIND>
+size_t bwd_workspace(int B, int T, int C, bool gated, bool ckpt) {
+  return chains_room(B, T, C) + (ckpt ? 0 : align256((size_t)B * blocks_of(T) * C * 4)) +
+         (gated ? align256(tiles_t(T, kBwdWaves) * B * C * 4) : 0);
+}
+
+template <typename T, typename X, int KIND, bool NORM>
 static hipError_t launch_v(const BwdP& p, bool vec, hipStream_t s) {
-  const int nw = p.nt > 1 ? kWaves : (int)blocks_of(p.T);
+  const int nw = p.nt > 1 ? kBwdWaves : (int)blocks_of(p.T);
   const dim3 grid((unsigned)((size_t)p.nchain * p.nt)), block(64 * nw);
-  if (vec) hipLaunchKernelGGL((scan_bwd_kernel<T, X, KIND, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((scan_bwd_kernel<T, X, KIND, false>), grid, block, 0, s, p);
+  if (vec) hipLaunchKernelGGL((scan_bwd_kernel<T, X, KIND, NORM, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((scan_bwd_kernel<T, X, KIND, NORM, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T, typename X>
 static hipError_t launch_kind(const BwdP& p, bool vec, hipStream_t s) {
-  if (p.alpha) return launch_v<T, X, 0>(p, vec, s);
-  return p.gate_x ? launch_v<T, X, 2>(p, vec, s) : launch_v<T, X, 1>(p, vec, s);
+  if (p.alpha) return launch_v<T, X, 0, false>(p, vec, s);
+  if (p.gate_x) return p.normalise ? launch_v<T, X, 2, true>(p, vec, s) : launch_v<T, X, 2, false>(p, vec, s);
+  return p.normalise ? launch_v<T, X, 1, true>(p, vec, s) : launch_v<T, X, 1, false>(p, vec, s);
 }
 
 hipError_t launch_scan_bwd(const gdr_scan_bwd_args& a, hipStream_t s) {
   char* ws = (char*)a.workspace;
-  char* rest = ws + align256(chain_bytes(a.B, a.T, a.C));
+  char* rest = ws + chains_room(a.B, a.T, a.C);
   const float* ckpt = a.ckpt;
   if (!ckpt) {
     const hipError_t e = launch_ckpt(a, (float*)rest, ws, s);
@@ -300,10 +318,10 @@ hipError_t launch_scan_bwd(const gdr_scan_bwd_args& a, hipStream_t s) {
     ckpt = (const float*)rest;
     rest += align256((size_t)a.B * blocks_of(a.T) * a.C * 4);
   }
-  BwdP p{a.B, a.T, a.C, a.normalise, (int)chains_of(a.B, a.C), (a.C + kTileC - 1) / kTileC, (int)tiles_t(a.T),
+  BwdP p{a.B, a.T, a.C, a.normalise, (int)chains_of(a.B, a.C), (a.C + kTileC - 1) / kTileC, (int)tiles_t(a.T, kBwdWaves),
          a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, ckpt, a.grad_y, a.grad_h, a.grad_x, a.grad_alpha,
          a.grad_decay_x, a.grad_gate_x, a.grad_h0, a.alpha ? nullptr : (float*)rest, {}};
-  hipError_t e = reset_chains(ws, a.B, a.T, a.C, &p.ch, s);
+  hipError_t e = reset_chains(ws, a.B, a.T, a.C, kBwdWaves, &p.ch, s);
   if (e != hipSuccess) return e;
   const size_t io = a.io_dtype == GDR_BF16 ? 2 : 4;
   const bool vec = a.C % 4 == 0 && vec4_ok(a.x, a.x_exp ? 1 : io) && vec4_ok(a.alpha, 4) && vec4_ok(a.decay_x, io) &&

@@ -29,14 +29,13 @@ struct FwdP {
 };
 
 // KIND: 0 alpha given, 1 decay from its pre-activation, 2 with an input gate too.
-// X: the type x is read in (T, or Code8).
-template <typename T, typename X, int KIND, bool VEC>
-__global__ __launch_bounds__(64 * kWaves) void scan_fwd_kernel(FwdP p) {
+// NORM: b has sqrt(1 - a^2).  X: the type x is read in (T, or Code8).
+template <typename T, typename X, int KIND, bool NORM, bool VEC>
+__global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   constexpr bool kCodes = !__is_same(X, T);
-  __shared__ float2 run[kWaves][kTileC];    // (P, H) of each wave
-  __shared__ float from[kWaves][kTileC];    // the state before each wave
+  __shared__ Joins<kFwdWaves> j;
   const Place q = take_place(p.C, p.nchain, p.nct, p.ch.ticket);
-  const int C = p.C, t0 = q.tt * kTileT;
+  const int C = p.C, t0 = q.tt * kFwdWaves * GDR_SCAN_BLOCK;
   const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);   // of the tile that exist
   const int r0 = q.wave * GDR_SCAN_BLOCK + q.grp * S;      // the thread's first row
   const size_t base = ((size_t)q.b * p.T + t0) * C;
@@ -79,13 +78,15 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd_kernel(FwdP p) {
         xs[i] = chan::scale_of(__builtin_amdgcn_raw_buffer_load_b8(be, oe + i * ng, 0, 0));
     }
   }
-  float A[V];
+  Scale A[V];
+  if constexpr (KIND != 0) {
 #pragma unroll
-  for (int k = 0; k < V; ++k) A[k] = KIND != 0 && k < q.nv ? p.decay_a[q.c + k] : 0.f;
-  // the first tile's start state, asked for early by the wave that carries it
+    for (int k = 0; k < V; ++k) A[k] = Scale(k < q.nv ? p.decay_a[q.c + k] : 0.f);
+  }
+  // the start state, asked for early by the wave that joins the first super's tiles to it
   const int cc = q.c0 + q.lane;
   float h_in = 0.f;
-  if (q.wave == 0 && q.tt == 0 && p.h0 && cc < C) h_in = p.h0[(size_t)q.b * C + cc];
+  if (q.wave == q.nw - 1 && q.tt < kSuper && p.h0 && cc < C) h_in = p.h0[(size_t)q.b * C + cc];
 
   float a[S][V], v[S][V], P[V], H[V];
 #pragma unroll
@@ -102,11 +103,10 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd_kernel(FwdP p) {
       if constexpr (KIND == 0) {
         a[i][k] = Four<float>::get(ra[i], k);
       } else {
-        float w;
-        const float u = A[k] * softplus(Four<T>::get(rd[i], k), w);
-        a[i][k] = exp_fast(-u);
+        const float sp = softplus(Four<T>::get(rd[i], k));
+        a[i][k] = decay(A[k], sp);
         if constexpr (KIND == 2) x *= sigmoid(Four<T>::get(rg[i], k));
-        if (p.normalise) x *= __builtin_amdgcn_sqrtf(one_minus_sq(u, a[i][k]));
+        if constexpr (NORM) x *= __builtin_amdgcn_sqrtf(one_minus_sq(A[k], sp, a[i][k]));
       }
       v[i][k] = x;
     }
@@ -127,38 +127,19 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd_kernel(FwdP p) {
   join_groups<true>(P, H, Pe, He, q.grp);
   if (q.grp == kGroups - 1) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) run[q.wave][q.cl + k] = float2{P[k], H[k]};
+    for (int k = 0; k < V; ++k) j.run[q.wave][q.cl + k] = float2{P[k], H[k]};
   }
-  __syncthreads();
-  if (q.wave == 0) {
-    float2 r[kWaves];
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) r[w] = w < q.nw ? run[w][q.lane] : float2{1.f, 0.f};
-    uint64_t* slot = p.ch.slots + (size_t)q.chain * kTileC + q.lane;
-    if (q.tt > 0) h_in = wait_for(slot, q.tt);
-    float h[kWaves + 1];
-    h[0] = h_in;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) h[w + 1] = fmaf(r[w].x, h[w], r[w].y);
-    if (q.tt + 1 < p.nt) hand_over(slot, h[kWaves], q.tt + 1);
-    else if (p.h_out && cc < C) p.h_out[(size_t)q.b * C + cc] = h[kWaves];
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) from[w][q.lane] = h[w];
-    if (p.ckpt && cc < C) {
-      const size_t nb = blocks_of(p.T), j0 = (size_t)q.tt * kWaves;
-      float* ck = p.ckpt + ((size_t)q.b * nb + j0) * C + cc;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-        if (w * GDR_SCAN_BLOCK < rows) ck[(size_t)w * C] = h[w];
-    }
-  }
-  if (!p.y) return;   // the states were all that was wanted (uniform)
-  __syncthreads();
+  float h_end;
+  const float h_wave = join_tiles(j, p.ch, q, p.nt, q.wave, h_in, h_end);
+  if (p.h_out && q.tt + 1 == p.nt && q.wave == q.nw - 1 && cc < C) p.h_out[(size_t)q.b * C + cc] = h_end;
+  if (p.ckpt && cc < C && q.wave * GDR_SCAN_BLOCK < rows)
+    p.ckpt[((size_t)q.b * blocks_of(p.T) + (size_t)q.tt * kFwdWaves + q.wave) * C + cc] = h_wave;
+  if (!p.y) return;   // the states were all that was wanted
   const rsrc_t by = buffer((const T*)p.y + base, rows * C * size_of<T>);
   const int oy = q.nv > 0 ? e0 * size_of<T> : kNoLane;
   float h[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) h[k] = fmaf(Pe[k], from[q.wave][q.cl + k], He[k]);
+  for (int k = 0; k < V; ++k) h[k] = fmaf(Pe[k], j.from[q.wave][q.cl + k], He[k]);
 #pragma unroll
   for (int i = 0; i < S; ++i) {
 #pragma unroll
@@ -175,11 +156,11 @@ __device__ inline void coefficients(const float* alpha, const void* decay_x, con
     a = alpha[i];
     return;
   }
-  float w;
-  const float u = A * softplus(ld((const T*)decay_x + i), w);
-  a = exp_fast(-u);
+  const Scale sc(A);
+  const float sp = softplus(ld((const T*)decay_x + i));
+  a = decay(sc, sp);
   if (gate_x) v *= sigmoid(ld((const T*)gate_x + i));
-  if (normalise) v *= __builtin_amdgcn_sqrtf(one_minus_sq(u, a));
+  if (normalise) v *= __builtin_amdgcn_sqrtf(one_minus_sq(sc, sp, a));
 }
 
 template <typename T>
@@ -194,47 +175,57 @@ __global__ __launch_bounds__(256) void scan_step_kernel(gdr_scan_step_args p) {
   st((T*)p.y + i, h);
 }
 
-// The chains' words hold no count yet, and the ticket starts at 0.
-__global__ __launch_bounds__(256) void reset_kernel(uint32_t* ticket, uint64_t* slots, uint32_t n) {
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+// No word is written yet, and the ticket starts at 0.
+__global__ __launch_bounds__(256) void reset_kernel(uint32_t* ticket, ulonglong2* words, size_t pairs) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i == 0) *ticket = 0u;
-  if (i < n) slots[i] = 0u;
+  for (size_t k = i; k < pairs; k += (size_t)gridDim.x * 256) words[k] = ulonglong2{0u, 0u};
 }
 
-size_t chain_bytes(int B, int T, int C) { return tiles_t(T) > 1 ? 256 + chains_of(B, C) * kTileC * 8 : 0; }
+static size_t words_of(int B, int T, int C, int waves) {
+  const size_t nt = tiles_t(T, waves);
+  return chains_of(B, C) * (nt + (nt + kSuper - 1) / kSuper) * kTileC;
+}
 
-size_t fwd_workspace(int B, int T, int C) { return chain_bytes(B, T, C); }
+size_t chain_bytes(int B, int T, int C, int waves) {
+  return tiles_t(T, waves) > 1 ? 256 + words_of(B, T, C, waves) * 8 : 0;
+}
 
-hipError_t reset_chains(void* workspace, int B, int T, int C, Chains* out, hipStream_t s) {
-  *out = Chains{nullptr, nullptr};
-  if (tiles_t(T) <= 1) return hipSuccess;
+size_t fwd_workspace(int B, int T, int C) { return chain_bytes(B, T, C, kFwdWaves); }
+
+hipError_t reset_chains(void* workspace, int B, int T, int C, int waves, Chains* out, hipStream_t s) {
+  *out = Chains{nullptr, nullptr, nullptr};
+  if (tiles_t(T, waves) <= 1) return hipSuccess;
   out->ticket = (uint32_t*)workspace;
-  out->slots = (uint64_t*)((char*)workspace + 256);
-  const uint32_t n = (uint32_t)(chains_of(B, C) * kTileC);   // < 2^29: fewer than 2^23 chains
-  hipLaunchKernelGGL(reset_kernel, dim3((n + 255) / 256), dim3(256), 0, s, out->ticket, out->slots, n);
+  out->tiles = (uint64_t*)((char*)workspace + 256);
+  out->supers = out->tiles + chains_of(B, C) * tiles_t(T, waves) * kTileC;
+  const size_t pairs = words_of(B, T, C, waves) / 2, blocks = (pairs + 255) / 256;
+  hipLaunchKernelGGL(reset_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s, out->ticket,
+                     (ulonglong2*)out->tiles, pairs);
   return hipGetLastError();
 }
 
-template <typename T, typename X, int KIND>
+template <typename T, typename X, int KIND, bool NORM>
 static hipError_t launch_v(const FwdP& p, bool vec, hipStream_t s) {
-  const int nw = p.nt > 1 ? kWaves : (int)blocks_of(p.T);
+  const int nw = p.nt > 1 ? kFwdWaves : (int)blocks_of(p.T);
   const dim3 grid((unsigned)((size_t)p.nchain * p.nt)), block(64 * nw);
-  if (vec) hipLaunchKernelGGL((scan_fwd_kernel<T, X, KIND, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((scan_fwd_kernel<T, X, KIND, false>), grid, block, 0, s, p);
+  if (vec) hipLaunchKernelGGL((scan_fwd_kernel<T, X, KIND, NORM, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((scan_fwd_kernel<T, X, KIND, NORM, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T, typename X>
 static hipError_t launch_kind(const FwdP& p, bool vec, hipStream_t s) {
-  if (p.alpha) return launch_v<T, X, 0>(p, vec, s);
-  return p.gate_x ? launch_v<T, X, 2>(p, vec, s) : launch_v<T, X, 1>(p, vec, s);
+  if (p.alpha) return launch_v<T, X, 0, false>(p, vec, s);
+  if (p.gate_x) return p.normalise ? launch_v<T, X, 2, true>(p, vec, s) : launch_v<T, X, 2, false>(p, vec, s);
+  return p.normalise ? launch_v<T, X, 1, true>(p, vec, s) : launch_v<T, X, 1, false>(p, vec, s);
 }
 
 static hipError_t launch(FwdP& p, int io_dtype, void* workspace, hipStream_t s) {
   p.nct = (p.C + kTileC - 1) / kTileC;
   p.nchain = (int)chains_of(p.B, p.C);
-  p.nt = (int)tiles_t(p.T);
-  const hipError_t e = reset_chains(workspace, p.B, p.T, p.C, &p.ch, s);
+  p.nt = (int)tiles_t(p.T, kFwdWaves);
+  const hipError_t e = reset_chains(workspace, p.B, p.T, p.C, kFwdWaves, &p.ch, s);
   if (e != hipSuccess) return e;
   const size_t io = io_dtype == GDR_BF16 ? 2 : 4;
   const bool vec = p.C % 4 == 0 && vec4_ok(p.x, p.x_exp ? 1 : io) && vec4_ok(p.alpha, 4) && vec4_ok(p.decay_x, io) &&

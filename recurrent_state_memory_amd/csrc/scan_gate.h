@@ -7,9 +7,12 @@
 // bits but m = 2u - ... must keep its relative accuracy (the input is scaled by
 // sqrt(m)).  So log1p corrects the rounding of 1 + w (s = fl(1 + w), c = w - (s
 // - 1) exactly, log1p(w) = log s + c / s, and c / s = c to within 2^-24 of the
-// result: where c matters s is near 1), and m comes from the series of
-// 1 - e^-z below z = 2u = 1/4 and from 1 - a a above it (relative error 4e-7 at
-// the border).  exp, log, rcp and sqrt are the hardware's, 1 ulp each.
+// result: where c matters s is near 1).  And m is z q(z) below z = 2u = 1/2, with
+// q a degree-4 fit of (1 - e^-z) / z at the Chebyshev nodes of [0, 1/2] (relative
+// error 8.4e-8), and 1 - a a above it, where the rounding of a is at most 2 in m.
+// exp, log, rcp and sqrt are the hardware's, 1 ulp each.  The scan kernels spend
+// about as long on these as on memory, so the scale's products are formed once a
+// channel.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -19,28 +22,35 @@ namespace scan {
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.69314718f;
 
-__device__ inline float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// A channel's scale A in the two forms that it is used in.
+struct Scale {
+  float exp2, twice;   // -A log2 e, 2 A
+  __device__ explicit Scale(float A = 0.f) : exp2(-A * kLog2e), twice(2.f * A) {}
+};
 
-// e^-|d| and softplus(d)
-__device__ inline float softplus(float d, float& w) {
-  w = __builtin_amdgcn_exp2f(-__builtin_fabsf(d) * kLog2e);
+__device__ inline float exp_neg_abs(float d) { return __builtin_amdgcn_exp2f(-__builtin_fabsf(d) * kLog2e); }
+__device__ inline float softplus(float d) {
+  const float w = exp_neg_abs(d);
   const float s = 1.f + w;
   const float c = w - (s - 1.f);
-  return fmaxf(d, 0.f) + fmaf(__builtin_amdgcn_logf(s), kLn2, c);
+  // max(d, 0) on the bits, one instruction (fmaxf takes two); a NaN d comes through w
+  const int bits = __float_as_int(d);
+  return __int_as_float(bits > 0 ? bits : 0) + fmaf(__builtin_amdgcn_logf(s), kLn2, c);
+}
+__device__ inline float decay(const Scale& A, float sp) { return __builtin_amdgcn_exp2f(A.exp2 * sp); }
+
+__device__ inline float one_minus_sq(const Scale& A, float sp, float a) {
+  const float z = A.twice * sp;
+  float q = fmaf(z, 0x1.bc858cp-8f, -0x1.4ffafp-5f);
+  q = fmaf(z, q, 0x1.55192ep-3f);
+  q = fmaf(z, q, -0x1.fffe22p-2f);
+  q = fmaf(z, q, 0x1.fffffep-1f);
+  return z < 0.5f ? z * q : fmaf(-a, a, 1.f);
 }
 
-// 1 - e^-2u, a = e^-u
-__device__ inline float one_minus_sq(float u, float a) {
-  const float z = 2.f * u;
-  float p = fmaf(z, -1.f / 720.f, 1.f / 120.f);
-  p = fmaf(z, p, -1.f / 24.f);
-  p = fmaf(z, p, 1.f / 6.f);
-  p = fmaf(z, p, -0.5f);
-  p = fmaf(z, p, 1.f);
-  return z < 0.25f ? z * p : fmaf(-a, a, 1.f);
+__device__ inline float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -kLog2e));
 }
-
-__device__ inline float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.f + exp_fast(-g)); }
 
 }  // namespace scan
 }  // namespace gdr

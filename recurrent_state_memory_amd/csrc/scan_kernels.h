@@ -10,15 +10,16 @@ namespace gdr {
 namespace scan {
 
 constexpr int kTileC = 64;      // channels of a tile
-constexpr int kWaves = 8;       // waves of a full tile
-constexpr int kTileT = kWaves * GDR_SCAN_BLOCK;   // its tokens
+constexpr int kFwdWaves = 8;    // waves of a full tile, one block of tokens each
+constexpr int kBwdWaves = 4;
+constexpr int kSuper = 8;       // tiles that share one hand-over along the sequence
 
 constexpr size_t blocks_of(int T) { return ((size_t)T + GDR_SCAN_BLOCK - 1) / GDR_SCAN_BLOCK; }
-constexpr size_t tiles_t(int T) { return ((size_t)T + kTileT - 1) / kTileT; }
+constexpr size_t tiles_t(int T, int waves) { return (blocks_of(T) + waves - 1) / waves; }
 constexpr size_t chains_of(int B, int C) { return (size_t)B * ((C + kTileC - 1) / kTileC); }
-// Tiles of a launch; a grid holds fewer than 2^23 (2^32 threads).
-constexpr size_t tiles_of(int B, int T, int C) { return chains_of(B, C) * tiles_t(T); }
+// A launch has fewer than 2^23 tiles (a grid holds 2^32 threads).
 constexpr size_t kMaxTiles = (size_t)1 << 23;
+constexpr bool too_many_tiles(int B, int T, int C) { return chains_of(B, C) * tiles_t(T, kBwdWaves) >= kMaxTiles; }
 
 // Workspace of the forward and of the backward (bytes; 0: none needed).
 size_t fwd_workspace(int B, int T, int C);
@@ -31,11 +32,12 @@ hipError_t launch_scan_step(const gdr_scan_step_args& a, hipStream_t s);
 
 // The hand-over words of the chains, and the ticket, at the start of a workspace.
 struct Chains {
-  uint32_t* ticket;   // NULL: one tile per chain, nothing is handed over
-  uint64_t* slots;    // [chains][64]
+  uint32_t* ticket;    // NULL: one tile per chain, nothing is handed over
+  uint64_t* tiles;     // [chains][tiles][64] each tile's map of the state
+  uint64_t* supers;    // [chains][supers][64] the state before each super
 };
-size_t chain_bytes(int B, int T, int C);
-hipError_t reset_chains(void* workspace, int B, int T, int C, Chains* out, hipStream_t s);
+size_t chain_bytes(int B, int T, int C, int waves);
+hipError_t reset_chains(void* workspace, int B, int T, int C, int waves, Chains* out, hipStream_t s);
 
 // The forward of the backward's inputs that writes the block-start states alone.
 hipError_t launch_ckpt(const gdr_scan_bwd_args& a, float* ckpt, void* workspace, hipStream_t s);

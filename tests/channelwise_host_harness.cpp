@@ -57,7 +57,7 @@ int main() {
   EXPECT(gdr_scan_fwd(&f, nullptr), GDR_ERR_UNSUPPORTED);   // tiles
   f.T = 1 << 22;
   EXPECT(gdr_scan_fwd(&f, nullptr), GDR_ERR_SHAPE);
-  f.T = 256 * 2047;
+  f.T = 128 * 2047;
   EXPECT(gdr_scan_fwd(&f, nullptr), GDR_OK);
   f.T += 1;
   EXPECT(gdr_scan_fwd(&f, nullptr), GDR_ERR_UNSUPPORTED);

@@ -150,6 +150,26 @@ def test_scan_long():
     check_bwd(d, "bf16", d["h"], d["dh"], "long gated bwd")
 
 
+@pytest.mark.parametrize("T", [255, 256, 257, 1100, 2049, 5000])
+@pytest.mark.parametrize("kind", ["alpha", "norm"])
+def test_scan_remembers(kind, T):
+    """Channels that keep their start state (and the last gradient) over the whole
+    sequence, beside ones that forget within some hundred tokens: a state lost or
+    taken twice anywhere along the tiles shows at its full size."""
+    B, C = 2, 70
+    d = scan_inputs((B, T), C, "f32", kind, seed=T)
+    A = np.exp(np.linspace(np.log(1e-7), np.log(0.05), C)).astype(np.float32)
+    if kind == "alpha":
+        d["kw"]["alpha"] = np.exp(-A * np.logaddexp(0, d["x"][:, ::-1])).astype(np.float32)
+    else:
+        d["kw"]["A"] = A
+    d["x"] = d["x"] * np.float32(0.01)
+    d["dy"] = d["dy"] * np.float32(0.01)
+    check_fwd(d, "f32", d["h"], f"remembers {kind}/{T}")
+    for ck in (False, True):
+        check_bwd(d, "f32", d["h"], d["dh"], f"remembers {kind}/{T}/ckpt={ck}", ck=ck)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("N,C", [(1, 1), (1, 2048), (7, 66), (256, 64), (3, 1001)])
