@@ -6,13 +6,15 @@
 // tile to tile with the last tiles first.  G_t = grad_y_t + K_{t+1}, so a run of
 // tokens takes K to P K + Q with P the same product of decays.
 //
-// A thread keeps a, b and the softplus of its 32 elements; what the gradients need
-// besides (the two sigmoids; 1 / (1 - a^2) = (s / b)^2) is evaluated again from the
-// inputs' raw registers, which costs less than the registers to keep it would.
+// A thread keeps a, b and the softplus of its 32 elements in registers and the two
+// sigmoids in LDS (its own 16 bytes a token, no barrier), so that they are evaluated
+// once; 1 / (1 - a^2) is (s / b)^2.
 //
 // grad_decay_a sums over all tokens: registers, lane groups, waves (one LDS pass
 // in a fixed order), then one partial row per tile that sum_kernel adds up, again
 // in a fixed order.
+#include <type_traits>
+
 #include "scan_gate.h"
 #include "scan_tile.h"
 
@@ -24,7 +26,7 @@ constexpr float kLeastB = 0x1p-60f;
 
 struct BwdP {
   int B, T, C, normalise;
-  int nchain, nct, nt;
+  int nchain, nct, nt, team;
   const void* x;
   const uint8_t* x_exp;
   const float* alpha;
@@ -47,7 +49,8 @@ template <typename T, typename X, int KIND, bool NORM, bool VEC>
 __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
   constexpr bool kCodes = !__is_same(X, T);
   __shared__ Joins<kBwdWaves> j;   // of the maps of K: later tokens first
-  const Place q = take_place(p.C, p.nchain, p.nct, p.ch.ticket);
+  __shared__ f32x4 kept[KIND == 0 ? 1 : KIND][KIND == 0 ? 1 : S][KIND == 0 ? 1 : 64 * kBwdWaves];   // sigmoid(decay_x), sigmoid(gate_x)
+  const Place q = take_place(p.C, p.nchain, p.nct, p.nt, p.team, p.ch.ticket);
   const int tile = p.nt - 1 - q.tt;         // the last tokens come first
   const int C = p.C, t0 = tile * kBwdWaves * GDR_SCAN_BLOCK;
   const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);
@@ -58,6 +61,15 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
   const int oa = q.nv > 0 ? e0 * 4 : kNoLane;
   const uint32_t tbytes = rows * C * size_of<T>;
 
+  // a wait for a load waits for those before it too: what is needed first comes
+  // first, and row by row
+  float scale[V];
+  if constexpr (KIND != 0) {
+    const Four<float>::R r = Four<float>::template load<VEC>(buffer(p.decay_a, C * 4), q.nv > 0 ? q.c * 4 : kNoLane, q.nv);
+#pragma unroll
+    for (int k = 0; k < V; ++k) scale[k] = Four<float>::get(r, k);
+  }
+  using XR = std::conditional_t<kCodes, __bf16, X>;   // codes become bf16, which holds their values
   typename Four<X>::R rx[S];
   typename Four<T>::R ry[S];
   Four<float>::R ra[KIND == 0 ? S : 1];
@@ -66,24 +78,15 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
   {
     const rsrc_t bx = buffer((const char*)p.x + base * size_of<X>, rows * C * size_of<X>);
     const rsrc_t by = buffer((const T*)p.grad_y + base, tbytes);
-    if constexpr (KIND == 0) {
-      const rsrc_t ba = buffer(p.alpha + base, rows * C * 4);
-#pragma unroll
-      for (int i = 0; i < S; ++i) ra[i] = Four<float>::template load<VEC>(ba, oa + i * C * 4, q.nv);
-    } else {
-      const rsrc_t bd = buffer((const T*)p.decay_x + base, tbytes);
-#pragma unroll
-      for (int i = 0; i < S; ++i) rd[i] = Four<T>::template load<VEC>(bd, ot + i * C * size_of<T>, q.nv);
-    }
+    const rsrc_t ba = buffer(KIND == 0 ? (const char*)(p.alpha + base) : (const char*)((const T*)p.decay_x + base),
+                             KIND == 0 ? rows * C * 4 : tbytes);
+    const rsrc_t bg = buffer(KIND == 2 ? (const T*)p.gate_x + base : nullptr, KIND == 2 ? tbytes : 0);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
+      if constexpr (KIND == 0) ra[i] = Four<float>::template load<VEC>(ba, oa + i * C * 4, q.nv);
+      else rd[i] = Four<T>::template load<VEC>(ba, ot + i * C * size_of<T>, q.nv);
       rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
-      ry[i] = Four<T>::template load<VEC>(by, ot + i * C * size_of<T>, q.nv);
-    }
-    if constexpr (KIND == 2) {
-      const rsrc_t bg = buffer((const T*)p.gate_x + base, tbytes);
-#pragma unroll
-      for (int i = 0; i < S; ++i) rg[i] = Four<T>::template load<VEC>(bg, ot + i * C * size_of<T>, q.nv);
+      if constexpr (KIND == 2) rg[i] = Four<T>::template load<VEC>(bg, ot + i * C * size_of<T>, q.nv);
     }
     if constexpr (kCodes) {
       const int ng = (C + 127) / 128;
@@ -93,25 +96,32 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
       for (int i = 0; i < S; ++i)
         xs[i] = chan::scale_of(__builtin_amdgcn_raw_buffer_load_b8(be, oe + i * ng, 0, 0));
     }
-  }
-  float scale[V], h0[V];
-  const size_t nb = blocks_of(p.T), block = (size_t)tile * kBwdWaves + q.wave;
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    scale[k] = KIND != 0 && k < q.nv ? p.decay_a[q.c + k] : 0.f;
-    h0[k] = k < q.nv && block < nb ? p.ckpt[((size_t)q.b * nb + block) * C + q.c + k] : 0.f;
+    for (int i = 0; i < S; ++i) ry[i] = Four<T>::template load<VEC>(by, ot + i * C * size_of<T>, q.nv);
   }
+  const size_t nb = blocks_of(p.T), block = (size_t)tile * kBwdWaves + q.wave;
+  const Four<float>::R rh = Four<float>::template load<VEC>(
+      buffer(p.ckpt + ((size_t)q.b * nb + (block < nb ? block : 0)) * C, block < nb ? C * 4 : 0),
+      q.nv > 0 ? q.c * 4 : kNoLane, q.nv);
   const int cc = q.c0 + q.lane;
   const int pos = q.nw - 1 - q.wave;        // the wave's place in the order of joining
+  const Words<kBwdWaves> words = look_ahead<kBwdWaves>(p.ch, q, p.nt, pos);
   float k_in = 0.f;
   if (q.wave == 0 && q.tt < kSuper && p.grad_h && cc < C) k_in = p.grad_h[(size_t)q.b * C + cc];
 
   // a and b; (P, H) forwards and (P, Q) backwards over the thread's run
+  typename Four<XR>::R xr[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    if constexpr (kCodes)
+      xr[i] = u32x2{bf16_pair(Four<X>::get(rx[i], 0) * xs[i], Four<X>::get(rx[i], 1) * xs[i]),
+                    bf16_pair(Four<X>::get(rx[i], 2) * xs[i], Four<X>::get(rx[i], 3) * xs[i])};
+    else
+      xr[i] = rx[i];
+  }
   float a[S][V], b[KIND == 2 || NORM ? S : 1][V], sp[KIND == 0 ? 1 : S][V], P[V], H[V], Q[V];
   const auto x_at = [&](int i, int k) {
-    const float x = Four<X>::get(rx[i], k);
-    if constexpr (kCodes) return x * xs[i];
-    return x;
+    return Four<XR>::get(xr[i], k);
   };
   const auto v_at = [&](int i, int k) {
     if constexpr (KIND == 2 || NORM) return b[i][k] * x_at(i, k);
@@ -124,34 +134,48 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
   }
 #pragma unroll
   for (int i = 0; i < S; ++i) {
+    f32x4 kd, kg;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       if constexpr (KIND == 0) {
         a[i][k] = Four<float>::get(ra[i], k);
       } else {
         const Scale A(scale[k]);
-        sp[i][k] = softplus(Four<T>::get(rd[i], k));
+        float sig;
+        sp[i][k] = softplus(Four<T>::get(rd[i], k), sig);
+        kd[k] = sig;
         a[i][k] = decay(A, sp[i][k]);
-        if constexpr (KIND == 2) b[i][k] = sigmoid(Four<T>::get(rg[i], k));
+        if constexpr (KIND == 2) kg[k] = b[i][k] = sigmoid(Four<T>::get(rg[i], k));
         if constexpr (NORM) {
           const float n = __builtin_amdgcn_sqrtf(one_minus_sq(A, sp[i][k], a[i][k]));
           b[i][k] = KIND == 2 ? b[i][k] * n : n;
         }
       }
     }
-    // behind the last token the state stays: x and grad_y read as 0 there, and a
-    // softplus of 0 keeps the row out of grad_decay_a
-    if (r0 + i >= rows) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        a[i][k] = 1.f;
-        if constexpr (KIND != 0) sp[i][k] = 0.f;
-      }
-    }
+    if constexpr (KIND != 0) kept[0][i][threadIdx.x] = kd;
+    if constexpr (KIND == 2) kept[1][i][threadIdx.x] = kg;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       P[k] *= a[i][k];
       H[k] = fmaf(a[i][k], H[k], v_at(i, k));
+    }
+  }
+  // behind the last token the state stays: x and grad_y read as 0 there, and a
+  // softplus of 0 keeps the row out of grad_decay_a
+  if (rows < q.nw * GDR_SCAN_BLOCK) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      P[k] = 1.f;
+      H[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        if (r0 + i >= rows) {
+          a[i][k] = 1.f;
+          if constexpr (KIND != 0) sp[i][k] = 0.f;
+        }
+        P[k] *= a[i][k];
+        H[k] = fmaf(a[i][k], H[k], v_at(i, k));
+      }
     }
   }
 #pragma unroll
@@ -165,7 +189,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
     for (int k = 0; k < V; ++k) Pf[k] = P[k];
     join_groups<true>(Pf, H, Pe, He, q.grp);
 #pragma unroll
-    for (int k = 0; k < V; ++k) h[k] = fmaf(Pe[k], h0[k], He[k]);   // the state before the run
+    for (int k = 0; k < V; ++k) h[k] = fmaf(Pe[k], Four<float>::get(rh, k), He[k]);   // the state before the run
   }
   join_groups<false>(P, Q, Pb, Qb, q.grp);
   if (q.grp == 0) {
@@ -173,7 +197,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
     for (int k = 0; k < V; ++k) j.run[pos][q.cl + k] = float2{P[k], Q[k]};
   }
   float k_end;
-  join_tiles(j, p.ch, q, p.nt, pos, k_in, k_end);
+  join_tiles(j, p.ch, q, words, p.nt, pos, k_in, k_end);
   if (p.grad_h0 && q.tt + 1 == p.nt && q.wave == 0 && cc < C) p.grad_h0[(size_t)q.b * C + cc] = k_end;
   float K[V];
 #pragma unroll
@@ -191,7 +215,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
   float prev[HS][V];
 #pragma unroll
   for (int i = 0; i < (half + 1) * HS; ++i) {
-    forget(rx[i]);
+    forget(xr[i]);
     forget(ry[i]);
   }
   {
@@ -211,8 +235,9 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
 #pragma unroll
   for (int i = (half + 1) * HS - 1; i >= half * HS; --i) {
     float ox_[V], od[V], og[V];
-    if constexpr (KIND != 0) forget(rd[i]);
-    if constexpr (KIND == 2) forget(rg[i]);
+    f32x4 kd, kg;
+    if constexpr (KIND != 0) kd = kept[0][i][threadIdx.x];
+    if constexpr (KIND == 2) kg = kept[1][i][threadIdx.x];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const float G = Four<T>::get(ry[i], k) + K[k];
@@ -226,7 +251,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
         ox_[k] = G;
         if constexpr (KIND == 2 || NORM) ox_[k] *= b[i][k];
         if constexpr (KIND == 2) {
-          sg = sigmoid(Four<T>::get(rg[i], k));
+          sg = kg[k];
           og[k] = G * v_at(i, k) * (1.f - sg);
         }
         if constexpr (NORM) {   // v a / m = x a s^2 / b
@@ -235,8 +260,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
         }
         const float du = K[k] * in;
         sum[k] = fmaf(du, sp[i][k], sum[k]);
-        const float d = Four<T>::get(rd[i], k), w = exp_neg_abs(d), r = __builtin_amdgcn_rcpf(1.f + w);
-        od[k] = du * scale[k] * (d > 0.f ? r : w * r);
+        od[k] = du * scale[k] * kd[k];
       }
     }
     Four<T>::template store<VEC>(gx, ot + i * C * size_of<T>, q.nv, ox_);
@@ -319,7 +343,7 @@ hipError_t launch_scan_bwd(const gdr_scan_bwd_args& a, hipStream_t s) {
     rest += align256((size_t)a.B * blocks_of(a.T) * a.C * 4);
   }
   BwdP p{a.B, a.T, a.C, a.normalise, (int)chains_of(a.B, a.C), (a.C + kTileC - 1) / kTileC, (int)tiles_t(a.T, kBwdWaves),
-         a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, ckpt, a.grad_y, a.grad_h, a.grad_x, a.grad_alpha,
+         team_of(a.alpha != nullptr, a.io_dtype), a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, ckpt, a.grad_y, a.grad_h, a.grad_x, a.grad_alpha,
          a.grad_decay_x, a.grad_gate_x, a.grad_h0, a.alpha ? nullptr : (float*)rest, {}};
   hipError_t e = reset_chains(ws, a.B, a.T, a.C, kBwdWaves, &p.ch, s);
   if (e != hipSuccess) return e;

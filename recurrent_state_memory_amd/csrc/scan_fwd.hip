@@ -14,7 +14,7 @@ using chan::st;
 
 struct FwdP {
   int B, T, C, normalise;
-  int nchain, nct, nt;   // chains, channel tiles of a row, tiles of a chain
+  int nchain, nct, nt, team;   // chains, channel tiles of a row, tiles of a chain
   const void* x;
   const uint8_t* x_exp;
   const float* alpha;
@@ -34,13 +34,21 @@ template <typename T, typename X, int KIND, bool NORM, bool VEC>
 __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   constexpr bool kCodes = !__is_same(X, T);
   __shared__ Joins<kFwdWaves> j;
-  const Place q = take_place(p.C, p.nchain, p.nct, p.ch.ticket);
+  const Place q = take_place(p.C, p.nchain, p.nct, p.nt, p.team, p.ch.ticket);
   const int C = p.C, t0 = q.tt * kFwdWaves * GDR_SCAN_BLOCK;
   const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);   // of the tile that exist
   const int r0 = q.wave * GDR_SCAN_BLOCK + q.grp * S;      // the thread's first row
   const size_t base = ((size_t)q.b * p.T + t0) * C;
   const int e0 = r0 * C + q.c;                             // its first element from base
 
+  // a wait for a load waits for those before it too: what is needed first comes
+  // first, and row by row
+  Scale A[V];
+  if constexpr (KIND != 0) {
+    const Four<float>::R r = Four<float>::template load<VEC>(buffer(p.decay_a, C * 4), q.nv > 0 ? q.c * 4 : kNoLane, q.nv);
+#pragma unroll
+    for (int k = 0; k < V; ++k) A[k] = Scale(Four<float>::get(r, k));
+  }
   typename Four<X>::R rx[S];
   Four<float>::R ra[KIND == 0 ? S : 1];
   typename Four<T>::R rd[KIND == 0 ? 1 : S], rg[KIND == 2 ? S : 1];
@@ -48,26 +56,16 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   {
     const rsrc_t bx = buffer((const char*)p.x + base * size_of<X>, rows * C * size_of<X>);
     const int ox = q.nv > 0 ? e0 * size_of<X> : kNoLane, ot = q.nv > 0 ? e0 * size_of<T> : kNoLane;
-    if constexpr (KIND == 0) {
-      const rsrc_t ba = buffer(p.alpha + base, rows * C * 4);
-      const int oa = q.nv > 0 ? e0 * 4 : kNoLane;
+    const rsrc_t ba = buffer(KIND == 0 ? (const char*)(p.alpha + base) : (const char*)((const T*)p.decay_x + base),
+                             rows * C * (KIND == 0 ? 4 : size_of<T>));
+    const rsrc_t bg = buffer(KIND == 2 ? (const T*)p.gate_x + base : nullptr, KIND == 2 ? rows * C * size_of<T> : 0);
+    const int oa = q.nv > 0 ? e0 * 4 : kNoLane;
 #pragma unroll
-      for (int i = 0; i < S; ++i) {
-        ra[i] = Four<float>::template load<VEC>(ba, oa + i * C * 4, q.nv);
-        rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
-      }
-    } else {
-      const rsrc_t bd = buffer((const T*)p.decay_x + base, rows * C * size_of<T>);
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        rd[i] = Four<T>::template load<VEC>(bd, ot + i * C * size_of<T>, q.nv);
-        rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
-      }
-      if constexpr (KIND == 2) {
-        const rsrc_t bg = buffer((const T*)p.gate_x + base, rows * C * size_of<T>);
-#pragma unroll
-        for (int i = 0; i < S; ++i) rg[i] = Four<T>::template load<VEC>(bg, ot + i * C * size_of<T>, q.nv);
-      }
+    for (int i = 0; i < S; ++i) {
+      if constexpr (KIND == 0) ra[i] = Four<float>::template load<VEC>(ba, oa + i * C * 4, q.nv);
+      else rd[i] = Four<T>::template load<VEC>(ba, ot + i * C * size_of<T>, q.nv);
+      rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
+      if constexpr (KIND == 2) rg[i] = Four<T>::template load<VEC>(bg, ot + i * C * size_of<T>, q.nv);
     }
     if constexpr (kCodes) {   // four neighbouring channels share a group of 128
       const int ng = (C + 127) / 128;
@@ -78,11 +76,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
         xs[i] = chan::scale_of(__builtin_amdgcn_raw_buffer_load_b8(be, oe + i * ng, 0, 0));
     }
   }
-  Scale A[V];
-  if constexpr (KIND != 0) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) A[k] = Scale(k < q.nv ? p.decay_a[q.c + k] : 0.f);
-  }
+  const Words<kFwdWaves> words = look_ahead<kFwdWaves>(p.ch, q, p.nt, q.wave);
   // the start state, asked for early by the wave that joins the first super's tiles to it
   const int cc = q.c0 + q.lane;
   float h_in = 0.f;
@@ -110,17 +104,26 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
       }
       v[i][k] = x;
     }
-    if (r0 + i >= rows) {   // behind the last token: the state stays
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        a[i][k] = 1.f;
-        v[i][k] = 0.f;
-      }
-    }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       P[k] *= a[i][k];
       H[k] = fmaf(a[i][k], H[k], v[i][k]);
+    }
+  }
+  if (rows < q.nw * GDR_SCAN_BLOCK) {   // behind the last token the state stays
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      P[k] = 1.f;
+      H[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        if (r0 + i >= rows) {
+          a[i][k] = 1.f;
+          v[i][k] = 0.f;
+        }
+        P[k] *= a[i][k];
+        H[k] = fmaf(a[i][k], H[k], v[i][k]);
+      }
     }
   }
   float Pe[V], He[V];
@@ -130,7 +133,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
     for (int k = 0; k < V; ++k) j.run[q.wave][q.cl + k] = float2{P[k], H[k]};
   }
   float h_end;
-  const float h_wave = join_tiles(j, p.ch, q, p.nt, q.wave, h_in, h_end);
+  const float h_wave = join_tiles(j, p.ch, q, words, p.nt, q.wave, h_in, h_end);
   if (p.h_out && q.tt + 1 == p.nt && q.wave == q.nw - 1 && cc < C) p.h_out[(size_t)q.b * C + cc] = h_end;
   if (p.ckpt && cc < C && q.wave * GDR_SCAN_BLOCK < rows)
     p.ckpt[((size_t)q.b * blocks_of(p.T) + (size_t)q.tt * kFwdWaves + q.wave) * C + cc] = h_wave;
@@ -225,6 +228,7 @@ static hipError_t launch(FwdP& p, int io_dtype, void* workspace, hipStream_t s) 
   p.nct = (p.C + kTileC - 1) / kTileC;
   p.nchain = (int)chains_of(p.B, p.C);
   p.nt = (int)tiles_t(p.T, kFwdWaves);
+  p.team = team_of(p.alpha != nullptr, io_dtype);
   const hipError_t e = reset_chains(workspace, p.B, p.T, p.C, kFwdWaves, &p.ch, s);
   if (e != hipSuccess) return e;
   const size_t io = io_dtype == GDR_BF16 ? 2 : 4;
@@ -236,13 +240,13 @@ static hipError_t launch(FwdP& p, int io_dtype, void* workspace, hipStream_t s) 
 }
 
 hipError_t launch_scan_fwd(const gdr_scan_args& a, hipStream_t s) {
-  FwdP p{a.B, a.T, a.C, a.normalise, 0, 0, 0, a.x, nullptr, a.alpha, a.decay_x, a.decay_a, a.gate_x, a.h0, a.y, a.h_out,
+  FwdP p{a.B, a.T, a.C, a.normalise, 0, 0, 0, 0, a.x, nullptr, a.alpha, a.decay_x, a.decay_a, a.gate_x, a.h0, a.y, a.h_out,
          a.ckpt, {}};
   return launch(p, a.io_dtype, a.workspace, s);
 }
 
 hipError_t launch_ckpt(const gdr_scan_bwd_args& a, float* ckpt, void* workspace, hipStream_t s) {
-  FwdP p{a.B, a.T, a.C, a.normalise, 0, 0, 0, a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, a.h0, nullptr,
+  FwdP p{a.B, a.T, a.C, a.normalise, 0, 0, 0, 0, a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, a.h0, nullptr,
          nullptr, ckpt, {}};
   return launch(p, a.io_dtype, workspace, s);
 }

@@ -28,14 +28,25 @@ struct Scale {
   __device__ explicit Scale(float A = 0.f) : exp2(-A * kLog2e), twice(2.f * A) {}
 };
 
-__device__ inline float exp_neg_abs(float d) { return __builtin_amdgcn_exp2f(-__builtin_fabsf(d) * kLog2e); }
-__device__ inline float softplus(float d) {
-  const float w = exp_neg_abs(d);
-  const float s = 1.f + w;
+__device__ inline float softplus(float d, float& w, float& s) {
+  w = __builtin_amdgcn_exp2f(-__builtin_fabsf(d) * kLog2e);
+  s = 1.f + w;
   const float c = w - (s - 1.f);
   // max(d, 0) on the bits, one instruction (fmaxf takes two); a NaN d comes through w
   const int bits = __float_as_int(d);
   return __int_as_float(bits > 0 ? bits : 0) + fmaf(__builtin_amdgcn_logf(s), kLn2, c);
+}
+__device__ inline float softplus(float d) {
+  float w, s;
+  return softplus(d, w, s);
+}
+// with sigmoid(d) = 1 / (1 + w) or w / (1 + w)
+__device__ inline float softplus(float d, float& sig) {
+  float w, s;
+  const float sp = softplus(d, w, s);
+  const float r = __builtin_amdgcn_rcpf(s);
+  sig = d > 0.f ? r : w * r;
+  return sp;
 }
 __device__ inline float decay(const Scale& A, float sp) { return __builtin_amdgcn_exp2f(A.exp2 * sp); }
 

@@ -15,8 +15,8 @@
 // reader sees about a microsecond later, serves 8 tiles (with one per tile, a
 // single sequence of 32785 tokens took 140 us, 128 hand-overs of about 1.05 us).
 //
-// Tile numbers are drawn from a ticket, in which all chains' first tiles come
-// before their second ones: a tile waits only for tiles whose workgroups have
+// Tile numbers are drawn from a ticket.  Chains are taken in teams, and a team's
+// first tiles come before its second ones: a tile waits only for tiles whose workgroups have
 // already started, and each publishes its map before it waits, so every wait ends;
 // were one not to (a workspace in use elsewhere), it gives up after kSpinLimit
 // polls with NaN.
@@ -34,6 +34,7 @@ constexpr int kSpinLimit = 1 << 22;   // a poll takes about a microsecond
 
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
 using rsrc_t = __amdgpu_buffer_rsrc_t;
 
 struct Code8 {};   // element type of 8-bit checkpoint codes
@@ -56,6 +57,12 @@ constexpr int kNoLane = 0x40000000;
 // access of all four (a row's channels are a multiple of 4: all are there, or none).
 // Else one access each, of the `nv` that are there.
 __device__ inline int at(int off, int k, int nv, int size) { return k < nv ? off + k * size : kNoLane; }
+
+__device__ inline uint32_t bf16_pair(float lo, float hi) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+  const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
 
 template <typename T>
 struct Four;
@@ -152,7 +159,7 @@ struct Place {
 
 // The next tile in ticket order (or the workgroup's own, when no tile waits for
 // another).  Contains barriers: every thread of the workgroup calls it.
-__device__ inline Place take_place(int C, int nchain, int nct, uint32_t* ticket) {
+__device__ inline Place take_place(int C, int nchain, int nct, int nt, int team_size, uint32_t* ticket) {
   __shared__ uint32_t drawn;
   uint32_t tile = blockIdx.x;
   if (ticket) {
@@ -162,8 +169,10 @@ __device__ inline Place take_place(int C, int nchain, int nct, uint32_t* ticket)
   }
   tile = __builtin_amdgcn_readfirstlane(tile);
   Place q;
-  q.chain = tile % (uint32_t)nchain;
-  q.tt = tile / (uint32_t)nchain;
+  const uint32_t full = (uint32_t)team_size * nt, team = tile / full, in = tile - team * full;
+  const uint32_t size = min((uint32_t)team_size, nchain - team * team_size);
+  q.tt = in / size;
+  q.chain = team * team_size + (in - q.tt * size);
   q.b = q.chain / nct;
   q.c0 = (q.chain % nct) * kTileC;
   q.lane = threadIdx.x & 63;
@@ -217,22 +226,26 @@ __device__ inline void put_map(uint64_t* word, float2 r) {
 __device__ inline void put_state(uint64_t* word, float h) {
   __hip_atomic_store(word, ((uint64_t)__float_as_uint(h) << 32) | 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// The wave's 64 words once all are written (0 after kSpinLimit polls).
-__device__ inline uint64_t wait_words(const uint64_t* word) {
+__device__ inline uint64_t look(const uint64_t* word) {
+  return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The wave's 64 words once all are written (0 after kSpinLimit polls); w is what
+// the lane saw at its first look.
+__device__ inline uint64_t wait_words(const uint64_t* word, uint64_t w) {
   for (int n = 0; n < kSpinLimit; ++n) {
-    const uint64_t w = __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (__all((uint32_t)w != 0u)) return w;
     __builtin_amdgcn_s_sleep(1);
+    w = look(word);
   }
   return 0;
 }
-__device__ inline float2 get_map(const uint64_t* word) {
-  const uint64_t w = wait_words(word);
+__device__ inline float2 get_map(const uint64_t* word, uint64_t seen) {
+  const uint64_t w = wait_words(word, seen);
   if ((uint32_t)w == 0u) return float2{__builtin_nanf(""), __builtin_nanf("")};
   return float2{__uint_as_float(~(uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
 }
-__device__ inline float get_state(const uint64_t* word) {
-  const uint64_t w = wait_words(word);
+__device__ inline float get_state(const uint64_t* word, uint64_t seen) {
+  const uint64_t w = wait_words(word, seen);
   return (uint32_t)w == 0u ? __builtin_nanf("") : __uint_as_float((uint32_t)(w >> 32));
 }
 
@@ -245,18 +258,42 @@ struct Joins {
   float from[NW][kTileC];        // and before each wave
 };
 
+// A tile's words, and a first look at those it will need, taken when its inputs are
+// asked for: where tiles outnumber the workgroups that run at once, the tiles
+// before are long done and nothing is waited for later.
+template <int NW>
+struct Words {
+  static constexpr int kMaps = (kSuper - 1 + NW - 1) / NW;   // maps that a wave fetches
+  uint64_t *tile, *super;
+  uint64_t map[kMaps], state;
+};
+template <int NW>
+__device__ inline Words<NW> look_ahead(const Chains& ch, const Place& q, int nt, int pos) {
+  Words<NW> w;
+  if (!ch.ticket) return w;
+  const int r = q.tt % kSuper, su = q.tt / kSuper, ns = (nt + kSuper - 1) / kSuper;
+  w.tile = ch.tiles + ((size_t)q.chain * nt + q.tt) * kTileC + q.lane;
+  w.super = ch.supers + ((size_t)q.chain * ns + su) * kTileC + q.lane;
+#pragma unroll
+  for (int i = 0; i < Words<NW>::kMaps; ++i) {
+    const int k = q.wave + i * NW;
+    w.map[i] = k < r ? look(w.tile - (size_t)(r - k) * kTileC) : 0u;
+  }
+  w.state = pos == NW - 1 && su > 0 ? look(w.super) : 0u;
+  return w;
+}
+
 // From the waves' maps (j.run, written before the call) to the state before each
 // wave, for channel `lane` (returned) and in j.from for the wave's own threads.
 // `pos` is the wave's place in the order of joining, `first` the state before the
 // chain (read by the last wave in order), `last` receives the state behind the
 // tile in that wave.  Every thread of the workgroup calls it.
 template <int NW>
-__device__ inline float join_tiles(Joins<NW>& j, const Chains& ch, const Place& q, int nt, int pos, float first,
-                                   float& last) {
-  const int lane = q.lane, r = q.tt % kSuper, su = q.tt / kSuper, ns = (nt + kSuper - 1) / kSuper;
+__device__ inline float join_tiles(Joins<NW>& j, const Chains& ch, const Place& q, const Words<NW>& words, int nt,
+                                   int pos, float first, float& last) {
+  const int lane = q.lane, r = q.tt % kSuper, su = q.tt / kSuper;
   __syncthreads();
   if (ch.ticket) {
-    uint64_t* tile = ch.tiles + ((size_t)q.chain * nt + q.tt) * kTileC + lane;
     if (q.wave == 0 && r < kSuper - 1 && q.tt + 1 < nt) {
       float2 m = {1.f, 0.f};
 #pragma unroll
@@ -264,10 +301,14 @@ __device__ inline float join_tiles(Joins<NW>& j, const Chains& ch, const Place& 
         const float2 a = j.run[w][lane];
         m = float2{m.x * a.x, fmaf(a.x, m.y, a.y)};
       }
-      put_map(tile, m);
+      put_map(words.tile, m);
     }
-    for (int k = q.wave; k < r; k += NW) j.pre[k][lane] = get_map(tile - (size_t)(r - k) * kTileC);
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < Words<NW>::kMaps; ++i) {
+      const int k = q.wave + i * NW;
+      if (k < r) j.pre[k][lane] = get_map(words.tile - (size_t)(r - k) * kTileC, words.map[i]);
+    }
+    if (r > 0) __syncthreads();
   }
   if (pos == q.nw - 1) {
     float2 before = {1.f, 0.f}, own = {1.f, 0.f};
@@ -283,11 +324,10 @@ __device__ inline float join_tiles(Joins<NW>& j, const Chains& ch, const Place& 
         const float2 a = j.run[w][lane];
         own = float2{own.x * a.x, fmaf(a.x, own.y, a.y)};
       }
-    uint64_t* super = ch.supers + ((size_t)q.chain * ns + su) * kTileC + lane;
-    const float in = su > 0 ? get_state(super) : first;
+    const float in = su > 0 ? get_state(words.super, words.state) : first;
     const float h = fmaf(before.x, in, before.y);
     last = fmaf(own.x, h, own.y);
-    if (r == kSuper - 1 && q.tt + 1 < nt) put_state(super + kTileC, last);
+    if (r == kSuper - 1 && q.tt + 1 < nt) put_state(words.super + kTileC, last);
     j.start[lane] = h;
   }
   __syncthreads();
