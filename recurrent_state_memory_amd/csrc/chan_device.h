@@ -32,17 +32,13 @@ __device__ inline float scale_of(uint32_t e) {
 }
 __device__ inline float inv_scale_of(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 
-// Two (four) scaled values as e4m3 codes, RNE.  The scaled magnitude is at most
-// 448, so nothing saturates; NaN and Inf are made NaN codes here rather than
-// left to the conversion's overflow rule.
+// Scaled values as e4m3 codes, RNE.  The scaled magnitude is at most 448, so nothing
+// saturates; Inf is made NaN before rather than left to the conversion's rule.
 __device__ inline float no_inf(float x) { return __builtin_fabsf(x) == __builtin_inff() ? __builtin_nanf("") : x; }
 __device__ inline uint32_t pack4_e4m3(float a, float b, float c, float d) {
-  int r = __builtin_amdgcn_cvt_pk_fp8_f32(no_inf(a), no_inf(b), 0, false);
-  r = __builtin_amdgcn_cvt_pk_fp8_f32(no_inf(c), no_inf(d), r, true);
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
   return (uint32_t)r;
-}
-__device__ inline uint8_t pack1_e4m3(float a) {
-  return (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(no_inf(a), 0.f, 0, false);
 }
 // Codes as numbers (byte i of c).
 template <int I>
@@ -181,21 +177,85 @@ struct Codes<4> {
   }
 };
 
-// Sum (maximum) over L neighbouring lanes, L a power of two up to 64.
+// Sum (maximum) over L neighbouring lanes, L a power of two from 8 to 64, in every
+// one of them.  Within rows of 16 lanes by rotation (DPP, no LDS), across rows by
+// the lane swaps: with both operands v, permlane16_swap leaves the even and the odd
+// rows' values in its two results, permlane32_swap the lower and the upper half's.
+template <int ROR>
+__device__ inline uint32_t row_ror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ROR, 0xf, 0xf, false);
+}
+template <int L, typename OP>
+__device__ inline uint32_t lane_join(uint32_t v, OP op) {
+  static_assert(L == 8 || L == 16 || L == 32 || L == 64, "lanes");
+  if constexpr (L == 8) {   // eight lanes of a row: exchanges within them
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, false));    // lane ^ 1
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, false));    // lane ^ 2
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));   // 7 - lane of each 8
+    return v;
+  } else {
+    v = op(v, row_ror<8>(v));
+    v = op(v, row_ror<4>(v));
+    v = op(v, row_ror<2>(v));
+    v = op(v, row_ror<1>(v));
+    if constexpr (L >= 32) {
+      const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+      v = op(r[0], r[1]);
+    }
+    if constexpr (L == 64) {
+      const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+      v = op(r[0], r[1]);
+    }
+    return v;
+  }
+}
 template <int L>
 __device__ inline float lane_sum(float v) {
-#pragma unroll
-  for (int off = 1; off < L; off <<= 1) v += __shfl_xor(v, off);
-  return v;
+  return __uint_as_float(lane_join<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 template <int L>
 __device__ inline uint32_t lane_max(uint32_t v) {
+  return lane_join<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+// 8-bit codes of a run that lies in a group of 128 values held by L lanes side by
+// side, and the group's exponent.  A group without NaN and Inf, nearly every one,
+// takes its maximum from the magnitudes' bits as they are.
+template <typename T, int L>
+__device__ inline typename Codes<Run<T>::N>::R pack_run(const raw4& r, int& e) {
+  constexpr int N = Run<T>::N;
+  float v[N];
 #pragma unroll
-  for (int off = 1; off < L; off <<= 1) {
-    const uint32_t o = __shfl_xor(v, off);
-    v = o > v ? o : v;
+  for (int k = 0; k < N; ++k) v[k] = Run<T>::get(r, k);
+  uint32_t m = 0;
+  if constexpr (N == 8) {   // bf16: two magnitudes to a register
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 h = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h = __builtin_elementwise_max(h, __builtin_bit_cast(u16x2, r[i] & 0x7fff7fffu));
+    m = (uint32_t)(h[0] > h[1] ? h[0] : h[1]) << 16;
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint32_t b = r[k] & 0x7fffffffu;
+      m = b > m ? b : m;
+    }
   }
-  return v;
+  m = lane_max<L>(m);
+  if (m >= 0x7f800000u) {
+    m = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint32_t b = finite_mag_bits(v[k]);
+      m = b > m ? b : m;
+      v[k] = no_inf(v[k]);
+    }
+    m = lane_max<L>(m);
+  }
+  e = ckpt8_exponent(m);
+  return Codes<N>::pack(v, inv_scale_of(e));
 }
 
 }  // namespace chan

@@ -43,17 +43,9 @@ __global__ __launch_bounds__(256) void pack_kernel(gdr_ckpt8_pack_args p, size_t
     }
 #pragma unroll
     for (int i = 0; i < kMany; ++i) {
-      float v[N];
-      uint32_t m = 0;
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        v[k] = Run<T>::get(r[i], k);
-        const uint32_t b = chan::finite_mag_bits(v[k]);
-        m = b > m ? b : m;
-      }
-      m = chan::lane_max<kLanes>(m);
-      const int e = chan::ckpt8_exponent(m);
-      Codes<N>::store(p.code + q[i].row * p.D + q[i].c0, q[i].n, Codes<N>::pack(v, chan::inv_scale_of(e)));
+      int e;
+      const auto c = chan::pack_run<T, kLanes>(r[i], e);
+      Codes<N>::store(p.code + q[i].row * p.D + q[i].c0, q[i].n, c);
       if (threadIdx.x % kLanes == 0 && q[i].n > 0) p.exp[g0 + i * step] = (uint8_t)e;
     }
   }

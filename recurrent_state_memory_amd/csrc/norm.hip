@@ -12,35 +12,38 @@ namespace gdr {
 namespace norm {
 
 using chan::Codes;
-using chan::lane_max;
 using chan::lane_sum;
 using chan::raw4;
 using chan::Run;
 
-constexpr int threads_of(int L) { return L > 256 ? L : 256; }
+constexpr int threads_of(int L) { return L > 256 ? L : 256; }   // of a forward workgroup
 
-// Sums of two values over the row's L threads; more than a wave: through LDS.
-template <int L, int NSUM>
-__device__ inline void row_sum(float (&v)[NSUM]) {
+// Sums over the row's L threads of a workgroup of TH; more than a wave: through LDS,
+// in one of two places by turns, so that one barrier a sum is enough.
+template <int TH, int NSUM>
+struct RowSums {
+  float part[2][NSUM][TH / 64];
+};
+template <int TH, int L, int NSUM>
+__device__ inline void row_sum(float (&v)[NSUM], RowSums<TH, NSUM>& lds, int& turn) {
   constexpr int W = L / 64;
 #pragma unroll
   for (int i = 0; i < NSUM; ++i) v[i] = lane_sum<(L < 64 ? L : 64)>(v[i]);
   if constexpr (W > 1) {
-    __shared__ float part[NSUM][W];
-    const int w = threadIdx.x >> 6;
-    __syncthreads();   // the last sums have been read
+    const int w = threadIdx.x >> 6, w0 = w / W * W;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < NSUM; ++i) part[i][w] = v[i];
+      for (int i = 0; i < NSUM; ++i) lds.part[turn][i][w] = v[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NSUM; ++i) {
       float s = 0.f;
 #pragma unroll
-      for (int k = 0; k < W; ++k) s += part[i][k];
+      for (int k = 0; k < W; ++k) s += lds.part[turn][i][w0 + k];
       v[i] = s;
     }
+    turn ^= 1;
   }
 }
 
@@ -49,6 +52,8 @@ __global__ __launch_bounds__(threads_of(L)) void norm_fwd_kernel(gdr_norm_args p
   constexpr int N = Run<T>::N;
   constexpr int kPer = threads_of(L) / L;           // rows of a workgroup
   constexpr int kGroupLanes = 128 / N < L ? 128 / N : L;
+  __shared__ RowSums<threads_of(L), 1> sums;
+  int turn = 0;
   const int l = threadIdx.x % L;
   const int D = p.D;
   const int64_t step = (int64_t)gridDim.x * kPer;
@@ -62,7 +67,7 @@ __global__ __launch_bounds__(threads_of(L)) void norm_fwd_kernel(gdr_norm_args p
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int k = 0; k < N; ++k) s[0] += Run<T>::get(r[j], k);   // 0 behind the row's end
-    row_sum<L, 1>(s);
+    row_sum<threads_of(L), L>(s, sums, turn);
     const float mean = s[0] / D;
     s[0] = 0.f;
 #pragma unroll
@@ -72,7 +77,7 @@ __global__ __launch_bounds__(threads_of(L)) void norm_fwd_kernel(gdr_norm_args p
         const float c = (j * L + l) * N + k < D ? Run<T>::get(r[j], k) - mean : 0.f;
         s[0] = fmaf(c, c, s[0]);
       }
-    row_sum<L, 1>(s);
+    row_sum<threads_of(L), L>(s, sums, turn);
     const float rstd = 1.f / sqrtf(s[0] / D + p.eps);
     if (l == 0) {
       if (p.mean) p.mean[row] = mean;
@@ -102,27 +107,20 @@ __global__ __launch_bounds__(threads_of(L)) void norm_fwd_kernel(gdr_norm_args p
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c0 = (j * L + l) * N;
-        float v[N];
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          v[k] = Run<T>::get(r[j], k);
-          const uint32_t b = chan::finite_mag_bits(v[k]);
-          m = b > m ? b : m;
-        }
-        m = lane_max<kGroupLanes>(m);
-        const int e = chan::ckpt8_exponent(m);
-        Codes<N>::store(p.x_code + (size_t)row * D + c0, D - c0, Codes<N>::pack(v, chan::inv_scale_of(e)));
+        int e;
+        const auto c = chan::pack_run<T, kGroupLanes>(r[j], e);
+        Codes<N>::store(p.x_code + (size_t)row * D + c0, D - c0, c);
         if (c0 < D && l % kGroupLanes == 0) p.x_exp[(size_t)row * G + c0 / 128] = (uint8_t)e;
       }
     }
   }
 }
 
-// Backward.  Each group of L threads takes every `step`-th row and keeps its
-// columns' sums in registers (SUMS); groups are joined over the wave and the
-// workgroup, in a fixed order, and a workgroup leaves one partial row of each sum
-// for join_kernel.
+// Backward.  A workgroup of TH threads takes TH / L rows at a time, every
+// (gridDim TH / L)-th; a thread keeps its columns' sums in registers (SUMS).  Groups
+// are joined over the wave and the workgroup, in a fixed order, and a workgroup
+// leaves one partial row of each sum for join_kernel.  AHEAD: the next row is asked
+// for before this one is worked on.
 template <typename T, bool CODES, int NV>
 struct BwdRow {
   static constexpr int N = Run<T>::N;
@@ -131,6 +129,18 @@ struct BwdRow {
   typename Codes<N>::R c[CODES ? NV : 1];
   uint8_t e[CODES ? NV : 1];
   float mean, rstd;
+  // x of run j as fp32
+  __device__ inline void get_x(int j, float (&v)[N]) const {
+    if constexpr (CODES) {
+      Codes<N>::unpack(c[j], v);
+      const float sc = chan::scale_of(e[j]);
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] *= sc;
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = Run<T>::get(x[j], k);
+    }
+  }
 };
 
 template <typename T, bool CODES, int L, int NV>
@@ -153,117 +163,125 @@ __device__ inline void load_row(const gdr_norm_bwd_args& p, int64_t row, int l, 
   r.rstd = p.rstd[row];
 }
 
-template <typename T, bool CODES, int L, int NV, bool SUMS>
-__global__ __launch_bounds__(threads_of(L)) void norm_bwd_kernel(gdr_norm_bwd_args p, float* part) {
+// weight of the columns from c0 on (1 without weights), 0 behind the row's end
+template <int N>
+__device__ inline void load_weight(const gdr_norm_bwd_args& p, int c0, float (&w)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; k += 4) {
+    const int n = p.D - c0 - k;
+    const raw4 r = p.weight ? Run<float>::load(p.weight + c0 + k, n) : raw4{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[k + i] = p.weight ? Run<float>::get(r, i) : n > i ? 1.f : 0.f;
+  }
+}
+
+template <typename T, bool CODES, int TH, int L, int NV, bool SUMS, bool AHEAD>
+__global__ __launch_bounds__(TH) void norm_bwd_kernel(gdr_norm_bwd_args p, float* part) {
   constexpr int N = Run<T>::N;
-  constexpr int kThreads = threads_of(L), kPer = kThreads / L;
+  constexpr int kPer = TH / L;
+  constexpr bool kHold = NV * N <= 16;   // weights stay in registers
+  constexpr int kJoin = SUMS && L < TH ? TH / (L < 64 ? 64 : L) : 1;   // sets of sums that meet in LDS
+  __shared__ RowSums<TH, 2> sums;
+  __shared__ float join[kJoin][kJoin > 1 ? L * N : 1];
+  int turn = 0;
   const int l = threadIdx.x % L, D = p.D;
   const int64_t step = (int64_t)gridDim.x * kPer;
-  float sw[SUMS ? NV : 1][N], sb[SUMS ? NV : 1][N];
+  float sw[SUMS ? NV : 1][N], sb[SUMS ? NV : 1][N], w[kHold ? NV : 1][N];
   if constexpr (SUMS) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int k = 0; k < N; ++k) sw[j][k] = sb[j][k] = 0.f;
   }
-  int64_t row = (int64_t)blockIdx.x * kPer + threadIdx.x / L;
+  if constexpr (kHold) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_weight<N>(p, (j * L + l) * N, w[j]);
+  }
   BwdRow<T, CODES, NV> r;
+  int64_t row = (int64_t)blockIdx.x * kPer + threadIdx.x / L;
   if (row < p.R) load_row<T, CODES, L, NV>(p, row, l, r);
-  for (; row < p.R; row += step) {
-    // the next row is on its way while this one is worked on
+  // the workgroup's threads make the same number of rounds: they meet in row_sum
+  for (int64_t first = (int64_t)blockIdx.x * kPer; first < p.R; first += step, row += step) {
+    const bool here = row < p.R;
     BwdRow<T, CODES, NV> next;
-    if (row + step < p.R) load_row<T, CODES, L, NV>(p, row + step, l, next);
-    float xh[NV][N], s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c0 = (j * L + l) * N, n = D - c0;
-      if constexpr (CODES) {
-        Codes<N>::unpack(r.c[j], xh[j]);
-        const float sc = chan::scale_of(r.e[j]);
-#pragma unroll
-        for (int k = 0; k < N; ++k) xh[j][k] = (xh[j][k] * sc - r.mean) * r.rstd;
-      } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) xh[j][k] = (Run<T>::get(r.x[j], k) - r.mean) * r.rstd;
-      }
-#pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        const raw4 rw = p.weight ? Run<float>::load(p.weight + c0 + k, n - k) : raw4{};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float dy = Run<T>::get(r.y[j], k + i);   // 0 behind the row's end
-          const float g = dy * (p.weight ? Run<float>::get(rw, i) : 1.f);
-          s[0] += g;
-          s[1] = fmaf(g, n > k + i ? xh[j][k + i] : 0.f, s[1]);
-        }
-      }
+    if constexpr (AHEAD) {
+      if (row + step < p.R) load_row<T, CODES, L, NV>(p, row + step, l, next);
+    } else {
+      if (first != (int64_t)blockIdx.x * kPer && here) load_row<T, CODES, L, NV>(p, row, l, r);
     }
-    row_sum<L, 2>(s);
-    s[0] /= D;
-    s[1] /= D;
+    float s[2] = {0.f, 0.f};
+    if (here) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c0 = (j * L + l) * N, n = D - c0;
-      float o[N];
+      for (int j = 0; j < NV; ++j) {
+        float x[N];
+        r.get_x(j, x);
+        if constexpr (!kHold) load_weight<N>(p, (j * L + l) * N, w[0]);
 #pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        const raw4 rw = p.weight ? Run<float>::load(p.weight + c0 + k, n - k) : raw4{};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float dy = Run<T>::get(r.y[j], k + i);
-          const float g = dy * (p.weight ? Run<float>::get(rw, i) : 1.f);
-          o[k + i] = r.rstd * (g - s[0] - xh[j][k + i] * s[1]);
+        for (int k = 0; k < N; ++k) {
+          // behind the row's end grad_y and the weight read as 0
+          const float dy = Run<T>::get(r.y[j], k), g = dy * w[kHold ? j : 0][k];
+          const float xh = (x[k] - r.mean) * r.rstd;
+          s[0] += g;
+          s[1] = fmaf(g, xh, s[1]);
           if constexpr (SUMS) {
-            sw[j][k + i] = fmaf(dy, xh[j][k + i], sw[j][k + i]);
-            sb[j][k + i] += dy;
+            sw[j][k] = fmaf(dy, xh, sw[j][k]);
+            sb[j][k] += dy;
           }
         }
       }
-      Run<T>::store((T*)p.grad_x + (size_t)row * D + c0, n, o);
     }
-    r = next;
-  }
-  if constexpr (SUMS) {
-    float* pw = part + (size_t)blockIdx.x * 2 * D;
-    if constexpr (L >= kThreads) {
+    row_sum<TH, L>(s, sums, turn);
+    s[0] /= D;
+    s[1] /= D;
+    if (here) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c0 = (j * L + l) * N;
+        float x[N], o[N];
+        r.get_x(j, x);
+        if constexpr (!kHold) load_weight<N>(p, c0, w[0]);
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          if (c0 + k < D) {
-            pw[c0 + k] = sw[j][k];
-            pw[D + c0 + k] = sb[j][k];
-          }
-      }
-    } else {
-      // lane groups, then waves
-      __shared__ float join[kThreads / 64][2][(L < 64 ? L : 64) * N];
-      const int w = threadIdx.x >> 6;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-#pragma unroll
-          for (int off = L; off < 64; off <<= 1) {
-            sw[j][k] += __shfl_xor(sw[j][k], off);
-            sb[j][k] += __shfl_xor(sb[j][k], off);
-          }
-        __syncthreads();
-        if ((threadIdx.x & 63) < L) {
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            join[w][0][l * N + k] = sw[j][k];
-            join[w][1][l * N + k] = sb[j][k];
-          }
+        for (int k = 0; k < N; ++k) {
+          const float xh = (x[k] - r.mean) * r.rstd;
+          o[k] = r.rstd * (fmaf(Run<T>::get(r.y[j], k), w[kHold ? j : 0][k], -s[0]) - xh * s[1]);
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * L * N; i += kThreads) {
-          const int which = i / (L * N), c = i % (L * N);
-          float t = 0.f;
+        Run<T>::store((T*)p.grad_x + (size_t)row * D + c0, D - c0, o);
+      }
+    }
+    if constexpr (AHEAD) r = next;
+  }
+  if constexpr (SUMS) {
+    float* pw = part + (size_t)blockIdx.x * 2 * D;
 #pragma unroll
-          for (int q = 0; q < kThreads / 64; ++q) t += join[q][which][c];
-          if (j * L * N + c < D) pw[(size_t)which * D + j * L * N + c] = t;
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        float* out = pw + (size_t)which * D;
+        float t[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          t[k] = which == 0 ? sw[j][k] : sb[j][k];
+#pragma unroll
+          for (int off = L; off < 64; off <<= 1) t[k] += __shfl_xor(t[k], off);
+        }
+        if constexpr (kJoin == 1) {
+          Run<float>::store(out + (j * L + l) * N, D - (j * L + l) * N, *(const float(*)[4]) & t[0]);
+          if constexpr (N == 8)
+            Run<float>::store(out + (j * L + l) * N + 4, D - (j * L + l) * N - 4, *(const float(*)[4]) & t[4]);
+        } else {
+          const int set = threadIdx.x / (L < 64 ? 64 : L);
+          if (L >= 64 || (threadIdx.x & 63) < L) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) join[set][l * N + k] = t[k];
+          }
+          __syncthreads();
+          for (int c = threadIdx.x; c < L * N; c += TH) {
+            float u = 0.f;
+#pragma unroll
+            for (int q = 0; q < kJoin; ++q) u += join[q][c];
+            if (j * L * N + c < D) out[j * L * N + c] = u;
+          }
+          __syncthreads();
         }
       }
     }
@@ -293,24 +311,25 @@ __global__ __launch_bounds__(256) void norm_cols_kernel(gdr_norm_bwd_args p, flo
   pw[p.D + c] = sb;
 }
 
-// grad_weight and grad_bias from the partial rows: 16 threads a column take every
-// 16th, then join.
-__global__ __launch_bounds__(512) void join_kernel(const float* part, int rows, int D, float* gw, float* gb) {
-  __shared__ float s[16][32];
-  const int l = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + l;   // of 2 D: the weight's columns, then the bias'
+// grad_weight and grad_bias from the partial rows: 64 threads a column take every
+// 64th, then join.
+__global__ __launch_bounds__(1024) void join_kernel(const float* part, int rows, int D, float* gw, float* gb) {
+  __shared__ float s[64][17];
+  const int l = threadIdx.x & 15, y = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + l;   // of 2 D: the weight's columns, then the bias'
   float t = 0.f;
   if (c < 2 * D)
-    for (int r = y; r < rows; r += 16) t += part[(size_t)r * 2 * D + c];
+    for (int r = y; r < rows; r += 64) t += part[(size_t)r * 2 * D + c];
   s[y][l] = t;
   __syncthreads();
-  if (y == 0 && c < 2 * D) {
-#pragma unroll
-    for (int k = 1; k < 16; ++k) t += s[k][l];
-    if (c < D) {
-      if (gw) gw[c] = t;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;   // a wave joins a column
+  t = chan::lane_sum<64>(s[lane][w]);
+  const int cw = blockIdx.x * 16 + w;
+  if (lane == 0 && cw < 2 * D) {
+    if (cw < D) {
+      if (gw) gw[cw] = t;
     } else if (gb) {
-      gb[c - D] = t;
+      gb[cw - D] = t;
     }
   }
 }
@@ -319,7 +338,7 @@ __global__ __launch_bounds__(512) void join_kernel(const float* part, int rows, 
 struct Shape {
   int L, NV;
 };
-constexpr Shape shape_of(int runs) {
+constexpr Shape fwd_shape(int runs) {
   if (runs <= 8) return {8, 1};
   if (runs <= 16) return {16, 1};
   if (runs <= 32) return {32, 1};
@@ -327,33 +346,44 @@ constexpr Shape shape_of(int runs) {
   if (runs <= 2048) return {256, runs <= 512 ? 2 : runs <= 768 ? 3 : runs <= 1024 ? 4 : runs <= 1280 ? 5 : runs <= 1536 ? 6 : 8};
   return {1024, runs <= 4096 ? 4 : runs <= 8192 ? 8 : 16};
 }
+constexpr Shape bwd_shape(int runs) {
+  if (runs <= 8) return {8, 1};
+  if (runs <= 16) return {16, 1};
+  if (runs <= 32) return {32, 1};
+  if (runs <= 64) return {64, 1};
+  if (runs <= 128) return {128, 1};
+  if (runs <= 2048)
+    return {256, runs <= 256 ? 1 : runs <= 512 ? 2 : runs <= 768 ? 3 : runs <= 1024 ? 4 : runs <= 1280 ? 5 : runs <= 1536 ? 6 : 8};
+  return {1024, runs <= 4096 ? 4 : runs <= 8192 ? 8 : 16};
+}
+// Threads of a backward workgroup, of N values a run.
+constexpr int bwd_threads(int L, int NV, int N) {
+  return L == 1024 || NV * N <= 8 ? 1024 : NV * N <= 24 ? 512 : 256;
+}
 inline int runs_of(int D, int io_dtype) { const int n = io_dtype == GDR_BF16 ? 8 : 4; return (D + n - 1) / n; }
-inline int64_t rows_per_group(int L) { return threads_of(L) / L; }
 
 // Workgroups of a forward launch (a grid holds 2^32 threads); they take further rows in turn.
 constexpr int64_t kMaxGroups = 1 << 20;
 
-// Partial rows of the columns' sums: enough workgroups to fill the card, no more
-// than there are rows for.
+// Workgroups of a backward launch, and partial rows of the columns' sums.
 constexpr int kParts = 512;
-inline int parts_of(int64_t R, int L) {
-  const int64_t n = (R + rows_per_group(L) - 1) / rows_per_group(L);
-  return (int)(n < kParts ? n : kParts);
-}
 
 size_t bwd_workspace(int64_t R, int D) {
   (void)R;
   return (size_t)kParts * 2 * D * sizeof(float);
 }
 
-#define GDR_NORM_SHAPES(X)                                                                                      \
-  X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(64, 2) X(64, 3) X(64, 4) X(256, 2) X(256, 3) X(256, 4) X(256, 5) X(256, 6) \
-  X(256, 8) X(1024, 4) X(1024, 8) X(1024, 16)
+#define GDR_NORM_SHAPES(X)                                                                                   \
+  X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(256, 2) X(256, 3) X(256, 4) X(256, 5) X(256, 6) X(256, 8) X(1024, 4) \
+  X(1024, 8) X(1024, 16)
+#define GDR_NORM_FWD_SHAPES(X) X(64, 2) X(64, 3) X(64, 4)
+#define GDR_NORM_BWD_SHAPES(X) X(128, 1) X(256, 1)
 
 template <typename T>
 static hipError_t fwd(const gdr_norm_args& a, hipStream_t s) {
-  const Shape sh = shape_of(runs_of(a.D, a.io_dtype));
-  const int64_t groups = (a.R + rows_per_group(sh.L) - 1) / rows_per_group(sh.L);
+  const Shape sh = fwd_shape(runs_of(a.D, a.io_dtype));
+  const int per = threads_of(sh.L) / sh.L;
+  const int64_t groups = (a.R + per - 1) / per;
   const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
 #define GDR_LAUNCH(LL, NN)                                                                                            \
   if (sh.L == LL && sh.NV == NN) {                                                                                    \
@@ -364,30 +394,37 @@ static hipError_t fwd(const gdr_norm_args& a, hipStream_t s) {
     }                                                                                                                 \
   }
   GDR_NORM_SHAPES(GDR_LAUNCH)
+  GDR_NORM_FWD_SHAPES(GDR_LAUNCH)
 #undef GDR_LAUNCH
   return hipErrorInvalidValue;
 }
 
 template <typename T, bool CODES>
 static hipError_t bwd(const gdr_norm_bwd_args& a, hipStream_t s) {
-  const Shape sh = shape_of(runs_of(a.D, a.io_dtype));
+  constexpr int N = Run<T>::N;
+  const Shape sh = bwd_shape(runs_of(a.D, a.io_dtype));
+  const int per = bwd_threads(sh.L, sh.NV, N) / sh.L;
+  const int64_t groups = (a.R + per - 1) / per;
+  const int parts = (int)(groups < kParts ? groups : kParts);
   const bool sums = a.grad_weight || a.grad_bias;
-  const int parts = parts_of(a.R, sh.L);
-  float* part = (float*)a.workspace;
   const bool beside = sh.L <= 256;   // the sums fit beside the row
+  float* part = (float*)a.workspace;
   bool launched = false;
-#define GDR_LAUNCH(LL, NN)                                                                                           \
-  if (sh.L == LL && sh.NV == NN) {                                                                                   \
-    if constexpr (LL * NN * Run<T>::N <= 65536) {                                                                    \
-      if constexpr (LL <= 256) {                                                                                     \
-        if (sums) hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, LL, NN, true>), dim3(parts), dim3(256), 0, s, a, part); \
-      }                                                                                                              \
-      if (!sums || !beside)                                                                                          \
-        hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, LL, NN, false>), dim3(parts), dim3(threads_of(LL)), 0, s, a, part); \
-      launched = true;                                                                                               \
-    }                                                                                                                \
+#define GDR_LAUNCH(LL, NN)                                                                                            \
+  if (sh.L == LL && sh.NV == NN) {                                                                                    \
+    if constexpr (LL * NN * N <= 65536) {                                                                             \
+      constexpr int TH = bwd_threads(LL, NN, N);                                                                      \
+      if constexpr (LL <= 256) {                                                                                      \
+        if (sums)                                                                                                     \
+          hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, TH, LL, NN, true, true>), dim3(parts), dim3(TH), 0, s, a, part); \
+      }                                                                                                               \
+      if (!sums || !beside)                                                                                           \
+        hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, TH, LL, NN, false, LL <= 256>), dim3(parts), dim3(TH), 0, s, a, part); \
+      launched = true;                                                                                                \
+    }                                                                                                                 \
   }
   GDR_NORM_SHAPES(GDR_LAUNCH)
+  GDR_NORM_BWD_SHAPES(GDR_LAUNCH)
 #undef GDR_LAUNCH
   if (!launched) return hipErrorInvalidValue;
   if (sums) {
@@ -396,7 +433,7 @@ static hipError_t bwd(const gdr_norm_bwd_args& a, hipStream_t s) {
       rows = a.R < kParts ? (int)a.R : kParts;
       hipLaunchKernelGGL((norm_cols_kernel<T, CODES>), dim3((a.D + 255) / 256, rows), dim3(256), 0, s, a, part);
     }
-    hipLaunchKernelGGL(join_kernel, dim3((2 * a.D + 31) / 32), dim3(512), 0, s, part, rows, a.D, a.grad_weight, a.grad_bias);
+    hipLaunchKernelGGL(join_kernel, dim3((2 * a.D + 15) / 16), dim3(1024), 0, s, part, rows, a.D, a.grad_weight, a.grad_bias);
   }
   return hipGetLastError();
 }
