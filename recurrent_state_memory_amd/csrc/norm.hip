@@ -119,8 +119,7 @@ __global__ __launch_bounds__(threads_of(L)) void norm_fwd_kernel(gdr_norm_args p
 // Backward.  A workgroup of TH threads takes TH / L rows at a time, every
 // (gridDim TH / L)-th; a thread keeps its columns' sums in registers (SUMS).  Groups
 // are joined over the wave and the workgroup, in a fixed order, and a workgroup
-// leaves one partial row of each sum for join_kernel.  AHEAD: the next row is asked
-// for before this one is worked on.
+// leaves one partial row of each sum for join_kernel.
 template <typename T, bool CODES, int NV>
 struct BwdRow {
   static constexpr int N = Run<T>::N;
@@ -175,7 +174,7 @@ __device__ inline void load_weight(const gdr_norm_bwd_args& p, int c0, float (&w
   }
 }
 
-template <typename T, bool CODES, int TH, int L, int NV, bool SUMS, bool AHEAD>
+template <typename T, bool CODES, int TH, int L, int NV, bool SUMS>
 __global__ __launch_bounds__(TH) void norm_bwd_kernel(gdr_norm_bwd_args p, float* part) {
   constexpr int N = Run<T>::N;
   constexpr int kPer = TH / L;
@@ -204,11 +203,7 @@ __global__ __launch_bounds__(TH) void norm_bwd_kernel(gdr_norm_bwd_args p, float
   for (int64_t first = (int64_t)blockIdx.x * kPer; first < p.R; first += step, row += step) {
     const bool here = row < p.R;
     BwdRow<T, CODES, NV> next;
-    if constexpr (AHEAD) {
-      if (row + step < p.R) load_row<T, CODES, L, NV>(p, row + step, l, next);
-    } else {
-      if (first != (int64_t)blockIdx.x * kPer && here) load_row<T, CODES, L, NV>(p, row, l, r);
-    }
+    if (row + step < p.R) load_row<T, CODES, L, NV>(p, row + step, l, next);   // on its way meanwhile
     float s[2] = {0.f, 0.f};
     if (here) {
 #pragma unroll
@@ -248,7 +243,7 @@ __global__ __launch_bounds__(TH) void norm_bwd_kernel(gdr_norm_bwd_args p, float
         Run<T>::store((T*)p.grad_x + (size_t)row * D + c0, D - c0, o);
       }
     }
-    if constexpr (AHEAD) r = next;
+    r = next;
   }
   if constexpr (SUMS) {
     float* pw = part + (size_t)blockIdx.x * 2 * D;
@@ -283,6 +278,46 @@ __global__ __launch_bounds__(TH) void norm_bwd_kernel(gdr_norm_bwd_args p, float
           }
           __syncthreads();
         }
+      }
+    }
+  }
+}
+
+// Rows of more than 2048 runs: a workgroup a row, read twice (the second time mostly
+// from the caches), as registers would not hold it beside what it needs.
+template <typename T, bool CODES>
+__global__ __launch_bounds__(1024) void norm_bwd_long_kernel(gdr_norm_bwd_args p) {
+  constexpr int N = Run<T>::N;
+  __shared__ RowSums<1024, 2> sums;
+  int turn = 0;
+  const int D = p.D, runs = (D + N - 1) / N;
+  for (int64_t row = blockIdx.x; row < p.R; row += gridDim.x) {
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int j = threadIdx.x; j < runs; j += 1024) {
+        BwdRow<T, CODES, 1> r;
+        load_row<T, CODES, 0, 1>(p, row, j, r);   // run j alone
+        float x[N], w[N], o[N];
+        r.get_x(0, x);
+        load_weight<N>(p, j * N, w);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float g = Run<T>::get(r.y[0], k) * w[k], xh = (x[k] - mean) * rstd;
+          if (pass == 0) {
+            s[0] += g;
+            s[1] = fmaf(g, xh, s[1]);
+          } else {
+            o[k] = rstd * ((g - s[0]) - xh * s[1]);
+          }
+        }
+        if (pass == 1) Run<T>::store((T*)p.grad_x + (size_t)row * D + j * N, D - j * N, o);
+      }
+      if (pass == 0) {
+        row_sum<1024, 1024>(s, sums, turn);
+        s[0] /= D;
+        s[1] /= D;
       }
     }
   }
@@ -354,29 +389,26 @@ constexpr Shape bwd_shape(int runs) {
   if (runs <= 128) return {128, 1};
   if (runs <= 2048)
     return {256, runs <= 256 ? 1 : runs <= 512 ? 2 : runs <= 768 ? 3 : runs <= 1024 ? 4 : runs <= 1280 ? 5 : runs <= 1536 ? 6 : 8};
-  return {1024, runs <= 4096 ? 4 : runs <= 8192 ? 8 : 16};
+  return {1024, 0};   // norm_bwd_long_kernel
 }
 // Threads of a backward workgroup, of N values a run.
-constexpr int bwd_threads(int L, int NV, int N) {
-  return L == 1024 || NV * N <= 8 ? 1024 : NV * N <= 24 ? 512 : 256;
-}
+constexpr int bwd_threads(int L, int NV, int N) { return NV * N <= 8 ? 1024 : NV * N <= 24 ? 512 : 256; }
 inline int runs_of(int D, int io_dtype) { const int n = io_dtype == GDR_BF16 ? 8 : 4; return (D + n - 1) / n; }
 
 // Workgroups of a forward launch (a grid holds 2^32 threads); they take further rows in turn.
 constexpr int64_t kMaxGroups = 1 << 20;
 
 // Workgroups of a backward launch, and partial rows of the columns' sums.
-constexpr int kParts = 512;
+constexpr int kParts = 256;
 
 size_t bwd_workspace(int64_t R, int D) {
   (void)R;
   return (size_t)kParts * 2 * D * sizeof(float);
 }
 
-#define GDR_NORM_SHAPES(X)                                                                                   \
-  X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(256, 2) X(256, 3) X(256, 4) X(256, 5) X(256, 6) X(256, 8) X(1024, 4) \
-  X(1024, 8) X(1024, 16)
-#define GDR_NORM_FWD_SHAPES(X) X(64, 2) X(64, 3) X(64, 4)
+#define GDR_NORM_SHAPES(X) \
+  X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(256, 2) X(256, 3) X(256, 4) X(256, 5) X(256, 6) X(256, 8)
+#define GDR_NORM_FWD_SHAPES(X) X(64, 2) X(64, 3) X(64, 4) X(1024, 4) X(1024, 8) X(1024, 16)
 #define GDR_NORM_BWD_SHAPES(X) X(128, 1) X(256, 1)
 
 template <typename T>
@@ -385,56 +417,55 @@ static hipError_t fwd(const gdr_norm_args& a, hipStream_t s) {
   const int per = threads_of(sh.L) / sh.L;
   const int64_t groups = (a.R + per - 1) / per;
   const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
-#define GDR_LAUNCH(LL, NN)                                                                                            \
-  if (sh.L == LL && sh.NV == NN) {                                                                                    \
-    if constexpr (LL * NN * Run<T>::N <= 65536) {                                                                     \
-      if (a.x_code) hipLaunchKernelGGL((norm_fwd_kernel<T, LL, NN, true>), grid, dim3(threads_of(LL)), 0, s, a);      \
-      else hipLaunchKernelGGL((norm_fwd_kernel<T, LL, NN, false>), grid, dim3(threads_of(LL)), 0, s, a);              \
-      return hipGetLastError();                                                                                       \
-    }                                                                                                                 \
+#define GDR_LAUNCH(LL, NN)                                                                                       \
+  if (sh.L == LL && sh.NV == NN) {                                                                               \
+    if constexpr (LL * NN * Run<T>::N <= 65536) {                                                                \
+      if constexpr (LL <= 256) {                                                                                 \
+        if (a.x_code) {                                                                                          \
+          hipLaunchKernelGGL((norm_fwd_kernel<T, LL, NN, true>), grid, dim3(threads_of(LL)), 0, s, a);           \
+          return hipGetLastError();                                                                              \
+        }                                                                                                        \
+      }                                                                                                          \
+      hipLaunchKernelGGL((norm_fwd_kernel<T, LL, NN, false>), grid, dim3(threads_of(LL)), 0, s, a);              \
+    }                                                                                                            \
   }
   GDR_NORM_SHAPES(GDR_LAUNCH)
   GDR_NORM_FWD_SHAPES(GDR_LAUNCH)
 #undef GDR_LAUNCH
-  return hipErrorInvalidValue;
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.x_code) return e;
+  // rows of more than 2048 runs: no registers are left to pack beside them
+  const gdr_ckpt8_pack_args c{a.R, a.D, a.io_dtype, a.x, a.x_code, a.x_exp};
+  return ckpt8::launch_pack(c, s);
 }
 
 template <typename T, bool CODES>
 static hipError_t bwd(const gdr_norm_bwd_args& a, hipStream_t s) {
   constexpr int N = Run<T>::N;
   const Shape sh = bwd_shape(runs_of(a.D, a.io_dtype));
-  const int per = bwd_threads(sh.L, sh.NV, N) / sh.L;
-  const int64_t groups = (a.R + per - 1) / per;
-  const int parts = (int)(groups < kParts ? groups : kParts);
   const bool sums = a.grad_weight || a.grad_bias;
-  const bool beside = sh.L <= 256;   // the sums fit beside the row
   float* part = (float*)a.workspace;
-  bool launched = false;
-#define GDR_LAUNCH(LL, NN)                                                                                            \
-  if (sh.L == LL && sh.NV == NN) {                                                                                    \
-    if constexpr (LL * NN * N <= 65536) {                                                                             \
-      constexpr int TH = bwd_threads(LL, NN, N);                                                                      \
-      if constexpr (LL <= 256) {                                                                                      \
-        if (sums)                                                                                                     \
-          hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, TH, LL, NN, true, true>), dim3(parts), dim3(TH), 0, s, a, part); \
-      }                                                                                                               \
-      if (!sums || !beside)                                                                                           \
-        hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, TH, LL, NN, false, LL <= 256>), dim3(parts), dim3(TH), 0, s, a, part); \
-      launched = true;                                                                                                \
-    }                                                                                                                 \
+  int parts = (int)(a.R < kParts ? a.R : kParts);
+  if (sh.NV == 0) {
+    hipLaunchKernelGGL((norm_bwd_long_kernel<T, CODES>), dim3(parts), dim3(1024), 0, s, a);
+    if (sums) hipLaunchKernelGGL((norm_cols_kernel<T, CODES>), dim3((a.D + 255) / 256, parts), dim3(256), 0, s, a, part);
+  } else {
+    const int per = bwd_threads(sh.L, sh.NV, N) / sh.L;
+    const int64_t groups = (a.R + per - 1) / per;
+    if (groups < parts) parts = (int)groups;
+#define GDR_LAUNCH(LL, NN)                                                                                           \
+  if (sh.L == LL && sh.NV == NN) {                                                                                   \
+    constexpr int TH = bwd_threads(LL, NN, N);                                                                       \
+    if (sums) hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, TH, LL, NN, true>), dim3(parts), dim3(TH), 0, s, a, part); \
+    else hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, TH, LL, NN, false>), dim3(parts), dim3(TH), 0, s, a, part);   \
   }
-  GDR_NORM_SHAPES(GDR_LAUNCH)
-  GDR_NORM_BWD_SHAPES(GDR_LAUNCH)
+    GDR_NORM_SHAPES(GDR_LAUNCH)
+    GDR_NORM_BWD_SHAPES(GDR_LAUNCH)
 #undef GDR_LAUNCH
-  if (!launched) return hipErrorInvalidValue;
-  if (sums) {
-    int rows = parts;
-    if (!beside) {
-      rows = a.R < kParts ? (int)a.R : kParts;
-      hipLaunchKernelGGL((norm_cols_kernel<T, CODES>), dim3((a.D + 255) / 256, rows), dim3(256), 0, s, a, part);
-    }
-    hipLaunchKernelGGL(join_kernel, dim3((2 * a.D + 15) / 16), dim3(1024), 0, s, part, rows, a.D, a.grad_weight, a.grad_bias);
   }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !sums) return e;
+  hipLaunchKernelGGL(join_kernel, dim3((2 * a.D + 15) / 16), dim3(1024), 0, s, part, parts, a.D, a.grad_weight, a.grad_bias);
   return hipGetLastError();
 }
 
