@@ -128,7 +128,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   }
   float Pe[V], He[V];
   join_groups<true>(P, H, Pe, He, q.grp);
-  if (q.grp == kGroups - 1) {
+  if (q.grp == 0) {
 #pragma unroll
     for (int k = 0; k < V; ++k) j.run[q.wave][q.cl + k] = float2{P[k], H[k]};
   }

@@ -185,32 +185,34 @@ __device__ inline Place take_place(int C, int nchain, int nct, int nt, int team_
   return q;
 }
 
-// Join (P, H) over the wave's lane groups, earlier tokens in lower groups (UP)
-// or in higher ones: on return P, H cover the thread's run and all before it,
-// Pe, He all before it.
-template <bool UP>
-__device__ inline float from_group(float x, int dist) {
-  return UP ? __shfl_up(x, dist * kSide) : __shfl_down(x, dist * kSide);
+// (P, H) of one run after another.
+__device__ inline float2 after(float2 later, float2 earlier) {
+  return float2{later.x * earlier.x, fmaf(later.x, earlier.y, later.y)};
 }
+// Join (P, H) over the wave's four lane groups, which are its rows of 16 lanes,
+// earlier tokens in lower rows (UP) or in higher ones: on return P, H cover the
+// whole wave, Pe, He all before the thread's run.  The lane swaps (VALU, no LDS)
+// give every row the values of its pair's even and odd row, and every half those of
+// both halves.
 template <bool UP>
 __device__ inline void join_groups(float (&P)[V], float (&H)[V], float (&Pe)[V], float (&He)[V], int grp) {
-  const int pos = UP ? grp : kGroups - 1 - grp;   // place in the order of joining
-#pragma unroll
-  for (int dist = 1; dist < kGroups; dist *= 2) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const float p = from_group<UP>(P[k], dist), h = from_group<UP>(H[k], dist);
-      if (pos >= dist) {
-        H[k] = fmaf(P[k], h, H[k]);
-        P[k] *= p;
-      }
-    }
-  }
+  const bool second = (grp & 1) == (UP ? 1 : 0), behind = (grp >> 1) == (UP ? 1 : 0);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const float p = from_group<UP>(P[k], 1), h = from_group<UP>(H[k], 1);
-    Pe[k] = pos > 0 ? p : 1.f;
-    He[k] = pos > 0 ? h : 0.f;
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(P[k]), __float_as_uint(P[k]), false, false);
+    const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(H[k]), __float_as_uint(H[k]), false, false);
+    const float2 even = {__uint_as_float(p[0]), __uint_as_float(h[0])}, odd = {__uint_as_float(p[1]), __uint_as_float(h[1])};
+    const float2 a = UP ? even : odd, pair = after(UP ? odd : even, a);
+    const auto pp = __builtin_amdgcn_permlane32_swap(__float_as_uint(pair.x), __float_as_uint(pair.x), false, false);
+    const auto hh = __builtin_amdgcn_permlane32_swap(__float_as_uint(pair.y), __float_as_uint(pair.y), false, false);
+    const float2 low = {__uint_as_float(pp[0]), __uint_as_float(hh[0])}, high = {__uint_as_float(pp[1]), __uint_as_float(hh[1])};
+    const float2 b = UP ? low : high, all = after(UP ? high : low, b);
+    float2 ex = second ? a : float2{1.f, 0.f};
+    if (behind) ex = after(ex, b);
+    P[k] = all.x;
+    H[k] = all.y;
+    Pe[k] = ex.x;
+    He[k] = ex.y;
   }
 }
 
@@ -297,10 +299,7 @@ __device__ inline float join_tiles(Joins<NW>& j, const Chains& ch, const Place& 
     if (q.wave == 0 && r < kSuper - 1 && q.tt + 1 < nt) {
       float2 m = {1.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float2 a = j.run[w][lane];
-        m = float2{m.x * a.x, fmaf(a.x, m.y, a.y)};
-      }
+      for (int w = 0; w < NW; ++w) m = after(j.run[w][lane], m);
       put_map(words.tile, m);
     }
 #pragma unroll
@@ -314,16 +313,10 @@ __device__ inline float join_tiles(Joins<NW>& j, const Chains& ch, const Place& 
     float2 before = {1.f, 0.f}, own = {1.f, 0.f};
 #pragma unroll
     for (int k = 0; k < kSuper - 1; ++k)
-      if (k < r) {
-        const float2 a = j.pre[k][lane];
-        before = float2{before.x * a.x, fmaf(a.x, before.y, a.y)};
-      }
+      if (k < r) before = after(j.pre[k][lane], before);
 #pragma unroll
     for (int w = 0; w < NW; ++w)
-      if (w < q.nw) {
-        const float2 a = j.run[w][lane];
-        own = float2{own.x * a.x, fmaf(a.x, own.y, a.y)};
-      }
+      if (w < q.nw) own = after(j.run[w][lane], own);
     const float in = su > 0 ? get_state(words.super, words.state) : first;
     const float h = fmaf(before.x, in, before.y);
     last = fmaf(own.x, h, own.y);
