@@ -6,9 +6,9 @@
 // tile to tile with the last tiles first.  G_t = grad_y_t + K_{t+1}, so a run of
 // tokens takes K to P K + Q with P the same product of decays.
 //
-// A thread keeps a, b and the softplus of its 32 elements in registers and the two
-// sigmoids in LDS (its own 16 bytes a token, no barrier), so that they are evaluated
-// once; 1 / (1 - a^2) is (s / b)^2.
+// A thread keeps a, b and the softplus of its 32 elements in registers, and
+// sigmoid(decay_x) and 1 / n, n = sqrt(1 - a^2), in LDS (its own 16 bytes a token, no
+// barrier), so that everything is evaluated once; b = s n gives back s = b / n.
 //
 // grad_decay_a sums over all tokens: registers, lane groups, waves (one LDS pass
 // in a fixed order), then one partial row per tile that sum_kernel adds up, again
@@ -21,8 +21,9 @@
 namespace gdr {
 namespace scan {
 
-// Below this, sqrt(1 - a^2) counts as 0: the term it divides vanishes with it.
-constexpr float kLeastB = 0x1p-60f;
+// Below this, 1 - a^2 counts as 0, and so does the term that it divides, which
+// vanishes with its root.
+constexpr float kLeastM = 0x1p-120f;
 
 struct BwdP {
   int B, T, C, normalise;
@@ -46,10 +47,11 @@ struct BwdP {
 };
 
 template <typename T, typename X, int KIND, bool NORM, bool VEC>
-__global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
+__global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   constexpr bool kCodes = !__is_same(X, T);
   __shared__ Joins<kBwdWaves> j;   // of the maps of K: later tokens first
-  __shared__ f32x4 kept[KIND == 0 ? 1 : KIND][KIND == 0 ? 1 : S][KIND == 0 ? 1 : 64 * kBwdWaves];   // sigmoid(decay_x), sigmoid(gate_x)
+  constexpr int kKept = (KIND != 0 ? 1 : 0) + (NORM ? 1 : 0);   // sigmoid(decay_x), 1 / sqrt(1 - a^2)
+  __shared__ f32x4 kept[kKept == 0 ? 1 : kKept][kKept == 0 ? 1 : S][kKept == 0 ? 1 : 64 * kBwdWaves];
   const Place q = take_place(p.C, p.nchain, p.nct, p.nt, p.team, p.ch.ticket);
   const int tile = p.nt - 1 - q.tt;         // the last tokens come first
   const int C = p.C, t0 = tile * kBwdWaves * GDR_SCAN_BLOCK;
@@ -134,7 +136,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
   }
 #pragma unroll
   for (int i = 0; i < S; ++i) {
-    f32x4 kd, kg;
+    f32x4 kd, kn;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       if constexpr (KIND == 0) {
@@ -145,15 +147,16 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
         sp[i][k] = softplus(Four<T>::get(rd[i], k), sig);
         kd[k] = sig;
         a[i][k] = decay(A, sp[i][k]);
-        if constexpr (KIND == 2) kg[k] = b[i][k] = sigmoid(Four<T>::get(rg[i], k));
-        if constexpr (NORM) {
-          const float n = __builtin_amdgcn_sqrtf(one_minus_sq(A, sp[i][k], a[i][k]));
-          b[i][k] = KIND == 2 ? b[i][k] * n : n;
+        if constexpr (KIND == 2) b[i][k] = sigmoid(Four<T>::get(rg[i], k));
+        if constexpr (NORM) {   // 1 / n, and n = m / n
+          const float m = one_minus_sq(A, sp[i][k], a[i][k]);
+          kn[k] = m > kLeastM ? __builtin_amdgcn_rsqf(m) : 0.f;
+          b[i][k] = KIND == 2 ? b[i][k] * (m * kn[k]) : m * kn[k];
         }
       }
     }
     if constexpr (KIND != 0) kept[0][i][threadIdx.x] = kd;
-    if constexpr (KIND == 2) kept[1][i][threadIdx.x] = kg;
+    if constexpr (NORM) kept[1][i][threadIdx.x] = kn;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       P[k] *= a[i][k];
@@ -235,9 +238,9 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
 #pragma unroll
   for (int i = (half + 1) * HS - 1; i >= half * HS; --i) {
     float ox_[V], od[V], og[V];
-    f32x4 kd, kg;
+    f32x4 kd, kn;
     if constexpr (KIND != 0) kd = kept[0][i][threadIdx.x];
-    if constexpr (KIND == 2) kg = kept[1][i][threadIdx.x];
+    if constexpr (NORM) kn = kept[1][i][threadIdx.x];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const float G = Four<T>::get(ry[i], k) + K[k];
@@ -247,16 +250,16 @@ __global__ __launch_bounds__(64 * kBwdWaves) void scan_bwd_kernel(BwdP p) {
         ox_[k] = G;
         od[k] = G * prev[i - half * HS][k];
       } else {
-        float in = -prev[i - half * HS][k], sg = 1.f;
+        float in = -prev[i - half * HS][k];
+        const float x = x_at(i, k);
         ox_[k] = G;
         if constexpr (KIND == 2 || NORM) ox_[k] *= b[i][k];
         if constexpr (KIND == 2) {
-          sg = kg[k];
-          og[k] = G * v_at(i, k) * (1.f - sg);
-        }
-        if constexpr (NORM) {   // v a / m = x a s^2 / b
-          const float t = x_at(i, k) * ak * __builtin_amdgcn_rcpf(b[i][k]);
-          in += b[i][k] > kLeastB * sg ? (KIND == 2 ? t * sg * sg : t) : 0.f;
+          const float sg = NORM ? b[i][k] * kn[k] : b[i][k];
+          og[k] = ox_[k] * x * (1.f - sg);
+          if constexpr (NORM) in = fmaf(x * sg, ak * kn[k], in);   // v a / m = x s a / n
+        } else if constexpr (NORM) {
+          in = fmaf(x, ak * kn[k], in);
         }
         const float du = K[k] * in;
         sum[k] = fmaf(du, sp[i][k], sum[k]);
