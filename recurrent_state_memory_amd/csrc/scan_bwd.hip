@@ -58,16 +58,15 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);
   const int r0 = q.wave * GDR_SCAN_BLOCK + q.grp * S;
   const size_t base = ((size_t)q.b * p.T + t0) * C;
-  const int e0 = r0 * C + q.c;
-  const int ox = q.nv > 0 ? e0 * size_of<X> : kNoLane, ot = q.nv > 0 ? e0 * size_of<T> : kNoLane;
-  const int oa = q.nv > 0 ? e0 * 4 : kNoLane;
-  const uint32_t tbytes = rows * C * size_of<T>;
+  const auto view = [&](auto t, const void* array) {
+    return View<decltype(t), VEC>(array, base, rows, C, r0, q.c, q.nv);
+  };
 
   // a wait for a load waits for those before it too: what is needed first comes
   // first, and row by row
   float scale[V];
   if constexpr (KIND != 0) {
-    const Four<float>::R r = Four<float>::template load<VEC>(buffer(p.decay_a, C * 4), q.nv > 0 ? q.c * 4 : kNoLane, q.nv);
+    const Four<float>::R r = View<float, VEC>(p.decay_a, 0, 1, C, 0, q.c, q.nv).load(0);
 #pragma unroll
     for (int k = 0; k < V; ++k) scale[k] = Four<float>::get(r, k);
   }
@@ -78,17 +77,15 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   typename Four<T>::R rd[KIND == 0 ? 1 : S], rg[KIND == 2 ? S : 1];
   float xs[kCodes ? S : 1];
   {
-    const rsrc_t bx = buffer((const char*)p.x + base * size_of<X>, rows * C * size_of<X>);
-    const rsrc_t by = buffer((const T*)p.grad_y + base, tbytes);
-    const rsrc_t ba = buffer(KIND == 0 ? (const char*)(p.alpha + base) : (const char*)((const T*)p.decay_x + base),
-                             KIND == 0 ? rows * C * 4 : tbytes);
-    const rsrc_t bg = buffer(KIND == 2 ? (const T*)p.gate_x + base : nullptr, KIND == 2 ? tbytes : 0);
+    const auto vx = view(X{}, p.x);
+    const auto va = view(float{}, p.alpha);
+    const auto vd = view(T{}, p.decay_x), vg = view(T{}, p.gate_x);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      if constexpr (KIND == 0) ra[i] = Four<float>::template load<VEC>(ba, oa + i * C * 4, q.nv);
-      else rd[i] = Four<T>::template load<VEC>(ba, ot + i * C * size_of<T>, q.nv);
-      rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
-      if constexpr (KIND == 2) rg[i] = Four<T>::template load<VEC>(bg, ot + i * C * size_of<T>, q.nv);
+      if constexpr (KIND == 0) ra[i] = va.load(i);
+      else rd[i] = vd.load(i);
+      rx[i] = vx.load(i);
+      if constexpr (KIND == 2) rg[i] = vg.load(i);
     }
     if constexpr (kCodes) {
       const int ng = (C + 127) / 128;
@@ -98,13 +95,13 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
       for (int i = 0; i < S; ++i)
         xs[i] = chan::scale_of(__builtin_amdgcn_raw_buffer_load_b8(be, oe + i * ng, 0, 0));
     }
+    const auto vy = view(T{}, p.grad_y);
 #pragma unroll
-    for (int i = 0; i < S; ++i) ry[i] = Four<T>::template load<VEC>(by, ot + i * C * size_of<T>, q.nv);
+    for (int i = 0; i < S; ++i) ry[i] = vy.load(i);
   }
   const size_t nb = blocks_of(p.T), block = (size_t)tile * kBwdWaves + q.wave;
-  const Four<float>::R rh = Four<float>::template load<VEC>(
-      buffer(p.ckpt + ((size_t)q.b * nb + (block < nb ? block : 0)) * C, block < nb ? C * 4 : 0),
-      q.nv > 0 ? q.c * 4 : kNoLane, q.nv);
+  const Four<float>::R rh =
+      View<float, VEC>(p.ckpt, ((size_t)q.b * nb + (block < nb ? block : 0)) * C, block < nb ? 1 : 0, C, 0, q.c, q.nv).load(0);
   const int cc = q.c0 + q.lane;
   const int pos = q.nw - 1 - q.wave;        // the wave's place in the order of joining
   const Words<kBwdWaves> words = look_ahead<kBwdWaves>(p.ch, q, p.nt, pos);
@@ -205,9 +202,9 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   float K[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) K[k] = fmaf(Pb[k], j.from[pos][q.cl + k], Qb[k]);
-  const rsrc_t gx = buffer((const T*)p.grad_x + base, tbytes);
-  const rsrc_t gd = KIND == 0 ? buffer(p.grad_alpha + base, rows * C * 4) : buffer((const T*)p.grad_decay_x + base, tbytes);
-  const rsrc_t gg = KIND == 2 ? buffer((const T*)p.grad_gate_x + base, tbytes) : gx;
+  const auto gx = view(T{}, p.grad_x);
+  const auto ga = view(float{}, p.grad_alpha);
+  const auto gd = view(T{}, p.grad_decay_x), gg = view(T{}, p.grad_gate_x);
   float sum[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) sum[k] = 0.f;
@@ -266,10 +263,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
         od[k] = du * scale[k] * kd[k];
       }
     }
-    Four<T>::template store<VEC>(gx, ot + i * C * size_of<T>, q.nv, ox_);
-    if constexpr (KIND == 0) Four<float>::template store<VEC>(gd, oa + i * C * 4, q.nv, od);
-    else Four<T>::template store<VEC>(gd, ot + i * C * size_of<T>, q.nv, od);
-    if constexpr (KIND == 2) Four<T>::template store<VEC>(gg, ot + i * C * size_of<T>, q.nv, og);
+    gx.store(i, ox_);
+    if constexpr (KIND == 0) ga.store(i, od);
+    else gd.store(i, od);
+    if constexpr (KIND == 2) gg.store(i, og);
   }
   }
   if constexpr (KIND != 0) {
@@ -308,15 +305,13 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float* part, float* out
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Room of the hand-over words, first the recomputed forward's, then the backward's.
-static size_t chains_room(int B, int T, int C) {
-  const size_t f = chain_bytes(B, T, C, kFwdWaves), b = chain_bytes(B, T, C, kBwdWaves);
-  return align256(f > b ? f : b);
-}
+// The hand-over words of the recomputed forward, if there is one, then the
+// backward's, its states and its partial sums.
+static size_t recomputed_bytes(int B, int T, int C, bool ckpt) { return ckpt ? 0 : chain_bytes(B, T, C, kFwdWaves); }
 
 size_t bwd_workspace(int B, int T, int C, bool gated, bool ckpt) {
-  return chains_room(B, T, C) + (ckpt ? 0 : align256((size_t)B * blocks_of(T) * C * 4)) +
-         (gated ? align256(tiles_t(T, kBwdWaves) * B * C * 4) : 0);
+  return recomputed_bytes(B, T, C, ckpt) + chain_bytes(B, T, C, kBwdWaves) +
+         (ckpt ? 0 : align256((size_t)B * blocks_of(T) * C * 4)) + (gated ? align256(tiles_t(T, kBwdWaves) * B * C * 4) : 0);
 }
 
 template <typename T, typename X, int KIND, bool NORM>
@@ -337,19 +332,21 @@ static hipError_t launch_kind(const BwdP& p, bool vec, hipStream_t s) {
 
 hipError_t launch_scan_bwd(const gdr_scan_bwd_args& a, hipStream_t s) {
   char* ws = (char*)a.workspace;
-  char* rest = ws + chains_room(a.B, a.T, a.C);
+  const size_t first = recomputed_bytes(a.B, a.T, a.C, a.ckpt != nullptr), words = first + chain_bytes(a.B, a.T, a.C, kBwdWaves);
+  char* rest = ws + words;
+  hipError_t e = clear_chains(ws, words, s);
+  if (e != hipSuccess) return e;
   const float* ckpt = a.ckpt;
   if (!ckpt) {
-    const hipError_t e = launch_ckpt(a, (float*)rest, ws, s);
+    e = launch_ckpt(a, (float*)rest, ws, s);
     if (e != hipSuccess) return e;
     ckpt = (const float*)rest;
     rest += align256((size_t)a.B * blocks_of(a.T) * a.C * 4);
   }
   BwdP p{a.B, a.T, a.C, a.normalise, (int)chains_of(a.B, a.C), (a.C + kTileC - 1) / kTileC, (int)tiles_t(a.T, kBwdWaves),
          team_of(a.alpha != nullptr, a.io_dtype), a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, ckpt, a.grad_y, a.grad_h, a.grad_x, a.grad_alpha,
-         a.grad_decay_x, a.grad_gate_x, a.grad_h0, a.alpha ? nullptr : (float*)rest, {}};
-  hipError_t e = reset_chains(ws, a.B, a.T, a.C, kBwdWaves, &p.ch, s);
-  if (e != hipSuccess) return e;
+         a.grad_decay_x, a.grad_gate_x, a.grad_h0, a.alpha ? nullptr : (float*)rest,
+         chains_at(ws + first, a.B, a.T, a.C, kBwdWaves)};
   const size_t io = a.io_dtype == GDR_BF16 ? 2 : 4;
   const bool vec = a.C % 4 == 0 && vec4_ok(a.x, a.x_exp ? 1 : io) && vec4_ok(a.alpha, 4) && vec4_ok(a.decay_x, io) &&
                    vec4_ok(a.gate_x, io) && vec4_ok(a.grad_y, io) && vec4_ok(a.grad_x, io) && vec4_ok(a.grad_alpha, 4) &&

@@ -39,13 +39,12 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);   // of the tile that exist
   const int r0 = q.wave * GDR_SCAN_BLOCK + q.grp * S;      // the thread's first row
   const size_t base = ((size_t)q.b * p.T + t0) * C;
-  const int e0 = r0 * C + q.c;                             // its first element from base
 
   // a wait for a load waits for those before it too: what is needed first comes
   // first, and row by row
   Scale A[V];
   if constexpr (KIND != 0) {
-    const Four<float>::R r = Four<float>::template load<VEC>(buffer(p.decay_a, C * 4), q.nv > 0 ? q.c * 4 : kNoLane, q.nv);
+    const Four<float>::R r = View<float, VEC>(p.decay_a, 0, 1, C, 0, q.c, q.nv).load(0);
 #pragma unroll
     for (int k = 0; k < V; ++k) A[k] = Scale(Four<float>::get(r, k));
   }
@@ -54,18 +53,18 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   typename Four<T>::R rd[KIND == 0 ? 1 : S], rg[KIND == 2 ? S : 1];
   float xs[kCodes ? S : 1];
   {
-    const rsrc_t bx = buffer((const char*)p.x + base * size_of<X>, rows * C * size_of<X>);
-    const int ox = q.nv > 0 ? e0 * size_of<X> : kNoLane, ot = q.nv > 0 ? e0 * size_of<T> : kNoLane;
-    const rsrc_t ba = buffer(KIND == 0 ? (const char*)(p.alpha + base) : (const char*)((const T*)p.decay_x + base),
-                             rows * C * (KIND == 0 ? 4 : size_of<T>));
-    const rsrc_t bg = buffer(KIND == 2 ? (const T*)p.gate_x + base : nullptr, KIND == 2 ? rows * C * size_of<T> : 0);
-    const int oa = q.nv > 0 ? e0 * 4 : kNoLane;
+    const auto view = [&](auto t, const void* array) {
+      return View<decltype(t), VEC>(array, base, rows, C, r0, q.c, q.nv);
+    };
+    const auto vx = view(X{}, p.x);
+    const auto va = view(float{}, p.alpha);
+    const auto vd = view(T{}, p.decay_x), vg = view(T{}, p.gate_x);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      if constexpr (KIND == 0) ra[i] = Four<float>::template load<VEC>(ba, oa + i * C * 4, q.nv);
-      else rd[i] = Four<T>::template load<VEC>(ba, ot + i * C * size_of<T>, q.nv);
-      rx[i] = Four<X>::template load<VEC>(bx, ox + i * C * size_of<X>, q.nv);
-      if constexpr (KIND == 2) rg[i] = Four<T>::template load<VEC>(bg, ot + i * C * size_of<T>, q.nv);
+      if constexpr (KIND == 0) ra[i] = va.load(i);
+      else rd[i] = vd.load(i);
+      rx[i] = vx.load(i);
+      if constexpr (KIND == 2) rg[i] = vg.load(i);
     }
     if constexpr (kCodes) {   // four neighbouring channels share a group of 128
       const int ng = (C + 127) / 128;
@@ -138,8 +137,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   if (p.ckpt && cc < C && q.wave * GDR_SCAN_BLOCK < rows)
     p.ckpt[((size_t)q.b * blocks_of(p.T) + (size_t)q.tt * kFwdWaves + q.wave) * C + cc] = h_wave;
   if (!p.y) return;   // the states were all that was wanted
-  const rsrc_t by = buffer((const T*)p.y + base, rows * C * size_of<T>);
-  const int oy = q.nv > 0 ? e0 * size_of<T> : kNoLane;
+  const View<T, VEC> vy(p.y, base, rows, C, r0, q.c, q.nv);
   float h[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) h[k] = fmaf(Pe[k], j.from[q.wave][q.cl + k], He[k]);
@@ -147,7 +145,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   for (int i = 0; i < S; ++i) {
 #pragma unroll
     for (int k = 0; k < V; ++k) h[k] = fmaf(a[i][k], h[k], v[i][k]);
-    Four<T>::template store<VEC>(by, oy + i * C * size_of<T>, q.nv, h);
+    vy.store(i, h);
   }
 }
 
@@ -178,33 +176,29 @@ __global__ __launch_bounds__(256) void scan_step_kernel(gdr_scan_step_args p) {
   st((T*)p.y + i, h);
 }
 
-// No word is written yet, and the ticket starts at 0.
-__global__ __launch_bounds__(256) void reset_kernel(uint32_t* ticket, ulonglong2* words, size_t pairs) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i == 0) *ticket = 0u;
-  for (size_t k = i; k < pairs; k += (size_t)gridDim.x * 256) words[k] = ulonglong2{0u, 0u};
+__global__ __launch_bounds__(256) void clear_kernel(ulonglong2* p, size_t n) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = ulonglong2{0u, 0u};
 }
 
-static size_t words_of(int B, int T, int C, int waves) {
-  const size_t nt = tiles_t(T, waves);
-  return chains_of(B, C) * (nt + (nt + kSuper - 1) / kSuper) * kTileC;
-}
-
+// The ticket (in 256 bytes), the tiles' words, the supers'.
 size_t chain_bytes(int B, int T, int C, int waves) {
-  return tiles_t(T, waves) > 1 ? 256 + words_of(B, T, C, waves) * 8 : 0;
+  const size_t nt = tiles_t(T, waves);
+  return nt > 1 ? 256 + chains_of(B, C) * (nt + (nt + kSuper - 1) / kSuper) * kTileC * 8 : 0;
 }
 
 size_t fwd_workspace(int B, int T, int C) { return chain_bytes(B, T, C, kFwdWaves); }
 
-hipError_t reset_chains(void* workspace, int B, int T, int C, int waves, Chains* out, hipStream_t s) {
-  *out = Chains{nullptr, nullptr, nullptr};
-  if (tiles_t(T, waves) <= 1) return hipSuccess;
-  out->ticket = (uint32_t*)workspace;
-  out->tiles = (uint64_t*)((char*)workspace + 256);
-  out->supers = out->tiles + chains_of(B, C) * tiles_t(T, waves) * kTileC;
-  const size_t pairs = words_of(B, T, C, waves) / 2, blocks = (pairs + 255) / 256;
-  hipLaunchKernelGGL(reset_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s, out->ticket,
-                     (ulonglong2*)out->tiles, pairs);
+Chains chains_at(void* workspace, int B, int T, int C, int waves) {
+  if (tiles_t(T, waves) <= 1) return Chains{nullptr, nullptr, nullptr};
+  uint64_t* tiles = (uint64_t*)((char*)workspace + 256);
+  return Chains{(uint32_t*)workspace, tiles, tiles + chains_of(B, C) * tiles_t(T, waves) * kTileC};
+}
+
+hipError_t clear_chains(void* workspace, size_t bytes, hipStream_t s) {
+  if (bytes == 0) return hipSuccess;
+  const size_t n = bytes / 16, blocks = (n + 255) / 256;   // whole rows of 64 words
+  hipLaunchKernelGGL(clear_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s,
+                     (ulonglong2*)workspace, n);
   return hipGetLastError();
 }
 
@@ -229,8 +223,7 @@ static hipError_t launch(FwdP& p, int io_dtype, void* workspace, hipStream_t s) 
   p.nchain = (int)chains_of(p.B, p.C);
   p.nt = (int)tiles_t(p.T, kFwdWaves);
   p.team = team_of(p.alpha != nullptr, io_dtype);
-  const hipError_t e = reset_chains(workspace, p.B, p.T, p.C, kFwdWaves, &p.ch, s);
-  if (e != hipSuccess) return e;
+  p.ch = chains_at(workspace, p.B, p.T, p.C, kFwdWaves);
   const size_t io = io_dtype == GDR_BF16 ? 2 : 4;
   const bool vec = p.C % 4 == 0 && vec4_ok(p.x, p.x_exp ? 1 : io) && vec4_ok(p.alpha, 4) && vec4_ok(p.decay_x, io) &&
                    vec4_ok(p.gate_x, io) && vec4_ok(p.y, io);
@@ -242,7 +235,8 @@ static hipError_t launch(FwdP& p, int io_dtype, void* workspace, hipStream_t s) 
 hipError_t launch_scan_fwd(const gdr_scan_args& a, hipStream_t s) {
   FwdP p{a.B, a.T, a.C, a.normalise, 0, 0, 0, 0, a.x, nullptr, a.alpha, a.decay_x, a.decay_a, a.gate_x, a.h0, a.y, a.h_out,
          a.ckpt, {}};
-  return launch(p, a.io_dtype, a.workspace, s);
+  const hipError_t e = clear_chains(a.workspace, fwd_workspace(a.B, a.T, a.C), s);
+  return e == hipSuccess ? launch(p, a.io_dtype, a.workspace, s) : e;
 }
 
 hipError_t launch_ckpt(const gdr_scan_bwd_args& a, float* ckpt, void* workspace, hipStream_t s) {

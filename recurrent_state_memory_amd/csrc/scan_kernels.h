@@ -44,10 +44,13 @@ struct Chains {
   uint64_t* tiles;     // [chains][tiles][64] each tile's map of the state
   uint64_t* supers;    // [chains][supers][64] the state before each super
 };
-size_t chain_bytes(int B, int T, int C, int waves);
-hipError_t reset_chains(void* workspace, int B, int T, int C, int waves, Chains* out, hipStream_t s);
+size_t chain_bytes(int B, int T, int C, int waves);   // a multiple of 256
+Chains chains_at(void* workspace, int B, int T, int C, int waves);
+// No word written, and the tickets at 0, before the kernels that use them.
+hipError_t clear_chains(void* workspace, size_t bytes, hipStream_t s);
 
-// The forward of the backward's inputs that writes the block-start states alone.
+// The forward of the backward's inputs that writes the block-start states alone (its
+// chains cleared).
 hipError_t launch_ckpt(const gdr_scan_bwd_args& a, float* ckpt, void* workspace, hipStream_t s);
 
 // Whether rows and buffers allow four channels at a time.

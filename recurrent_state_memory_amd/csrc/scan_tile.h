@@ -53,85 +53,118 @@ __device__ inline rsrc_t buffer(const void* base, uint32_t bytes) {
 // rows are at most 2^28 bytes), also after a row offset is added.
 constexpr int kNoLane = 0x40000000;
 
-// Four neighbouring channels of a row: raw registers, and as fp32.  VEC: one
-// access of all four (a row's channels are a multiple of 4: all are there, or none).
-// Else one access each, of the `nv` that are there.
-__device__ inline int at(int off, int k, int nv, int size) { return k < nv ? off + k * size : kNoLane; }
-
 __device__ inline uint32_t bf16_pair(float lo, float hi) {
   typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
   const bf16x2 v = {(__bf16)lo, (__bf16)hi};
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// Four neighbouring channels of a row: raw registers, and as fp32.  `load` and
+// `store` go through a buffer; `from` and `to` take the elements wherever they are
+// (aligned to one of them), `some` of them where a row ends.
 template <typename T>
 struct Four;
 template <>
 struct Four<float> {
   using R = u32x4;
-  template <bool VEC>
-  static __device__ inline R load(rsrc_t b, int off, int nv) {
-    if constexpr (VEC) return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
-    R r;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = __builtin_amdgcn_raw_buffer_load_b32(b, at(off, k, nv, 4), 0, 0);
-    return r;
-  }
+  typedef u32x4 at4 __attribute__((aligned(4), may_alias));
+  static __device__ inline R load(rsrc_t b, int off) { return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0); }
   static __device__ inline float get(const R& r, int k) { return __uint_as_float(r[k]); }
-  template <bool VEC>
-  static __device__ inline void store(rsrc_t b, int off, int nv, const float (&v)[4]) {
-    R r;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = __float_as_uint(v[k]);
-    if constexpr (VEC) {
-      __builtin_amdgcn_raw_buffer_store_b128(r, b, off, 0, 0);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) __builtin_amdgcn_raw_buffer_store_b32(r[k], b, at(off, k, nv, 4), 0, 0);
-    }
+  static __device__ inline R pack(const float (&v)[4]) {
+    return R{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
   }
+  static __device__ inline void store(rsrc_t b, int off, const R& r) { __builtin_amdgcn_raw_buffer_store_b128(r, b, off, 0, 0); }
+  static __device__ inline R from(const char* p) { return *(const at4*)p; }
+  static __device__ inline R some(const char* p, int n) {
+    const uint32_t* e = (const uint32_t*)p;
+    return R{n > 0 ? e[0] : 0u, n > 1 ? e[1] : 0u, n > 2 ? e[2] : 0u, 0u};
+  }
+  static __device__ inline void to(char* p, const R& r) { *(at4*)p = r; }
+  static __device__ inline void to(char* p, const R& r, int k) { ((uint32_t*)p)[k] = r[k]; }
 };
 template <>
 struct Four<__bf16> {
   using R = u32x2;
-  template <bool VEC>
-  static __device__ inline R load(rsrc_t b, int off, int nv) {
-    if constexpr (VEC) return __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0);
-    uint32_t h[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = __builtin_amdgcn_raw_buffer_load_b16(b, at(off, k, nv, 2), 0, 0);
-    return R{h[0] | h[1] << 16, h[2] | h[3] << 16};
-  }
+  typedef u32x2 at2 __attribute__((aligned(2), may_alias));
+  static __device__ inline R load(rsrc_t b, int off) { return __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0); }
   static __device__ inline float get(const R& r, int k) {
     return __uint_as_float(k & 1 ? r[k >> 1] & 0xffff0000u : r[k >> 1] << 16);
   }
-  template <bool VEC>
-  static __device__ inline void store(rsrc_t b, int off, int nv, const float (&v)[4]) {
-    if constexpr (VEC) {
-      typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
-      const bf16x4 h = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(R, h), b, off, 0, 0);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v[k]), b, at(off, k, nv, 2), 0, 0);
-    }
+  static __device__ inline R pack(const float (&v)[4]) { return R{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}; }
+  static __device__ inline void store(rsrc_t b, int off, const R& r) { __builtin_amdgcn_raw_buffer_store_b64(r, b, off, 0, 0); }
+  static __device__ inline R from(const char* p) { return *(const at2*)p; }
+  static __device__ inline R some(const char* p, int n) {
+    const uint16_t* e = (const uint16_t*)p;
+    const uint32_t e0 = n > 0 ? e[0] : 0u, e1 = n > 1 ? e[1] : 0u, e2 = n > 2 ? e[2] : 0u;
+    return R{e0 | e1 << 16, e2};
   }
+  static __device__ inline void to(char* p, const R& r) { *(at2*)p = r; }
+  static __device__ inline void to(char* p, const R& r, int k) { ((uint16_t*)p)[k] = (uint16_t)(r[k >> 1] >> (16 * (k & 1))); }
 };
 template <>
 struct Four<Code8> {
   using R = uint32_t;
-  template <bool VEC>
-  static __device__ inline R load(rsrc_t b, int off, int nv) {
-    if constexpr (VEC) return __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0);
-    R r = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      r |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(b, at(off, k, nv, 1), 0, 0) << (8 * k);
-    return r;
-  }
+  typedef uint32_t at1 __attribute__((aligned(1), may_alias));
+  static __device__ inline R load(rsrc_t b, int off) { return __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0); }
   static __device__ inline float get(const R& r, int k) {
     return k == 0 ? chan::code_f32<0>(r) : k == 1 ? chan::code_f32<1>(r) : k == 2 ? chan::code_f32<2>(r) : chan::code_f32<3>(r);
+  }
+  static __device__ inline R from(const char* p) { return *(const at1*)p; }
+  static __device__ inline R some(const char* p, int n) {
+    const uint8_t* e = (const uint8_t*)p;
+    return (n > 0 ? e[0] : 0u) | (n > 1 ? (uint32_t)e[1] << 8 : 0u) | (n > 2 ? (uint32_t)e[2] << 16 : 0u);
+  }
+};
+
+// A thread's rows of one of the call's arrays, from the tile's first element on.
+// VEC (rows of a multiple of 4 channels, in buffers aligned to 4 elements): through a
+// buffer that ends with the tile's rows.  Else with a test of what exists: four
+// channels at once wherever they lie, one by one at a row's end.  (One access each
+// everywhere took 76 us against 122 for 4 x 2048 x 2047 against 8 x 4096 x 2048.)
+template <typename T, bool VEC>
+struct View {
+  rsrc_t b;
+  int off;
+  char* p;
+  int nv, mine, step;
+  __device__ inline View(const void* array, size_t base, int rows, int C, int r0, int c, int nv_) {
+    step = C * size_of<T>;
+    const int first = r0 * step + c * size_of<T>;
+    char* tile = (char*)const_cast<void*>(array) + base * size_of<T>;
+    if constexpr (VEC) {
+      b = buffer(tile, rows * step);
+      off = nv_ > 0 ? first : kNoLane;
+    } else {
+      p = tile + first;
+      nv = nv_;
+      mine = rows - r0;
+    }
+  }
+  __device__ inline typename Four<T>::R load(int i) const {
+    if constexpr (VEC) {
+      return Four<T>::load(b, off + i * step);
+    } else {
+      typename Four<T>::R r = {};
+      if (i < mine) {
+        if (nv >= 4) r = Four<T>::from(p + i * step);
+        else if (nv > 0) r = Four<T>::some(p + i * step, nv);
+      }
+      return r;
+    }
+  }
+  __device__ inline void store(int i, const float (&v)[4]) const {
+    const typename Four<T>::R r = Four<T>::pack(v);
+    if constexpr (VEC) {
+      Four<T>::store(b, off + i * step, r);
+    } else if (i < mine) {
+      if (nv >= 4) {
+        Four<T>::to(p + i * step, r);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (k < nv) Four<T>::to(p + i * step, r, k);
+      }
+    }
   }
 };
 
