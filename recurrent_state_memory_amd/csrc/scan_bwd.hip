@@ -288,19 +288,18 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   }
 }
 
-// grad_decay_a[c]: 16 threads per channel take every 16th partial row, then join.
+// grad_decay_a[c]: 64 threads per channel take every 64th partial row, then join.
 __global__ __launch_bounds__(1024) void sum_kernel(const float* part, float* out, int rows, int C) {
-  __shared__ float s[16][64];
-  const int l = threadIdx.x & 63, y = threadIdx.x >> 6, c = blockIdx.x * 64 + l;
+  __shared__ float s[64][17];
+  const int l = threadIdx.x & 15, y = threadIdx.x >> 4, c = blockIdx.x * 16 + l;
   float t = 0.f;
   if (c < C)
-    for (int r = y; r < rows; r += 16) t += part[(size_t)r * C + c];
+    for (int r = y; r < rows; r += 64) t += part[(size_t)r * C + c];
   s[y][l] = t;
   __syncthreads();
-  if (y == 0 && c < C) {
-    for (int k = 1; k < 16; ++k) t += s[k][l];
-    out[c] = t;
-  }
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;   // a wave joins a channel
+  t = chan::lane_sum<64>(s[lane][w]);
+  if (lane == 0 && blockIdx.x * 16 + w < C) out[blockIdx.x * 16 + w] = t;
 }
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -356,7 +355,7 @@ hipError_t launch_scan_bwd(const gdr_scan_bwd_args& a, hipStream_t s) {
   else
     e = a.x_exp ? launch_kind<float, Code8>(p, vec, s) : launch_kind<float, float>(p, vec, s);
   if (e != hipSuccess || a.alpha) return e;
-  hipLaunchKernelGGL(sum_kernel, dim3((a.C + 63) / 64), dim3(1024), 0, s, p.part, a.grad_decay_a, p.nt * a.B, a.C);
+  hipLaunchKernelGGL(sum_kernel, dim3((a.C + 15) / 16), dim3(1024), 0, s, p.part, a.grad_decay_a, p.nt * a.B, a.C);
   return hipGetLastError();
 }
 
