@@ -70,7 +70,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
 #pragma unroll
     for (int k = 0; k < V; ++k) scale[k] = Four<float>::get(r, k);
   }
-  using XR = std::conditional_t<kCodes, __bf16, X>;   // codes become bf16, which holds their values
+  using XR = std::conditional_t<kCodes, __bf16, X>;   // codes become bf16, which holds their values (to 2^-133)
   typename Four<X>::R rx[S];
   typename Four<T>::R ry[S];
   Four<float>::R ra[KIND == 0 ? S : 1];
@@ -160,19 +160,16 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
       H[k] = fmaf(a[i][k], H[k], v_at(i, k));
     }
   }
-  // behind the last token the state stays: x and grad_y read as 0 there, and a
-  // softplus of 0 keeps the row out of grad_decay_a
-  if (rows < q.nw * GDR_SCAN_BLOCK) {
+  // behind the last token the state stays: x and grad_y read as 0 there
+  const bool ragged = rows < q.nw * GDR_SCAN_BLOCK;
+  if (ragged) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       P[k] = 1.f;
       H[k] = 0.f;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        if (r0 + i >= rows) {
-          a[i][k] = 1.f;
-          if constexpr (KIND != 0) sp[i][k] = 0.f;
-        }
+        if (r0 + i >= rows) a[i][k] = 1.f;
         P[k] *= a[i][k];
         H[k] = fmaf(a[i][k], H[k], v_at(i, k));
       }
@@ -258,7 +255,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
         } else if constexpr (NORM) {
           in = fmaf(x, ak * kn[k], in);
         }
-        const float du = K[k] * in;
+        float du = K[k] * in;
+        if (ragged && r0 + i >= rows) du = 0.f;   // no part of grad_decay_a, also where the state is NaN
         sum[k] = fmaf(du, sp[i][k], sum[k]);
         od[k] = du * scale[k] * kd[k];
       }

@@ -166,9 +166,9 @@ __device__ inline void coefficients(const float* alpha, const void* decay_x, con
 
 template <typename T>
 __global__ __launch_bounds__(256) void scan_step_kernel(gdr_scan_step_args p) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (size_t)p.N * p.C) return;
-  const float A = p.alpha ? 0.f : p.decay_a[i % p.C];
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;   // N C < 2^31
+  if (i >= (uint32_t)(p.N * p.C)) return;
+  const float A = p.alpha ? 0.f : p.decay_a[i % (uint32_t)p.C];
   float a, v;
   coefficients<T>(p.alpha, p.decay_x, p.gate_x, A, p.normalise, i, ld((const T*)p.x + i), a, v);
   const float h = fmaf(a, p.h[i], v);

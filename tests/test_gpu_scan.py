@@ -247,6 +247,18 @@ def test_scan_nan_stays_in_its_channel():
     assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("T", [100, 130])
+def test_scan_nan_in_the_last_token(T):
+    """A NaN that reaches the state with the last token alone leaves every gradient
+    that does not read it finite (the tile's rows behind T included)."""
+    import torch
+    d = scan_inputs((1, T), 64, "f32", "decay", seed=T)
+    clean = call_bwd(d, "f32", h0=dev(d["h"]), grad_h=dev(d["dh"]))
+    d["x"][0, T - 1, 7] = np.nan
+    g = call_bwd(d, "f32", h0=dev(d["h"]), grad_h=dev(d["dh"]))
+    assert all(torch.equal(g[k], clean[k]) for k in clean)
+
+
 def test_scan_writes_only_its_outputs():
     """Outputs inside larger buffers: the bytes around them stay as they were; the
     results are the same at every alignment."""
