@@ -22,10 +22,13 @@ Entry points (same names as the C ABI):
 * ``gdr_norm_fwd``, ``gdr_norm_bwd`` -- layer norm (include/gdr_norm.h)
 * ``gdr_ckpt8_pack``, ``gdr_ckpt8_unpack`` -- activations kept in 8 bits for the
   backward (include/gdr_ckpt8.h)
+
+The channelwise operators (the last three lines) run on the device of their
+tensors, on its current stream or on ``stream``, and allocate what they return
+and their workspaces on that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -768,24 +771,24 @@ def _opt(t, name, shape, dtype, dev):
     return None if t is None else _in(t, name, shape, dtype, dev)
 
 
-_NULL_CONTEXT = contextlib.nullcontext()
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call on ``dev`` has to leave the current device or stream."""
+    import torch
+    return stream is not None or dev.type != "cuda" or dev.index != torch._C._cuda_getDevice()
 
 
-def _on(dev, stream):
-    """Context in which a call on ``dev`` allocates and launches: the current
-    stream of ``dev``, or ``stream``, which must belong to it.  Outputs and
-    workspaces are allocated inside, so that the allocator ties them to the
-    stream that uses them."""
+def _there(dev, stream):
+    """Context of a call that has to: ``stream``, which must belong to ``dev``, or the
+    current stream of ``dev``.  Outputs and workspaces are allocated inside, so that the
+    allocator ties them to the stream that uses them."""
     import torch
     if dev.type != "cuda":
         raise ValueError("gdr: tensors must live on the GPU")
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"gdr: stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
+    if stream is None:
         return torch.cuda.device(dev)
-    return _NULL_CONTEXT
+    if stream.device != dev:
+        raise ValueError(f"gdr: stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
 def _launch(entry, args, dev):
@@ -831,20 +834,23 @@ def _scan_fwd(x, alpha, decay_x, decay_a, gate_x, normalise, h0, y, h_out, ckpt,
         a.normalise = int(bool(normalise))
     a.h0 = _opt(h0, "h0", (B, C), f32, dev)
     lib = load_library()
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty_like(x)
-        if h_out is None and return_state:
-            h_out = torch.empty((B, C), dtype=f32, device=dev)
-        cshape = (B, -(-T // GDR_SCAN_BLOCK), C)
-        if ckpt is None and return_ckpt:
-            ckpt = torch.empty(cshape, dtype=f32, device=dev)
-        a.y = _in(y, "y", shape, io, dev)
-        a.h_out = _opt(h_out, "h_out", (B, C), f32, dev)
-        a.ckpt = _opt(ckpt, "ckpt", cshape, f32, dev)
-        a.workspace, a.workspace_bytes, keep = _workspace(
-            lib.gdr_scan_fwd_workspace(ctypes.byref(a)), workspace, dev)
-        _launch(lib.gdr_scan_fwd, a, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return _scan_fwd(x, alpha, decay_x, decay_a, gate_x, normalise, h0, y, h_out, ckpt, return_state, return_ckpt,
+                             workspace, None)
+    if y is None:
+        y = torch.empty_like(x)
+    if h_out is None and return_state:
+        h_out = torch.empty((B, C), dtype=f32, device=dev)
+    cshape = (B, -(-T // GDR_SCAN_BLOCK), C)
+    if ckpt is None and return_ckpt:
+        ckpt = torch.empty(cshape, dtype=f32, device=dev)
+    a.y = _in(y, "y", shape, io, dev)
+    a.h_out = _opt(h_out, "h_out", (B, C), f32, dev)
+    a.ckpt = _opt(ckpt, "ckpt", cshape, f32, dev)
+    a.workspace, a.workspace_bytes, keep = _workspace(
+        lib.gdr_scan_fwd_workspace(ctypes.byref(a)), workspace, dev)
+    _launch(lib.gdr_scan_fwd, a, dev)
     return y, h_out, ckpt
 
 
@@ -908,25 +914,28 @@ def _scan_bwd(x, alpha, decay_x, decay_a, gate_x, normalise, grad_y, h0, grad_h,
     a.grad_h = _opt(grad_h, "grad_h", (B, C), f32, dev)
     lib = load_library()
     g = {}
-    with _on(dev, stream):
-        g["x"] = torch.empty(shape, dtype=io, device=dev)
-        a.grad_x = g["x"].data_ptr()
-        if alpha is not None:
-            g["alpha"] = torch.empty(shape, dtype=f32, device=dev)
-            a.grad_alpha = g["alpha"].data_ptr()
-        else:
-            g["decay_x"] = torch.empty(shape, dtype=io, device=dev)
-            g["decay_a"] = torch.empty((C,), dtype=f32, device=dev)
-            a.grad_decay_x, a.grad_decay_a = g["decay_x"].data_ptr(), g["decay_a"].data_ptr()
-            if gate_x is not None:
-                g["gate_x"] = torch.empty(shape, dtype=io, device=dev)
-                a.grad_gate_x = g["gate_x"].data_ptr()
-        if need_grad_h0:
-            g["h0"] = torch.empty((B, C), dtype=f32, device=dev)
-            a.grad_h0 = g["h0"].data_ptr()
-        a.workspace, a.workspace_bytes, keep = _workspace(
-            lib.gdr_scan_bwd_workspace(ctypes.byref(a)), workspace, dev)
-        _launch(lib.gdr_scan_bwd, a, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return _scan_bwd(x, alpha, decay_x, decay_a, gate_x, normalise, grad_y, h0, grad_h, ckpt, need_grad_h0,
+                             workspace, None)
+    g["x"] = torch.empty(shape, dtype=io, device=dev)
+    a.grad_x = g["x"].data_ptr()
+    if alpha is not None:
+        g["alpha"] = torch.empty(shape, dtype=f32, device=dev)
+        a.grad_alpha = g["alpha"].data_ptr()
+    else:
+        g["decay_x"] = torch.empty(shape, dtype=io, device=dev)
+        g["decay_a"] = torch.empty((C,), dtype=f32, device=dev)
+        a.grad_decay_x, a.grad_decay_a = g["decay_x"].data_ptr(), g["decay_a"].data_ptr()
+        if gate_x is not None:
+            g["gate_x"] = torch.empty(shape, dtype=io, device=dev)
+            a.grad_gate_x = g["gate_x"].data_ptr()
+    if need_grad_h0:
+        g["h0"] = torch.empty((B, C), dtype=f32, device=dev)
+        a.grad_h0 = g["h0"].data_ptr()
+    a.workspace, a.workspace_bytes, keep = _workspace(
+        lib.gdr_scan_bwd_workspace(ctypes.byref(a)), workspace, dev)
+    _launch(lib.gdr_scan_bwd, a, dev)
     return g
 
 
@@ -974,11 +983,16 @@ def _scan_step(h, x, alpha, decay_x, decay_a, gate_x, normalise, h_out, y, strea
     else:
         gates = (None, _in(decay_x, "decay_x", shape, io, dev), _in(decay_a, "decay_a", (C,), f32, dev),
                  _opt(gate_x, "gate_x", shape, io, dev))
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty_like(x)
-        a = ScanStepArgs(N, C, code_io, int(bool(normalise)), xp, *gates, hp, ho, _in(y, "y", shape, io, dev))
-        _launch(load_library().gdr_scan_step, a, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return _scan_step(h, x, alpha, decay_x, decay_a, gate_x, normalise, h_out, y, None)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _in(y, "y", shape, io, dev)
+    a = ScanStepArgs(N, C, code_io, int(bool(normalise)), xp, *gates, hp, ho, yp)
+    _launch(load_library().gdr_scan_step, a, dev)
     return y
 
 
@@ -1000,12 +1014,14 @@ def gdr_scan_step_gated(h, x, decay_x, decay_a, *, gate_x=None, normalise=True, 
     return _scan_step(h, x, None, decay_x, decay_a, gate_x, normalise, h_out, y, stream)
 
 
-def gdr_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, return_ckpt8=False, stream=None):
+def gdr_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, return_stats=True, return_ckpt8=False,
+                 stream=None):
     """Layer norm over the last dimension (see ``gdr_norm_fwd`` in include/gdr_norm.h).
 
     x [...,D] bf16 or fp32; weight, bias fp32 [D] or None.  Returns (y like x,
-    mean, rstd, ckpt8): the statistics fp32 [...], and with ``return_ckpt8`` the
-    8-bit copy of x for the backward (the tuple of ``gdr_ckpt8_pack``), else None.
+    mean, rstd, ckpt8): the statistics fp32 [...] (None without ``return_stats``),
+    and with ``return_ckpt8`` the 8-bit copy of x for the backward (the tuple of
+    ``gdr_ckpt8_pack``), else None.
     """
     import torch
     if x.dim() < 1:
@@ -1016,19 +1032,26 @@ def gdr_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, y=None, return_ckpt8=Fa
     xp = _in(x, "x", shape, io, dev)
     wp = _opt(weight, "weight", (D,), f32, dev)
     bp = _opt(bias, "bias", (D,), f32, dev)
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty_like(x)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_norm_fwd(x, weight, bias, eps=eps, y=y, return_stats=return_stats, return_ckpt8=return_ckpt8)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
         yp = _in(y, "y", shape, io, dev)
+    mean = rstd = mp = rp = None
+    if return_stats:
         mean = torch.empty(lead, dtype=f32, device=dev)
         rstd = torch.empty(lead, dtype=f32, device=dev)
-        code, kept = (None, None), None
-        if return_ckpt8:
-            kept = (torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev),
-                    torch.empty((*lead, -(-D // GDR_CKPT8_GROUP)), dtype=torch.uint8, device=dev))
-            code = kept[0].data_ptr(), kept[1].data_ptr()
-        a = NormArgs(R, D, code_io, eps, 0, xp, wp, bp, yp, mean.data_ptr(), rstd.data_ptr(), *code)
-        _launch(load_library().gdr_norm_fwd, a, dev)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    code, kept = (None, None), None
+    if return_ckpt8:
+        kept = (torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev),
+                torch.empty((*lead, -(-D // GDR_CKPT8_GROUP)), dtype=torch.uint8, device=dev))
+        code = kept[0].data_ptr(), kept[1].data_ptr()
+    a = NormArgs(R, D, code_io, eps, 0, xp, wp, bp, yp, mp, rp, *code)
+    _launch(load_library().gdr_norm_fwd, a, dev)
     return y, mean, rstd, kept
 
 
@@ -1056,18 +1079,21 @@ def gdr_norm_bwd(grad_y, x, mean, rstd, weight=None, *, need_grad_weight=True, n
     a.grad_y = _in(grad_y, "grad_y", shape, io, dev)
     lib = load_library()
     g = {}
-    with _on(dev, stream):
-        g["x"] = torch.empty(shape, dtype=io, device=dev)
-        a.grad_x = g["x"].data_ptr()
-        if need_grad_weight:
-            g["weight"] = torch.empty((D,), dtype=f32, device=dev)
-            a.grad_weight = g["weight"].data_ptr()
-        if need_grad_bias:
-            g["bias"] = torch.empty((D,), dtype=f32, device=dev)
-            a.grad_bias = g["bias"].data_ptr()
-        a.workspace, a.workspace_bytes, keep = _workspace(
-            lib.gdr_norm_bwd_workspace(ctypes.byref(a)), workspace, dev)
-        _launch(lib.gdr_norm_bwd, a, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_norm_bwd(grad_y, x, mean, rstd, weight, need_grad_weight=need_grad_weight,
+                                need_grad_bias=need_grad_bias, workspace=workspace)
+    g["x"] = torch.empty(shape, dtype=io, device=dev)
+    a.grad_x = g["x"].data_ptr()
+    if need_grad_weight:
+        g["weight"] = torch.empty((D,), dtype=f32, device=dev)
+        a.grad_weight = g["weight"].data_ptr()
+    if need_grad_bias:
+        g["bias"] = torch.empty((D,), dtype=f32, device=dev)
+        a.grad_bias = g["bias"].data_ptr()
+    a.workspace, a.workspace_bytes, keep = _workspace(
+        lib.gdr_norm_bwd_workspace(ctypes.byref(a)), workspace, dev)
+    _launch(lib.gdr_norm_bwd, a, dev)
     return g
 
 
@@ -1082,11 +1108,13 @@ def gdr_ckpt8_pack(x, *, stream=None):
     lead, D = shape[:-1], shape[-1]
     code_io = _io(x)
     xp = _in(x, "x", shape, x.dtype, dev)
-    with _on(dev, stream):
-        code = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
-        exp = torch.empty((*lead, -(-D // GDR_CKPT8_GROUP)), dtype=torch.uint8, device=dev)
-        a = Ckpt8PackArgs(math.prod(lead), D, code_io, xp, code.data_ptr(), exp.data_ptr())
-        _launch(load_library().gdr_ckpt8_pack, a, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_ckpt8_pack(x)
+    code = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    exp = torch.empty((*lead, -(-D // GDR_CKPT8_GROUP)), dtype=torch.uint8, device=dev)
+    a = Ckpt8PackArgs(math.prod(lead), D, code_io, xp, code.data_ptr(), exp.data_ptr())
+    _launch(load_library().gdr_ckpt8_pack, a, dev)
     return code, exp
 
 
@@ -1102,9 +1130,14 @@ def gdr_ckpt8_unpack(code, exp, *, dtype=None, x=None, stream=None):
         dtype = torch.bfloat16 if x is None else x.dtype
     cp = _in(code, "code", shape, torch.float8_e4m3fn, dev)
     ep = _in(exp, "exp", (*lead, -(-D // GDR_CKPT8_GROUP)), torch.uint8, dev)
-    with _on(dev, stream):
-        if x is None:
-            x = torch.empty(shape, dtype=dtype, device=dev)
-        a = Ckpt8UnpackArgs(math.prod(lead), D, _io(x), cp, ep, _in(x, "x", shape, dtype, dev))
-        _launch(load_library().gdr_ckpt8_unpack, a, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_ckpt8_unpack(code, exp, dtype=dtype, x=x)
+    if x is None:
+        x = torch.empty(shape, dtype=dtype, device=dev)
+        xp = x.data_ptr()
+    else:
+        xp = _in(x, "x", shape, dtype, dev)
+    a = Ckpt8UnpackArgs(math.prod(lead), D, _io(x), cp, ep, xp)
+    _launch(load_library().gdr_ckpt8_unpack, a, dev)
     return x

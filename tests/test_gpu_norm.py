@@ -135,6 +135,8 @@ def test_norm_leading_dimensions_and_alignment():
     ref = gdr.gdr_norm_fwd(dev(d["x"], "bf16"), dev(d["w"]), dev(d["b"]))
     y, m, r, _ = gdr.gdr_norm_fwd(dev(d["x"], "bf16").view(2, 3, 4, 256), dev(d["w"]), dev(d["b"]))
     assert y.shape == (2, 3, 4, 256) and m.shape == (2, 3, 4) and torch.equal(y.view(24, 256), ref[0])
+    y1, none, none2, _ = gdr.gdr_norm_fwd(dev(d["x"], "bf16"), dev(d["w"]), dev(d["b"]), return_stats=False)
+    assert none is None and none2 is None and torch.equal(y1, ref[0])
     g = gdr.gdr_norm_bwd(dev(d["dy"], "bf16").view(2, 3, 4, 256), dev(d["x"], "bf16").view(2, 3, 4, 256), m, r,
                          dev(d["w"]))
     assert g["x"].shape == (2, 3, 4, 256) and g["weight"].shape == (256,)
@@ -162,6 +164,25 @@ def test_norm_of_the_delta_rules_heads():
     yr, mr, rr = norm.forward(on)
     ty, _, _ = norm_bounds(on.reshape(-1, 128), None, mr.ravel(), rr.ravel(), 1e-5, yr.reshape(-1, 128), "bf16")
     check("heads y", y, yr, ty.reshape(yr.shape))
+
+
+def test_norm_other_stream_and_given_workspace():
+    """A call on a side stream, with a workspace that held something else before."""
+    import torch
+    import recurrent_state_memory_amd as gdr
+    d = inputs(600, 130, "f32", 50)
+    x, dy, w = dev(d["x"]), dev(d["dy"]), dev(d["w"])
+    _, m, r, _ = gdr.gdr_norm_fwd(x, w)
+    ref = gdr.gdr_norm_bwd(dy, x, m, r, w)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    y2, m2, r2, _ = gdr.gdr_norm_fwd(x, w, stream=side)
+    got = gdr.gdr_norm_bwd(dy, x, m2, r2, w, workspace=ws, stream=side)
+    side.synchronize()
+    assert all(torch.equal(ref[k], got[k]) for k in ref)
+    with pytest.raises(ValueError, match="workspace"):
+        gdr.gdr_norm_bwd(dy, x, m, r, w, workspace=ws[:100])
 
 
 def test_norm_graph_and_repeat():

@@ -292,6 +292,43 @@ def test_scan_repeats_bit_for_bit():
         assert all(torch.equal(fb[k], ab[k]) for k in fb)
 
 
+def test_scan_given_workspaces():
+    """Workspaces that held something else before, used again by a smaller and a larger call."""
+    import torch
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    for T, C in ((1000, 130), (300, 64), (3000, 260)):
+        d = scan_inputs((2, T), C, "bf16", "gate+norm", seed=T)
+        ref, rg = call_fwd(d, "bf16", h0=dev(d["h"])), call_bwd(d, "bf16", h0=dev(d["h"]))
+        got = call_fwd(d, "bf16", h0=dev(d["h"]), workspace=ws)
+        gg = call_bwd(d, "bf16", h0=dev(d["h"]), workspace=ws)
+        assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+        assert all(torch.equal(rg[k], gg[k]) for k in rg)
+    with pytest.raises(ValueError, match="workspace"):
+        call_fwd(d, "bf16", workspace=ws[:64])
+
+
+def test_scan_two_graphs_of_one_process():
+    """Two captured calls replayed in turn and again: neither finds the other's words."""
+    import torch
+    import recurrent_state_memory_amd as gdr
+    ds = [scan_inputs((2, 700 + 600 * i), 96, "f32", "alpha", seed=60 + i) for i in range(2)]
+    ins = [(dev(d["x"]), dev(d["kw"]["alpha"]), dev(d["h"])) for d in ds]
+    want = [gdr.gdr_scan_fwd(x, a, h0=h) for x, a, h in ins]
+    graphs, outs = [], []
+    for x, a, h in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(gdr.gdr_scan_fwd(x, a, h0=h))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        for t in outs[i][:2]:
+            t.fill_(7)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+        gdr.gdr_scan_fwd(*ins[i][:2])
+
+
 def test_scan_streams_and_graph():
     """Two streams at once, then forward and backward captured and replayed with new
     inputs and eager calls in between."""
