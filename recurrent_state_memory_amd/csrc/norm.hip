@@ -116,8 +116,8 @@ __global__ __launch_bounds__(threads_of(L)) void norm_fwd_kernel(gdr_norm_args p
   }
 }
 
-// Backward.  A workgroup of TH threads takes TH / L rows at a time, every
-// (gridDim TH / L)-th; a thread keeps its columns' sums in registers (SUMS).  Groups
+// Backward.  A workgroup of 1024 threads takes 1024 / L rows at a time, every
+// (gridDim 1024 / L)-th; a thread keeps its columns' sums in registers (SUMS).  Groups
 // are joined over the wave and the workgroup, in a fixed order, and a workgroup
 // leaves one partial row of each sum for join_kernel.
 template <typename T, bool CODES, int NV>
@@ -174,8 +174,9 @@ __device__ inline void load_weight(const gdr_norm_bwd_args& p, int c0, float (&w
   }
 }
 
-template <typename T, bool CODES, int TH, int L, int NV, bool SUMS>
-__global__ __launch_bounds__(TH) void norm_bwd_kernel(gdr_norm_bwd_args p, float* part) {
+template <typename T, bool CODES, int L, int NV, bool SUMS>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(gdr_norm_bwd_args p, float* part) {
+  constexpr int TH = 1024;
   constexpr int N = Run<T>::N;
   constexpr int kPer = TH / L;
   constexpr bool kHold = NV * N <= 16;   // weights stay in registers
@@ -373,26 +374,48 @@ __global__ __launch_bounds__(1024) void join_kernel(const float* part, int rows,
 struct Shape {
   int L, NV;
 };
-constexpr Shape fwd_shape(int runs) {
+constexpr Shape fwd_shape(int runs, bool ck) {
   if (runs <= 8) return {8, 1};
   if (runs <= 16) return {16, 1};
   if (runs <= 32) return {32, 1};
-  if (runs <= 256) return {64, runs <= 64 ? 1 : runs <= 128 ? 2 : runs <= 192 ? 3 : 4};
-  if (runs <= 2048) return {256, runs <= 512 ? 2 : runs <= 768 ? 3 : runs <= 1024 ? 4 : runs <= 1280 ? 5 : runs <= 1536 ? 6 : 8};
+  if (runs <= 64) return {64, 1};
+  if (runs <= 128) return {64, 2};
+  if (ck) {   // packing wants registers: fewer runs a thread
+    if (runs <= 384) return {128, runs <= 256 ? 2 : 3};
+    if (runs <= 1024) return {256, runs <= 512 ? 2 : runs <= 768 ? 3 : 4};
+    return {512, runs <= 1536 ? 3 : runs <= 2048 ? 4 : 0};   // 0: packed by a launch of its own
+  }
+  if (runs <= 256) return {64, runs <= 192 ? 3 : 4};
+  if (runs <= 384) return {128, 3};
+  if (runs <= 1024) return {256, runs <= 512 ? 2 : runs <= 768 ? 3 : 4};
+  if (runs <= 2048) return {512, runs <= 1536 ? 3 : 4};
   return {1024, runs <= 4096 ? 4 : runs <= 8192 ? 8 : 16};
 }
-constexpr Shape bwd_shape(int runs) {
+constexpr Shape bwd_shape(int runs, int N) {
   if (runs <= 8) return {8, 1};
   if (runs <= 16) return {16, 1};
   if (runs <= 32) return {32, 1};
   if (runs <= 64) return {64, 1};
   if (runs <= 128) return {128, 1};
-  if (runs <= 2048)
-    return {256, runs <= 256 ? 1 : runs <= 512 ? 2 : runs <= 768 ? 3 : runs <= 1024 ? 4 : runs <= 1280 ? 5 : runs <= 1536 ? 6 : 8};
+  if (runs <= 256) return {256, 1};
+  if (runs <= 512) return {512, 1};
+  if (N == 8 && runs <= 1024) return {1024, 1};
+  if (N == 4 && runs <= 1536) return {512, runs <= 1024 ? 2 : 3};
+  if (runs <= 2048) return {1024, 2};
+  if (N == 4 && runs <= 3072) return {1024, 3};
   return {1024, 0};   // norm_bwd_long_kernel
 }
-// Threads of a backward workgroup, of N values a run.
-constexpr int bwd_threads(int L, int NV, int N) { return NV * N <= 8 ? 1024 : NV * N <= 24 ? 512 : 256; }
+// Whether some row of runs of N values has this shape.
+constexpr bool bwd_has(int N, int L, int NV) {
+  for (int runs = 1; runs <= 3072; ++runs)
+    if (bwd_shape(runs, N).L == L && bwd_shape(runs, N).NV == NV) return true;
+  return false;
+}
+constexpr bool fwd_has(int N, int L, int NV, bool ck) {
+  for (int runs = 1; runs <= 65536 / N; runs += runs < 64 ? 1 : 64)   // shapes change after multiples of 64
+    if (fwd_shape(runs, ck).L == L && fwd_shape(runs, ck).NV == NV) return true;
+  return false;
+}
 inline int runs_of(int D, int io_dtype) { const int n = io_dtype == GDR_BF16 ? 8 : 4; return (D + n - 1) / n; }
 
 // Workgroups of a forward launch (a grid holds 2^32 threads); they take further rows in turn.
@@ -406,35 +429,32 @@ size_t bwd_workspace(int64_t R, int D) {
   return (size_t)kParts * 2 * D * sizeof(float);
 }
 
-#define GDR_NORM_SHAPES(X) \
-  X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(256, 2) X(256, 3) X(256, 4) X(256, 5) X(256, 6) X(256, 8)
-#define GDR_NORM_FWD_SHAPES(X) X(64, 2) X(64, 3) X(64, 4) X(1024, 4) X(1024, 8) X(1024, 16)
-#define GDR_NORM_BWD_SHAPES(X) X(128, 1) X(256, 1)
+#define GDR_NORM_SHAPES(X) X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(512, 3)
+#define GDR_NORM_FWD_SHAPES(X) \
+  X(64, 2) X(64, 3) X(64, 4) X(128, 2) X(128, 3) X(256, 2) X(256, 3) X(256, 4) X(512, 4) X(1024, 4) X(1024, 8) X(1024, 16)
+#define GDR_NORM_BWD_SHAPES(X) X(128, 1) X(256, 1) X(512, 1) X(512, 2) X(1024, 1) X(1024, 2) X(1024, 3)
 
 template <typename T>
 static hipError_t fwd(const gdr_norm_args& a, hipStream_t s) {
-  const Shape sh = fwd_shape(runs_of(a.D, a.io_dtype));
+  constexpr int N = Run<T>::N;
+  const int runs = runs_of(a.D, a.io_dtype);
+  const bool ck = a.x_code && fwd_shape(runs, true).NV > 0;   // packed on the way
+  const Shape sh = fwd_shape(runs, ck);
   const int per = threads_of(sh.L) / sh.L;
   const int64_t groups = (a.R + per - 1) / per;
   const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
-#define GDR_LAUNCH(LL, NN)                                                                                       \
-  if (sh.L == LL && sh.NV == NN) {                                                                               \
-    if constexpr (LL * NN * Run<T>::N <= 65536) {                                                                \
-      if constexpr (LL <= 256) {                                                                                 \
-        if (a.x_code) {                                                                                          \
-          hipLaunchKernelGGL((norm_fwd_kernel<T, LL, NN, true>), grid, dim3(threads_of(LL)), 0, s, a);           \
-          return hipGetLastError();                                                                              \
-        }                                                                                                        \
-      }                                                                                                          \
-      hipLaunchKernelGGL((norm_fwd_kernel<T, LL, NN, false>), grid, dim3(threads_of(LL)), 0, s, a);              \
-    }                                                                                                            \
+#define GDR_LAUNCH(LL, NN)                                                                               \
+  if (sh.L == LL && sh.NV == NN) {                                                                       \
+    if constexpr (fwd_has(N, LL, NN, true))                                                              \
+      if (ck) hipLaunchKernelGGL((norm_fwd_kernel<T, LL, NN, true>), grid, dim3(threads_of(LL)), 0, s, a); \
+    if constexpr (fwd_has(N, LL, NN, false))                                                             \
+      if (!ck) hipLaunchKernelGGL((norm_fwd_kernel<T, LL, NN, false>), grid, dim3(threads_of(LL)), 0, s, a); \
   }
   GDR_NORM_SHAPES(GDR_LAUNCH)
   GDR_NORM_FWD_SHAPES(GDR_LAUNCH)
 #undef GDR_LAUNCH
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.x_code) return e;
-  // rows of more than 2048 runs: no registers are left to pack beside them
+  if (e != hipSuccess || !a.x_code || ck) return e;
   const gdr_ckpt8_pack_args c{a.R, a.D, a.io_dtype, a.x, a.x_code, a.x_exp};
   return ckpt8::launch_pack(c, s);
 }
@@ -442,7 +462,7 @@ static hipError_t fwd(const gdr_norm_args& a, hipStream_t s) {
 template <typename T, bool CODES>
 static hipError_t bwd(const gdr_norm_bwd_args& a, hipStream_t s) {
   constexpr int N = Run<T>::N;
-  const Shape sh = bwd_shape(runs_of(a.D, a.io_dtype));
+  const Shape sh = bwd_shape(runs_of(a.D, a.io_dtype), N);
   const bool sums = a.grad_weight || a.grad_bias;
   float* part = (float*)a.workspace;
   int parts = (int)(a.R < kParts ? a.R : kParts);
@@ -450,14 +470,15 @@ static hipError_t bwd(const gdr_norm_bwd_args& a, hipStream_t s) {
     hipLaunchKernelGGL((norm_bwd_long_kernel<T, CODES>), dim3(parts), dim3(1024), 0, s, a);
     if (sums) hipLaunchKernelGGL((norm_cols_kernel<T, CODES>), dim3((a.D + 255) / 256, parts), dim3(256), 0, s, a, part);
   } else {
-    const int per = bwd_threads(sh.L, sh.NV, N) / sh.L;
+    const int per = 1024 / sh.L;
     const int64_t groups = (a.R + per - 1) / per;
     if (groups < parts) parts = (int)groups;
-#define GDR_LAUNCH(LL, NN)                                                                                           \
-  if (sh.L == LL && sh.NV == NN) {                                                                                   \
-    constexpr int TH = bwd_threads(LL, NN, N);                                                                       \
-    if (sums) hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, TH, LL, NN, true>), dim3(parts), dim3(TH), 0, s, a, part); \
-    else hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, TH, LL, NN, false>), dim3(parts), dim3(TH), 0, s, a, part);   \
+#define GDR_LAUNCH(LL, NN)                                                                                             \
+  if constexpr (bwd_has(N, LL, NN)) {                                                                                  \
+    if (sh.L == LL && sh.NV == NN) {                                                                                   \
+      if (sums) hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, LL, NN, true>), dim3(parts), dim3(1024), 0, s, a, part); \
+      else hipLaunchKernelGGL((norm_bwd_kernel<T, CODES, LL, NN, false>), dim3(parts), dim3(1024), 0, s, a, part);     \
+    }                                                                                                                  \
   }
     GDR_NORM_SHAPES(GDR_LAUNCH)
     GDR_NORM_BWD_SHAPES(GDR_LAUNCH)
