@@ -3,8 +3,11 @@
 // A row is held in registers by L threads of NV 16-byte runs each (thread l has
 // runs l, l + L, ...), so it is read once: the mean, then the squares about it,
 // then the outputs.  L is a part of a wave for short rows (64 / L rows side by side
-// in a wave, no barrier), a wave up to 4 runs a lane, then 256 or 1024 threads.
-// Both kernels are bound by HBM.
+// in a wave, no barrier), a wave, or up to 1024 threads: few runs a thread, since what
+// is under way at once hides the latency (backward of 64 Mi bf16 elements in rows of
+// 8192: one run of each of 1024 threads 82 us, four of 256 142 us).  Both kernels are
+// bound by HBM: forward of 32768 x 2048 bf16 51 us (5.3 TB/s), with the 8-bit copy 69 us
+// (4.9 TB/s), backward 81 us (5.0 TB/s); per-head rows of 128 channels 57 and 81 us.
 #include "chan_device.h"
 #include "norm_kernels.h"
 
@@ -421,7 +424,8 @@ inline int runs_of(int D, int io_dtype) { const int n = io_dtype == GDR_BF16 ? 8
 // Workgroups of a forward launch (a grid holds 2^32 threads); they take further rows in turn.
 constexpr int64_t kMaxGroups = 1 << 20;
 
-// Workgroups of a backward launch, and partial rows of the columns' sums.
+// Workgroups of a backward launch, and partial rows of the columns' sums: one for each
+// CU, as more mostly write more partial rows (fp32 5000 x 5003: 512 took 85 us, 256 76).
 constexpr int kParts = 256;
 
 size_t bwd_workspace(int64_t R, int D) {

@@ -19,7 +19,7 @@ constexpr int kSuper = 8;       // tiles that share one hand-over along the sequ
 // the gates' arithmetic bounds the kernel and not HBM, the more chains, the fewer
 // waits for a tile before.  8 x 4096 x 2048, teams of 32 against 128: decays given,
 // forward 107 / 113 us, backward 181 / 192; fp32 gated backward (half the batch) 186
-// / 194; bf16 gated backward 248 / 242, forward 120 / 118.
+// / 194; bf16 gated backward 248 / 242, forward 120 / 118 us.
 constexpr int team_of(bool alpha, int io_dtype) { return alpha || io_dtype != GDR_BF16 ? 32 : 128; }
 
 constexpr size_t blocks_of(int T) { return ((size_t)T + GDR_SCAN_BLOCK - 1) / GDR_SCAN_BLOCK; }

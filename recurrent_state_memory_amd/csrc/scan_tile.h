@@ -16,10 +16,10 @@
 // single sequence of 32785 tokens took 140 us, 128 hand-overs of about 1.05 us).
 //
 // Tile numbers are drawn from a ticket.  Chains are taken in teams, and a team's
-// first tiles come before its second ones: a tile waits only for tiles whose workgroups have
-// already started, and each publishes its map before it waits, so every wait ends;
-// were one not to (a workspace in use elsewhere), it gives up after kSpinLimit
-// polls with NaN.
+// first tiles come before its second ones: a tile waits only for tiles whose
+// workgroups have already started, and each publishes its map before it waits, so
+// every wait ends; were one not to (a workspace in use elsewhere), it gives up after
+// kSpinLimit polls with NaN.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -119,8 +119,8 @@ struct Four<Code8> {
 // A thread's rows of one of the call's arrays, from the tile's first element on.
 // VEC (rows of a multiple of 4 channels, in buffers aligned to 4 elements): through a
 // buffer that ends with the tile's rows.  Else with a test of what exists: four
-// channels at once wherever they lie, one by one at a row's end.  (One access each
-// everywhere took 76 us against 122 for 4 x 2048 x 2047 against 8 x 4096 x 2048.)
+// channels at once wherever they lie, one by one at a row's end (4 x 2048 x 2047 bf16,
+// gated: forward 62 us, backward 98; one access for each channel took 71 and 145).
 template <typename T, bool VEC>
 struct View {
   rsrc_t b;
