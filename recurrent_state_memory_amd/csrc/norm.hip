@@ -405,12 +405,12 @@ constexpr Shape bwd_shape(int runs, int N) {
   if (N == 8 && runs <= 1024) return {1024, 1};
   if (N == 4 && runs <= 1536) return {512, runs <= 1024 ? 2 : 3};
   if (runs <= 2048) return {1024, 2};
-  if (N == 4 && runs <= 3072) return {1024, 3};
+  if (N == 4 && runs <= 3 * 1024) return {1024, 3};
   return {1024, 0};   // norm_bwd_long_kernel
 }
 // Whether some row of runs of N values has this shape.
 constexpr bool bwd_has(int N, int L, int NV) {
-  for (int runs = 1; runs <= 3072; ++runs)
+  for (int runs = 1; runs <= 3 * 1024; ++runs)
     if (bwd_shape(runs, N).L == L && bwd_shape(runs, N).NV == NV) return true;
   return false;
 }
