@@ -166,6 +166,22 @@ def test_norm_of_the_delta_rules_heads():
     check("heads y", y, yr, ty.reshape(yr.shape))
 
 
+def test_norm_one_row_without_leading_dimensions():
+    import torch
+    import recurrent_state_memory_amd as gdr
+    d = inputs(1, 300, "f32", 51)
+    x, dy = dev(d["x"]), dev(d["dy"])
+    ref = gdr.gdr_norm_fwd(x, return_ckpt8=True)
+    y, m, r, kept = gdr.gdr_norm_fwd(x[0], return_ckpt8=True)
+    assert m.shape == () and kept[1].shape == (3,) and torch.equal(y, ref[0][0]) and torch.equal(m, ref[1][0])
+    g, g0 = gdr.gdr_norm_bwd(dy[0], kept, m, r), gdr.gdr_norm_bwd(dy, ref[3], ref[1], ref[2])
+    assert torch.equal(g["x"], g0["x"][0]) and torch.equal(g["weight"], g0["weight"])
+    with pytest.raises(gdr.GdrError):            # in place: refused
+        gdr.gdr_norm_fwd(x, y=x)
+    with pytest.raises(gdr.GdrError):            # no rows
+        gdr.gdr_norm_fwd(x[:0])
+
+
 def test_norm_other_stream_and_given_workspace():
     """A call on a side stream, with a workspace that held something else before."""
     import torch
