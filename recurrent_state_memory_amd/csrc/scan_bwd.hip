@@ -6,7 +6,7 @@
 // tile to tile with the last tiles first.  G_t = grad_y_t + K_{t+1}, so a run of
 // tokens takes K to P K + Q with P the same product of decays.
 //
-// A thread keeps a, b and the softplus of its 32 elements in registers, and
+// A thread keeps a, b, b x and the softplus of its 32 elements in registers, and
 // sigmoid(decay_x) and 1 / n, n = sqrt(1 - a^2), in LDS (its own 16 bytes a token, no
 // barrier), so that everything is evaluated once; b = s n gives back s = b / n.
 //
@@ -19,8 +19,6 @@
 // grad_decay_a sums over all tokens: registers, lane groups, waves (one LDS pass
 // in a fixed order), then one partial row per tile that sum_kernel adds up, again
 // in a fixed order.
-#include <type_traits>
-
 #include "scan_gate.h"
 #include "scan_tile.h"
 
@@ -76,7 +74,6 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
 #pragma unroll
     for (int k = 0; k < V; ++k) scale[k] = Four<float>::get(r, k);
   }
-  using XR = std::conditional_t<kCodes, __bf16, X>;   // codes become bf16, which holds their values (to 2^-133)
   typename Four<X>::R rx[S];
   typename Four<T>::R ry[S];
   Four<float>::R ra[KIND == 0 ? S : 1];
@@ -115,23 +112,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   if (q.wave == 0 && q.tt < kSuper && p.grad_h && cc < C) k_in = p.grad_h[(size_t)q.b * C + cc];
 
   // a and b; (P, H) forwards and (P, Q) backwards over the thread's run
-  typename Four<XR>::R xr[S];
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    if constexpr (kCodes)
-      xr[i] = u32x2{bf16_pair(Four<X>::get(rx[i], 0) * xs[i], Four<X>::get(rx[i], 1) * xs[i]),
-                    bf16_pair(Four<X>::get(rx[i], 2) * xs[i], Four<X>::get(rx[i], 3) * xs[i])};
-    else
-      xr[i] = rx[i];
-  }
-  float a[S][V], b[KIND == 2 || NORM ? S : 1][V], sp[KIND == 0 ? 1 : S][V], P[V], H[V], Q[V];
-  const auto x_at = [&](int i, int k) {
-    return Four<XR>::get(xr[i], k);
-  };
-  const auto v_at = [&](int i, int k) {
-    if constexpr (KIND == 2 || NORM) return b[i][k] * x_at(i, k);
-    return x_at(i, k);
-  };
+  float a[S][V], v[S][V], b[KIND == 2 || NORM ? S : 1][V], sp[KIND == 0 ? 1 : S][V], P[V], H[V], Q[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     P[k] = 1.f;
@@ -162,8 +143,14 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
     if constexpr (NORM) kept[1][i][threadIdx.x] = kn;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
+      v[i][k] = Four<X>::get(rx[i], k);
+      if constexpr (kCodes) v[i][k] *= xs[i];
+      if constexpr (KIND == 2 || NORM) v[i][k] *= b[i][k];
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
       P[k] *= a[i][k];
-      H[k] = fmaf(a[i][k], H[k], v_at(i, k));
+      H[k] = fmaf(a[i][k], H[k], v[i][k]);
     }
   }
   // behind the last token the state stays: x and grad_y read as 0 there
@@ -177,7 +164,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
       for (int i = 0; i < S; ++i) {
         if (r0 + i >= rows) a[i][k] = 1.f;
         P[k] *= a[i][k];
-        H[k] = fmaf(a[i][k], H[k], v_at(i, k));
+        H[k] = fmaf(a[i][k], H[k], v[i][k]);
       }
     }
   }
@@ -218,7 +205,6 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   float prev[HS][V];
 #pragma unroll
   for (int i = 0; i < (half + 1) * HS; ++i) {
-    forget(xr[i]);
     forget(ry[i]);
   }
   {
@@ -230,7 +216,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         if (i >= half * HS) prev[i - half * HS][k] = t[k];
-        t[k] = fmaf(a[i][k], t[k], v_at(i, k));
+        t[k] = fmaf(a[i][k], t[k], v[i][k]);
       }
 #pragma unroll
     for (int k = 0; k < V; ++k) prev[HS - 1][k] = t[k];
@@ -251,16 +237,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
         od[k] = G * prev[i - half * HS][k];
       } else {
         float in = -prev[i - half * HS][k];
-        const float x = x_at(i, k);
         ox_[k] = G;
         if constexpr (KIND == 2 || NORM) ox_[k] *= b[i][k];
-        if constexpr (KIND == 2) {
-          const float sg = NORM ? b[i][k] * kn[k] : b[i][k];
-          og[k] = ox_[k] * x * (1.f - sg);
-          if constexpr (NORM) in = fmaf(x * sg, ak * kn[k], in);   // v a / m = x s a / n
-        } else if constexpr (NORM) {
-          in = fmaf(x, ak * kn[k], in);
-        }
+        if constexpr (KIND == 2) og[k] = G * v[i][k] * (1.f - (NORM ? b[i][k] * kn[k] : b[i][k]));
+        if constexpr (NORM) in = fmaf(v[i][k] * kn[k], ak * kn[k], in);   // v a / m
         float du = K[k] * in;
         if (ragged && r0 + i >= rows) du = 0.f;   // no part of grad_decay_a, also where the state is NaN
         sum[k] = fmaf(du, sp[i][k], sum[k]);
