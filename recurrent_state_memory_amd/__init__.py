@@ -824,30 +824,39 @@ def _scan_fwd(x, alpha, decay_x, decay_a, gate_x, normalise, h0, y, h_out, ckpt,
         raise ValueError("gdr: x must be [B,T,C]")
     shape, io, f32, dev = x.shape, x.dtype, torch.float32, x.device
     B, T, C = shape
-    a = ScanArgs(B, T, C, _io(x), _in(x, "x", shape, io, dev))
+    code_io = _io(x)
+    xp = _in(x, "x", shape, io, dev)
+    ap = dp = sp = gp = None
     if alpha is not None:
-        a.alpha = _in(alpha, "alpha", shape, f32, dev)
+        ap = _in(alpha, "alpha", shape, f32, dev)
     else:
-        a.decay_x = _in(decay_x, "decay_x", shape, io, dev)
-        a.decay_a = _in(decay_a, "decay_a", (C,), f32, dev)
-        a.gate_x = _opt(gate_x, "gate_x", shape, io, dev)
-        a.normalise = int(bool(normalise))
-    a.h0 = _opt(h0, "h0", (B, C), f32, dev)
-    lib = load_library()
+        dp = _in(decay_x, "decay_x", shape, io, dev)
+        sp = _in(decay_a, "decay_a", (C,), f32, dev)
+        gp = _opt(gate_x, "gate_x", shape, io, dev)
+    hp = _opt(h0, "h0", (B, C), f32, dev)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
             return _scan_fwd(x, alpha, decay_x, decay_a, gate_x, normalise, h0, y, h_out, ckpt, return_state, return_ckpt,
                              workspace, None)
     if y is None:
         y = torch.empty_like(x)
-    if h_out is None and return_state:
+        yp = y.data_ptr()
+    else:
+        yp = _in(y, "y", shape, io, dev)
+    op = cp = None
+    if h_out is not None:
+        op = _in(h_out, "h_out", (B, C), f32, dev)
+    elif return_state:
         h_out = torch.empty((B, C), dtype=f32, device=dev)
+        op = h_out.data_ptr()
     cshape = (B, -(-T // GDR_SCAN_BLOCK), C)
-    if ckpt is None and return_ckpt:
+    if ckpt is not None:
+        cp = _in(ckpt, "ckpt", cshape, f32, dev)
+    elif return_ckpt:
         ckpt = torch.empty(cshape, dtype=f32, device=dev)
-    a.y = _in(y, "y", shape, io, dev)
-    a.h_out = _opt(h_out, "h_out", (B, C), f32, dev)
-    a.ckpt = _opt(ckpt, "ckpt", cshape, f32, dev)
+        cp = ckpt.data_ptr()
+    lib = load_library()
+    a = ScanArgs(B, T, C, code_io, xp, ap, dp, sp, gp, int(alpha is None and bool(normalise)), 0, hp, yp, op, cp)
     a.workspace, a.workspace_bytes, keep = _workspace(
         lib.gdr_scan_fwd_workspace(ctypes.byref(a)), workspace, dev)
     _launch(lib.gdr_scan_fwd, a, dev)
@@ -894,45 +903,43 @@ def _scan_bwd(x, alpha, decay_x, decay_a, gate_x, normalise, grad_y, h0, grad_h,
         raise ValueError("gdr: grad_y must be [B,T,C]")
     shape, io, f32, dev = grad_y.shape, grad_y.dtype, torch.float32, grad_y.device
     B, T, C = shape
-    a = ScanBwdArgs(B, T, C, _io(grad_y))
-    if isinstance(x, tuple):
-        a.x, a.x_exp = _x8(x, (B, T), C, dev)
-    else:
-        a.x = _in(x, "x", shape, io, dev)
+    code_io = _io(grad_y)
+    xp, ep = _x8(x, (B, T), C, dev) if isinstance(x, tuple) else (_in(x, "x", shape, io, dev), None)
+    ap = dp = sp = gp = None
     if alpha is not None:
-        a.alpha = _in(alpha, "alpha", shape, f32, dev)
+        ap = _in(alpha, "alpha", shape, f32, dev)
     else:
-        a.decay_x = _in(decay_x, "decay_x", shape, io, dev)
-        a.decay_a = _in(decay_a, "decay_a", (C,), f32, dev)
-        a.gate_x = _opt(gate_x, "gate_x", shape, io, dev)
-        a.normalise = int(bool(normalise))
+        dp = _in(decay_x, "decay_x", shape, io, dev)
+        sp = _in(decay_a, "decay_a", (C,), f32, dev)
+        gp = _opt(gate_x, "gate_x", shape, io, dev)
     if ckpt is not None and h0 is not None:
         raise ValueError("gdr: pass either ckpt or h0, not both (ckpt holds the start state)")
-    a.h0 = _opt(h0, "h0", (B, C), f32, dev)
-    a.ckpt = _opt(ckpt, "ckpt", (B, -(-T // GDR_SCAN_BLOCK), C), f32, dev)
-    a.grad_y = _in(grad_y, "grad_y", shape, io, dev)
-    a.grad_h = _opt(grad_h, "grad_h", (B, C), f32, dev)
-    lib = load_library()
-    g = {}
+    hp = _opt(h0, "h0", (B, C), f32, dev)
+    cp = _opt(ckpt, "ckpt", (B, -(-T // GDR_SCAN_BLOCK), C), f32, dev)
+    gyp = _in(grad_y, "grad_y", shape, io, dev)
+    ghp = _opt(grad_h, "grad_h", (B, C), f32, dev)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
             return _scan_bwd(x, alpha, decay_x, decay_a, gate_x, normalise, grad_y, h0, grad_h, ckpt, need_grad_h0,
                              workspace, None)
-    g["x"] = torch.empty(shape, dtype=io, device=dev)
-    a.grad_x = g["x"].data_ptr()
+    g = {"x": torch.empty_like(grad_y)}
+    gal = gdx = gda = ggx = gh0 = None
     if alpha is not None:
-        g["alpha"] = torch.empty(shape, dtype=f32, device=dev)
-        a.grad_alpha = g["alpha"].data_ptr()
+        g["alpha"] = torch.empty_like(alpha)
+        gal = g["alpha"].data_ptr()
     else:
-        g["decay_x"] = torch.empty(shape, dtype=io, device=dev)
-        g["decay_a"] = torch.empty((C,), dtype=f32, device=dev)
-        a.grad_decay_x, a.grad_decay_a = g["decay_x"].data_ptr(), g["decay_a"].data_ptr()
+        g["decay_x"] = torch.empty_like(decay_x)
+        g["decay_a"] = torch.empty_like(decay_a)
+        gdx, gda = g["decay_x"].data_ptr(), g["decay_a"].data_ptr()
         if gate_x is not None:
-            g["gate_x"] = torch.empty(shape, dtype=io, device=dev)
-            a.grad_gate_x = g["gate_x"].data_ptr()
+            g["gate_x"] = torch.empty_like(gate_x)
+            ggx = g["gate_x"].data_ptr()
     if need_grad_h0:
         g["h0"] = torch.empty((B, C), dtype=f32, device=dev)
-        a.grad_h0 = g["h0"].data_ptr()
+        gh0 = g["h0"].data_ptr()
+    lib = load_library()
+    a = ScanBwdArgs(B, T, C, code_io, xp, ep, ap, dp, sp, gp, int(alpha is None and bool(normalise)), 0, hp, cp, gyp,
+                    ghp, g["x"].data_ptr(), gal, gdx, gda, ggx, gh0)
     a.workspace, a.workspace_bytes, keep = _workspace(
         lib.gdr_scan_bwd_workspace(ctypes.byref(a)), workspace, dev)
     _launch(lib.gdr_scan_bwd, a, dev)
@@ -1069,28 +1076,25 @@ def gdr_norm_bwd(grad_y, x, mean, rstd, weight=None, *, need_grad_weight=True, n
         raise ValueError("gdr: grad_y must be [...,D]")
     shape, io, f32, dev = grad_y.shape, grad_y.dtype, torch.float32, grad_y.device
     lead, D = shape[:-1], shape[-1]
-    a = NormBwdArgs(math.prod(lead), D, _io(grad_y))
-    if isinstance(x, tuple):
-        a.x, a.x_exp = _x8(x, lead, D, dev)
-    else:
-        a.x = _in(x, "x", shape, io, dev)
-    a.mean, a.rstd = _in(mean, "mean", lead, f32, dev), _in(rstd, "rstd", lead, f32, dev)
-    a.weight = _opt(weight, "weight", (D,), f32, dev)
-    a.grad_y = _in(grad_y, "grad_y", shape, io, dev)
-    lib = load_library()
-    g = {}
+    R, code_io = math.prod(lead), _io(grad_y)
+    xp, ep = _x8(x, lead, D, dev) if isinstance(x, tuple) else (_in(x, "x", shape, io, dev), None)
+    mp, rp = _in(mean, "mean", lead, f32, dev), _in(rstd, "rstd", lead, f32, dev)
+    wp = _opt(weight, "weight", (D,), f32, dev)
+    gyp = _in(grad_y, "grad_y", shape, io, dev)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
             return gdr_norm_bwd(grad_y, x, mean, rstd, weight, need_grad_weight=need_grad_weight,
                                 need_grad_bias=need_grad_bias, workspace=workspace)
-    g["x"] = torch.empty(shape, dtype=io, device=dev)
-    a.grad_x = g["x"].data_ptr()
+    g = {"x": torch.empty_like(grad_y)}
+    gwp = gbp = None
     if need_grad_weight:
         g["weight"] = torch.empty((D,), dtype=f32, device=dev)
-        a.grad_weight = g["weight"].data_ptr()
+        gwp = g["weight"].data_ptr()
     if need_grad_bias:
         g["bias"] = torch.empty((D,), dtype=f32, device=dev)
-        a.grad_bias = g["bias"].data_ptr()
+        gbp = g["bias"].data_ptr()
+    lib = load_library()
+    a = NormBwdArgs(R, D, code_io, xp, ep, mp, rp, wp, gyp, g["x"].data_ptr(), gwp, gbp)
     a.workspace, a.workspace_bytes, keep = _workspace(
         lib.gdr_norm_bwd_workspace(ctypes.byref(a)), workspace, dev)
     _launch(lib.gdr_norm_bwd, a, dev)

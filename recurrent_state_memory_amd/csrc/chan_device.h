@@ -177,7 +177,7 @@ struct Codes<4> {
   }
 };
 
-// Sum (maximum) over L neighbouring lanes, L a power of two from 8 to 64, in every
+// Sum (maximum) over L neighbouring lanes, L a power of two from 2 to 64, in every
 // one of them.  Within rows of 16 lanes by rotation (DPP, no LDS), across rows by
 // the lane swaps: with both operands v, permlane16_swap leaves the even and the odd
 // rows' values in its two results, permlane32_swap the lower and the upper half's.
@@ -187,11 +187,11 @@ __device__ inline uint32_t row_ror(uint32_t v) {
 }
 template <int L, typename OP>
 __device__ inline uint32_t lane_join(uint32_t v, OP op) {
-  static_assert(L == 8 || L == 16 || L == 32 || L == 64, "lanes");
-  if constexpr (L == 8) {   // eight lanes of a row: exchanges within them
-    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, false));    // lane ^ 1
-    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, false));    // lane ^ 2
-    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));   // 7 - lane of each 8
+  static_assert(L == 2 || L == 4 || L == 8 || L == 16 || L == 32 || L == 64, "lanes");
+  if constexpr (L <= 8) {   // up to eight lanes of a row: exchanges within them
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, false));                           // lane ^ 1
+    if constexpr (L >= 4) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, false));     // lane ^ 2
+    if constexpr (L == 8) v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));    // 7 - lane
     return v;
   } else {
     v = op(v, row_ror<8>(v));

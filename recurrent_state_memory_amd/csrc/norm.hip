@@ -378,6 +378,8 @@ struct Shape {
   int L, NV;
 };
 constexpr Shape fwd_shape(int runs, bool ck) {
+  if (runs <= 2) return {2, 1};
+  if (runs <= 4) return {4, 1};
   if (runs <= 8) return {8, 1};
   if (runs <= 16) return {16, 1};
   if (runs <= 32) return {32, 1};
@@ -395,6 +397,8 @@ constexpr Shape fwd_shape(int runs, bool ck) {
   return {1024, runs <= 4096 ? 4 : runs <= 8192 ? 8 : 16};
 }
 constexpr Shape bwd_shape(int runs, int N) {
+  if (runs <= 2) return {2, 1};
+  if (runs <= 4) return {4, 1};
   if (runs <= 8) return {8, 1};
   if (runs <= 16) return {16, 1};
   if (runs <= 32) return {32, 1};
@@ -433,7 +437,7 @@ size_t bwd_workspace(int64_t R, int D) {
   return (size_t)kParts * 2 * D * sizeof(float);
 }
 
-#define GDR_NORM_SHAPES(X) X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(512, 3)
+#define GDR_NORM_SHAPES(X) X(2, 1) X(4, 1) X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(512, 3)
 #define GDR_NORM_FWD_SHAPES(X) \
   X(64, 2) X(64, 3) X(64, 4) X(128, 2) X(128, 3) X(256, 2) X(256, 3) X(256, 4) X(512, 4) X(1024, 4) X(1024, 8) X(1024, 16)
 #define GDR_NORM_BWD_SHAPES(X) X(128, 1) X(256, 1) X(512, 1) X(512, 2) X(1024, 1) X(1024, 2) X(1024, 3)
