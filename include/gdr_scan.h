@@ -64,7 +64,9 @@ typedef struct gdr_scan_args {
 size_t gdr_scan_fwd_workspace(const gdr_scan_args *args);
 
 /* Forward on `stream`; GDR_ERR_* as in gdr.h, all checked before any HIP call.
- * A workspace serves one call at a time. */
+ * Workgroups hand states to each other through the workspace, which the call clears
+ * itself: it serves one call at a time (calls on one stream, or a graph replayed on
+ * it, may share one). */
 gdr_status gdr_scan_fwd(const gdr_scan_args *args, void *stream);
 
 /* Gradients of a loss L through y and h_out.  With G_t = dL/dh_t (everything

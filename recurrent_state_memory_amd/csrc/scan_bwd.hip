@@ -11,10 +11,11 @@
 // barrier), so that everything is evaluated once; b = s n gives back s = b / n.
 //
 // With given decays it is bound by HBM (8 x 4096 x 2048: 944 MB of least traffic in
-// 181 us).  Gated in bf16 (882 MB, x in 8 bits) it takes 230 us: about 76 vector
+// 181 us).  Gated in bf16 (882 MB, x in 8 bits) it takes 223 us: about 71 vector
 // instructions an element keep the vector units busy in two thirds of the cycles at
-// two waves per SIMD (the registers' limit); four tokens a thread at four waves per
-// SIMD executed more and took 249 us, workgroups that stay for further tiles 242 us.
+// two waves per SIMD (the registers' limit).  At 235 us, four tokens a thread at four
+// waves per SIMD executed more and took 249, and workgroups that stay for further
+// tiles 242.
 //
 // grad_decay_a sums over all tokens: registers, lane groups, waves (one LDS pass
 // in a fixed order), then one partial row per tile that sum_kernel adds up, again
