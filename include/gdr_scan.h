@@ -16,9 +16,10 @@
  * (the decay's form is the gated delta rule's, gdr_chunk_fwd_gated; with
  * normalise the state of a white input keeps its variance whatever the decay).
  *
- * Decays: alpha in [0, 1] and decay_a >= 0 are not checked.  A decay of 0 is an
- * exact reset (it starts a new sequence packed behind another), alpha = 1 with
- * x = 0 leaves the state as it is (padding).  NaN and Inf propagate.
+ * Decays: alpha in [0, 1] and decay_a >= 0 are not checked.  A decay of 0
+ * (alpha = 0, decay_x = +Inf) is an exact reset: it starts a new sequence packed
+ * behind another.  alpha = 1 with x = 0, or decay_x = -Inf with normalise, leaves the
+ * state as it is (padding).  NaN, and Inf in x, h0 and the gradients, propagate.
  *
  * Sizes: any B, C and T >= 1 with B * T * C < 2^40, C <= 2^18 and
  * B * ceil(C/64) * ceil(T/128) < 2^23.  Every pointer is

@@ -203,56 +203,56 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   constexpr int HS = S / 2;
 #pragma unroll
   for (int half = 1; half >= 0; --half) {
-  float prev[HS][V];
+    float prev[HS][V];
 #pragma unroll
-  for (int i = 0; i < (half + 1) * HS; ++i) {
-    forget(ry[i]);
-  }
-  {
-    float t[V];
+    for (int i = 0; i < (half + 1) * HS; ++i) {
+      forget(ry[i]);
+    }
+    {
+      float t[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) t[k] = h[k];
+      for (int k = 0; k < V; ++k) t[k] = h[k];
 #pragma unroll
-    for (int i = 0; i < (half + 1) * HS - 1; ++i)
+      for (int i = 0; i < (half + 1) * HS - 1; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          if (i >= half * HS) prev[i - half * HS][k] = t[k];
+          t[k] = fmaf(a[i][k], t[k], v[i][k]);
+        }
+#pragma unroll
+      for (int k = 0; k < V; ++k) prev[HS - 1][k] = t[k];
+    }
+#pragma unroll
+    for (int i = (half + 1) * HS - 1; i >= half * HS; --i) {
+      float ox_[V], od[V], og[V];
+      f32x4 kd, kn;
+      if constexpr (KIND != 0) kd = kept[0][i][threadIdx.x];
+      if constexpr (NORM) kn = kept[1][i][threadIdx.x];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        if (i >= half * HS) prev[i - half * HS][k] = t[k];
-        t[k] = fmaf(a[i][k], t[k], v[i][k]);
+        const float G = Four<T>::get(ry[i], k) + K[k];
+        const float ak = a[i][k];
+        K[k] = ak * G;
+        if constexpr (KIND == 0) {
+          ox_[k] = G;
+          od[k] = G * prev[i - half * HS][k];
+        } else {
+          float in = -prev[i - half * HS][k];
+          ox_[k] = G;
+          if constexpr (KIND == 2 || NORM) ox_[k] *= b[i][k];
+          if constexpr (KIND == 2) og[k] = G * v[i][k] * (1.f - (NORM ? b[i][k] * kn[k] : b[i][k]));
+          if constexpr (NORM) in = fmaf(v[i][k] * kn[k], ak * kn[k], in);   // v a / m
+          float du = K[k] * in;
+          if (ragged && r0 + i >= rows) du = 0.f;   // no part of grad_decay_a, also where the state is NaN
+          sum[k] = fmaf(du, sp[i][k], sum[k]);
+          od[k] = du * scale[k] * kd[k];
+        }
       }
-#pragma unroll
-    for (int k = 0; k < V; ++k) prev[HS - 1][k] = t[k];
-  }
-#pragma unroll
-  for (int i = (half + 1) * HS - 1; i >= half * HS; --i) {
-    float ox_[V], od[V], og[V];
-    f32x4 kd, kn;
-    if constexpr (KIND != 0) kd = kept[0][i][threadIdx.x];
-    if constexpr (NORM) kn = kept[1][i][threadIdx.x];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const float G = Four<T>::get(ry[i], k) + K[k];
-      const float ak = a[i][k];
-      K[k] = ak * G;
-      if constexpr (KIND == 0) {
-        ox_[k] = G;
-        od[k] = G * prev[i - half * HS][k];
-      } else {
-        float in = -prev[i - half * HS][k];
-        ox_[k] = G;
-        if constexpr (KIND == 2 || NORM) ox_[k] *= b[i][k];
-        if constexpr (KIND == 2) og[k] = G * v[i][k] * (1.f - (NORM ? b[i][k] * kn[k] : b[i][k]));
-        if constexpr (NORM) in = fmaf(v[i][k] * kn[k], ak * kn[k], in);   // v a / m
-        float du = K[k] * in;
-        if (ragged && r0 + i >= rows) du = 0.f;   // no part of grad_decay_a, also where the state is NaN
-        sum[k] = fmaf(du, sp[i][k], sum[k]);
-        od[k] = du * scale[k] * kd[k];
-      }
+      gx.store(i, ox_);
+      if constexpr (KIND == 0) ga.store(i, od);
+      else gd.store(i, od);
+      if constexpr (KIND == 2) gg.store(i, og);
     }
-    gx.store(i, ox_);
-    if constexpr (KIND == 0) ga.store(i, od);
-    else gd.store(i, od);
-    if constexpr (KIND == 2) gg.store(i, og);
-  }
   }
   if constexpr (KIND != 0) {
 #pragma unroll
@@ -329,8 +329,10 @@ hipError_t launch_scan_bwd(const gdr_scan_bwd_args& a, hipStream_t s) {
   }
   BwdP p{a.B, a.T, a.C, a.normalise, (int)chains_of(a.B, a.C), (a.C + kTileC - 1) / kTileC, (int)tiles_t(a.T, kBwdWaves),
          team_of(a.alpha != nullptr, a.io_dtype), a.x, a.x_exp, a.alpha, a.decay_x, a.decay_a, a.gate_x, ckpt, a.grad_y, a.grad_h, a.grad_x, a.grad_alpha,
-         a.grad_decay_x, a.grad_gate_x, a.grad_h0, a.alpha ? nullptr : (float*)rest,
+         a.grad_decay_x, a.grad_gate_x, a.grad_h0, (float*)rest,
          chains_at(ws + first, a.B, a.T, a.C, kBwdWaves)};
+  const int rows = p.nt * a.B;
+  if (rows == 1) p.part = a.grad_decay_a;   // one partial row is the sum
   const size_t io = a.io_dtype == GDR_BF16 ? 2 : 4;
   const bool vec = a.C % 4 == 0 && vec4_ok(a.x, a.x_exp ? 1 : io) && vec4_ok(a.alpha, 4) && vec4_ok(a.decay_x, io) &&
                    vec4_ok(a.gate_x, io) && vec4_ok(a.grad_y, io) && vec4_ok(a.grad_x, io) && vec4_ok(a.grad_alpha, 4) &&
@@ -339,8 +341,8 @@ hipError_t launch_scan_bwd(const gdr_scan_bwd_args& a, hipStream_t s) {
     e = a.x_exp ? launch_kind<__bf16, Code8>(p, vec, s) : launch_kind<__bf16, __bf16>(p, vec, s);
   else
     e = a.x_exp ? launch_kind<float, Code8>(p, vec, s) : launch_kind<float, float>(p, vec, s);
-  if (e != hipSuccess || a.alpha) return e;
-  hipLaunchKernelGGL(sum_kernel, dim3((a.C + 15) / 16), dim3(1024), 0, s, p.part, a.grad_decay_a, p.nt * a.B, a.C);
+  if (e != hipSuccess || a.alpha || rows == 1) return e;
+  hipLaunchKernelGGL(sum_kernel, dim3((a.C + 15) / 16), dim3(1024), 0, s, p.part, a.grad_decay_a, rows, a.C);
   return hipGetLastError();
 }
 

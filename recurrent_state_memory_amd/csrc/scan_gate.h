@@ -32,9 +32,11 @@ __device__ inline float softplus(float d, float& w, float& s) {
   w = __builtin_amdgcn_exp2f(-__builtin_fabsf(d) * kLog2e);
   s = 1.f + w;
   const float c = w - (s - 1.f);
-  // max(d, 0) on the bits, one instruction (fmaxf takes two); a NaN d comes through w
-  const int bits = __float_as_int(d);
-  return __int_as_float(bits > 0 ? bits : 0) + fmaf(__builtin_amdgcn_logf(s), kLn2, c);
+  // max(d, 0) on the bits, one instruction (fmaxf takes two), and at most the largest
+  // float, so that a = 0 of an infinite d has no 0 * Inf in its gradients; a NaN d
+  // comes through w
+  const int bits = __float_as_int(d), pos = bits > 0 ? bits : 0;
+  return __int_as_float(pos < 0x7f7fffff ? pos : 0x7f7fffff) + fmaf(__builtin_amdgcn_logf(s), kLn2, c);
 }
 __device__ inline float softplus(float d) {
   float w, s;

@@ -71,9 +71,10 @@ def gate_bounds(q, g):
     softplus: exp (its argument's rounding |d| E log2 e is below sp's scale: the
     result moves by w/(1+w) of it), the log and two additions: 8 E.  u = A sp: 9
     E.  a = exp2(-u log2 e): the argument's relative error 11 E moves a by 11 u E,
-    the exp 2 E.  m = 1 - a^2: below z = 1/4 the series' error is z's, 9 E, and 8
-    of its own (the last term left out, z^6/5040, is below 1 E); above, a^2's
-    relative error 2 (11 u + 2) + 1 divided by m >= 0.22 with a^2 <= 0.78.  b takes
+    the exp 2 E.  m = 1 - a^2: below z = 2u = 1/2 as z times a fit, whose error is z's,
+    9 E, and at most 9 of its own (the fit 1.4, its evaluation); above, a^2's relative
+    error 2 (11 u + 2) + 1 divided by m >= 0.39 with a^2 <= 0.61.  (The bound changes
+    over between z = 0.2 and 0.3, where the second is the larger.)  b takes
     half of m's, 2 for the sqrt, 2 for products; the sigmoid 2 (|g| + 1) for its
     argument and exp, 1 for 1 + e, 2 for the rcp."""
     if q["u"] is None:

@@ -234,6 +234,35 @@ def test_scan_saturated_gates():
     gr = gdr.gdr_scan_bwd_gated(dev(x), dev(d), dev(A), dev(x), gate_x=dev(g), h0=dev(np.ones((1, 4))))
     for n, t in gr.items():
         assert torch.isfinite(t).all(), n
+    # an infinite pre-activation is the reset that a very large one is, gradients included
+    d[0, 7], d[0, 3] = np.inf, 3e38
+    dm = np.where(np.isinf(d) & (d > 0), np.float32(3e38), d)
+    outs = []
+    for dd in (d, dm):
+        y, h, ck = gdr.gdr_scan_fwd_gated(dev(x), dev(dd), dev(A), gate_x=dev(g), h0=dev(np.ones((1, 4))), return_ckpt=True)
+        g2 = gdr.gdr_scan_bwd_gated(dev(x), dev(dd), dev(A), dev(x), gate_x=dev(g), ckpt=ck)
+        outs.append([y, h, *g2.values()])
+    assert all(torch.isfinite(a).all() and torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_scan_padded_batch():
+    """Padding (decay_x = -Inf with normalise) behind rows of different lengths: the
+    final states and every gradient are those of the rows alone, and the padding's are 0."""
+    import torch
+    d = scan_inputs((3, 300), 70, "bf16", "gate+norm", seed=70)
+    lens = (300, 129, 37)
+    for b, n in enumerate(lens):
+        d["kw"]["d"][b, n:] = -np.inf
+        d["dy"][b, n:] = 0.0
+    _, h, _ = call_fwd(d, "bf16", h0=dev(d["h"]))
+    g = call_bwd(d, "bf16", h0=dev(d["h"]), grad_h=dev(d["dh"]))
+    for b, n in enumerate(lens):
+        one = dict(x=d["x"][b:b + 1, :n], dy=d["dy"][b:b + 1, :n], kw=dict(d["kw"], d=d["kw"]["d"][b:b + 1, :n], g=d["kw"]["g"][b:b + 1, :n]))
+        _, h1, _ = call_fwd(one, "bf16", h0=dev(d["h"][b:b + 1]))
+        g1 = call_bwd(one, "bf16", h0=dev(d["h"][b:b + 1]), grad_h=dev(d["dh"][b:b + 1]))
+        assert torch.equal(h[b], h1[0]) and torch.equal(g["h0"][b], g1["h0"][0])
+        for k in ("x", "decay_x", "gate_x"):
+            assert torch.equal(g[k][b, :n], g1[k][0]) and (g[k][b, n:] == 0).all(), (b, k)
 
 
 def test_scan_nan_stays_in_its_channel():
