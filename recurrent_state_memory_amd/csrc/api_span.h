@@ -44,6 +44,4 @@ inline bool spans_apart(const Span (&ins)[NI], const Span (&outs)[NO], int same_
   return true;
 }
 
-inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 }  // namespace gdr
