@@ -68,25 +68,30 @@ def scan_inputs(lead, C, io, kind, seed, reset=False):
 def gate_bounds(q, g):
     """Relative errors (in E) of a and of b from their evaluation in fp32.
 
-    softplus: exp (its argument's rounding |d| E log2 e is below sp's scale: the
-    result moves by w/(1+w) of it), the log and two additions: 8 E.  u = A sp: 9
-    E.  a = exp2(-u log2 e): the argument's relative error 11 E moves a by 11 u E,
-    the exp 2 E.  m = 1 - a^2: below z = 2u = 1/2 as z times a fit, whose error is z's,
-    9 E, and at most 9 of its own (the fit 1.4, its evaluation); above, a^2's relative
-    error 2 (11 u + 2) + 1 divided by m >= 0.39 with a^2 <= 0.61.  (The bound changes
-    over between z = 0.2 and 0.3, where the second is the larger.)  b takes
-    half of m's, 2 for the sqrt, 2 for products; the sigmoid 2 (|g| + 1) for its
-    argument and exp, 1 for 1 + e, 2 for the rcp."""
+    softplus: for d >= 0 it is at least ln 2, and w = e^-|d| enters it by less than its
+    own size: exp, log and two additions, 8 E.  For d < 0 it is about w, whose exponent
+    |d| log2 e is rounded once (E) from a constant that is off by 0.22 E: ln 2 |d| log2 e
+    1.22 E = 1.22 |d| E on top, N = 1.3 |d| below.  u = A sp: 9 + N.  a = exp2(-u log2 e):
+    the argument's relative error 11 + N moves a by (11 + N) u, the exp 2 E.  m = 1 - a^2:
+    below z = 2u = 1/2 as z times a fit, whose error is z's, 9 + N, and at most 9 of its
+    own (the fit 1.4, its evaluation); above, a^2's relative error 2 ((11 + N) u + 2) + 1
+    divided by m >= 0.39 with a^2 <= 0.61.  (The bound changes over between z = 0.2 and
+    0.3, where the second is the larger.)  b takes half of m's, 2 for the sqrt, 2 for
+    products; the sigmoid 2 (|g| + 1) for its argument and exp, 1 for 1 + e, 2 for the
+    rcp."""
     if q["u"] is None:
         return 0.0, 0.0
     u = q["u"]
-    ra = 11 * u + 2
+    with np.errstate(divide="ignore"):
+        d = np.log(q["sig"]) - np.log1p(-q["sig"])
+    q["neg"] = 1.3 * np.where(d < 0, np.minimum(-d, 200.0), 0.0)
+    ra = (11 + q["neg"]) * u + 2
     rb = np.zeros_like(u)
     if q["m"] is not None:
         series = 2 * u < 0.3
         with np.errstate(divide="ignore", invalid="ignore"):
             direct = (2 * ra + 1) * q["a"] ** 2 / q["m"] + 1
-        q["rm"] = np.where(series, 18.0, np.minimum(direct, 1e6))
+        q["rm"] = np.where(series, 18.0 + q["neg"], np.minimum(direct, 1e6))
         q["rm"] = np.where((2 * u > 0.2) & series, np.maximum(q["rm"], direct), q["rm"])
         rb = rb + q["rm"] / 2 + 4
     if q["s"] is not None:

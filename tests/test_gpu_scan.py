@@ -97,9 +97,10 @@ def check_bwd(d, io, h0, dh, what, x8=False, ck=False):
     edu = NG * a * inner + Ga * a * ((ra + 4) * E * inner + ei)
     A = d["kw"]["A"].astype(np.float64)
     check(what + " dd", g["decay_x"], r["dd"],
-          edu * A * q["sig"] + np.abs(r["dd"]) * (12 * E + hs) + np.abs(r["dd"]) * 3 * E * np.abs(d["kw"]["d"]))
-    # the sum over tokens: at most 64 + (B T) / 32 additions behind any value
-    k = min(B * T, 64 + B * T // 32) + 10
+          edu * A * q["sig"] + np.abs(r["dd"]) * (12 * E + hs + q["neg"] * E))
+    # the sum over tokens: at most 64 + (B T) / 32 additions behind any value; the
+    # softplus' own error beside them
+    k = min(B * T, 64 + B * T // 32) + 10 + q["neg"]
     check(what + " dA", g["decay_a"], r["dA"], (edu * q["sp"] + np.abs(r["du"] * q["sp"]) * k * E).sum((0, 1)))
 
 
