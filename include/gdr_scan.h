@@ -77,8 +77,9 @@ gdr_status gdr_scan_fwd(const gdr_scan_args *args, void *stream);
  *   dL/du = G a (b x a / (1 - a^2) [if normalise] - h_{t-1}),
  *   grad_decay_x = dL/du decay_a sigmoid(decay_x),
  *   grad_decay_a = sum over (b, t) of dL/du softplus(decay_x).
- * The quotient is taken as 0 where 1 - a^2 is below 2^-120 (the term vanishes with
- * its root; at decay_a = 0 it has no limit).
+ * b has the forward's own sqrt(1 - a^2).  Where 1 - a^2 is below fp32's least normal
+ * number 2^-126, the quotient is taken with 2^63 for the inverse of that root, so it is 0
+ * where the root is (the term vanishes with it; at decay_a = 0 it has no limit).
  * States inside a block of 32 tokens are computed again from ckpt (as
  * gdr_scan_fwd wrote it); without ckpt the whole recurrence is run again from
  * h0, and ckpt and h0 are not given together.  x may be 8-bit: then x_exp holds

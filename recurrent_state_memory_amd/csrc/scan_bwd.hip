@@ -26,9 +26,9 @@
 namespace gdr {
 namespace scan {
 
-// Below this, 1 - a^2 counts as 0, and so does the term that it divides, which
-// vanishes with its root.
-constexpr float kLeastM = 0x1p-120f;
+// The most that 1 / n counts as, n = sqrt(1 - a^2): that of n^2 = 2^-126, fp32's least
+// normal number, so that the term that n^2 divides vanishes where n, and with it b x, is 0.
+constexpr float kMostInv = 0x1p63f;
 
 struct BwdP {
   int B, T, C, normalise;
@@ -133,10 +133,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
         kd[k] = sig;
         a[i][k] = decay(A, sp[i][k]);
         if constexpr (KIND == 2) b[i][k] = sigmoid(Four<T>::get(rg[i], k));
-        if constexpr (NORM) {   // 1 / n, and n = m / n
-          const float m = one_minus_sq(A, sp[i][k], a[i][k]);
-          kn[k] = m > kLeastM ? __builtin_amdgcn_rsqf(m) : 0.f;
-          b[i][k] = KIND == 2 ? b[i][k] * (m * kn[k]) : m * kn[k];
+        if constexpr (NORM) {   // n, as the forward has it, and 1 / n
+          const float n = __builtin_amdgcn_sqrtf(one_minus_sq(A, sp[i][k], a[i][k]));
+          kn[k] = __builtin_fminf(__builtin_amdgcn_rcpf(n), kMostInv);
+          b[i][k] = KIND == 2 ? b[i][k] * n : n;
         }
       }
     }
