@@ -77,6 +77,8 @@ gdr_status gdr_scan_fwd(const gdr_scan_args *args, void *stream);
  *   dL/du = G a (b x a / (1 - a^2) [if normalise] - h_{t-1}),
  *   grad_decay_x = dL/du decay_a sigmoid(decay_x),
  *   grad_decay_a = sum over (b, t) of dL/du softplus(decay_x).
+ * 1 - sigmoid is formed without the difference, so grad_gate_x is accurate relative to
+ * itself for open gates too (from gate_x = 87 on it counts as 2^-126).
  * b has the forward's own sqrt(1 - a^2).  Where 1 - a^2 is below fp32's least normal
  * number 2^-126, the quotient is taken with 2^63 for the inverse of that root, so it is 0
  * where the root is (the term vanishes with it; at decay_a = 0 it has no limit).

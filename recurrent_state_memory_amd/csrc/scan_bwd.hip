@@ -6,16 +6,20 @@
 // tile to tile with the last tiles first.  G_t = grad_y_t + K_{t+1}, so a run of
 // tokens takes K to P K + Q with P the same product of decays.
 //
-// A thread keeps a, b, b x and the softplus of its 32 elements in registers, and
-// sigmoid(decay_x) and 1 / n, n = sqrt(1 - a^2), in LDS (its own 16 bytes a token, no
-// barrier), so that everything is evaluated once; b = s n gives back s = b / n.
+// A thread keeps a, b x, the softplus and the input gate of its 32 elements in
+// registers, and sigmoid(decay_x) and n = sqrt(1 - a^2) in LDS (its own 16 bytes a
+// token, no barrier), so that no exponential is evaluated twice.  The input gate is
+// kept as the pair of s and 1 - s (scan_gate.h): grad_gate_x has the factor 1 - s, which
+// from s alone, or from b = s n, has no correct digit left behind gate_x = 17.  That and
+// 1 / n taken again from n cost 4 % (223 to 231 us below); the exponential taken again from
+// gate_x instead cost a little more, and spilled in fp32.
 //
 // With given decays it is bound by HBM (8 x 4096 x 2048: 944 MB of least traffic in
-// 181 us).  Gated in bf16 (882 MB, x in 8 bits) it takes 223 us: about 71 vector
+// 181 us).  Gated in bf16 (882 MB, x in 8 bits) it takes 231 us: about 75 vector
 // instructions an element keep the vector units busy in two thirds of the cycles at
-// two waves per SIMD (the registers' limit).  At 235 us, four tokens a thread at four
-// waves per SIMD executed more and took 249, and workgroups that stay for further
-// tiles 242.
+// two waves per SIMD (the registers' limit).  Before the gate was kept as a pair, four
+// tokens a thread at four waves per SIMD took 249 us and workgroups that stay for further
+// tiles 242, against 235 then.
 //
 // grad_decay_a sums over all tokens: registers, lane groups, waves (one LDS pass
 // in a fixed order), then one partial row per tile that sum_kernel adds up, again
@@ -55,7 +59,7 @@ template <typename T, typename X, int KIND, bool NORM, bool VEC>
 __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   constexpr bool kCodes = !__is_same(X, T);
   __shared__ Joins<kBwdWaves> j;   // of the maps of K: later tokens first
-  constexpr int kKept = (KIND != 0 ? 1 : 0) + (NORM ? 1 : 0);   // sigmoid(decay_x), 1 / sqrt(1 - a^2)
+  constexpr int kKept = (KIND != 0 ? 1 : 0) + (NORM ? 1 : 0);   // sigmoid(decay_x), sqrt(1 - a^2)
   __shared__ f32x4 kept[kKept == 0 ? 1 : kKept][kKept == 0 ? 1 : S][kKept == 0 ? 1 : 64 * kBwdWaves];
   const Place q = take_place(p.C, p.nchain, p.nct, p.nt, p.team, p.ch.ticket);
   const int tile = p.nt - 1 - q.tt;         // the last tokens come first
@@ -112,8 +116,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   float k_in = 0.f;
   if (q.wave == 0 && q.tt < kSuper && p.grad_h && cc < C) k_in = p.grad_h[(size_t)q.b * C + cc];
 
-  // a and b; (P, H) forwards and (P, Q) backwards over the thread's run
-  float a[S][V], v[S][V], b[KIND == 2 || NORM ? S : 1][V], sp[KIND == 0 ? 1 : S][V], P[V], H[V], Q[V];
+  // a and v = b x; (P, H) forwards and (P, Q) backwards over the thread's run
+  float a[S][V], v[S][V], gate[KIND == 2 ? S : 1][V], sp[KIND == 0 ? 1 : S][V], P[V], H[V], Q[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     P[k] = 1.f;
@@ -132,12 +136,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
         sp[i][k] = softplus(Four<T>::get(rd[i], k), sig);
         kd[k] = sig;
         a[i][k] = decay(A, sp[i][k]);
-        if constexpr (KIND == 2) b[i][k] = sigmoid(Four<T>::get(rg[i], k));
-        if constexpr (NORM) {   // n, as the forward has it, and 1 / n
-          const float n = __builtin_amdgcn_sqrtf(one_minus_sq(A, sp[i][k], a[i][k]));
-          kn[k] = __builtin_fminf(__builtin_amdgcn_rcpf(n), kMostInv);
-          b[i][k] = KIND == 2 ? b[i][k] * n : n;
-        }
+        if constexpr (KIND == 2) gate[i][k] = gate_pair(Four<T>::get(rg[i], k));
+        if constexpr (NORM) kn[k] = __builtin_amdgcn_sqrtf(one_minus_sq(A, sp[i][k], a[i][k]));   // as the forward has it
       }
     }
     if constexpr (KIND != 0) kept[0][i][threadIdx.x] = kd;
@@ -146,7 +146,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
     for (int k = 0; k < V; ++k) {
       v[i][k] = Four<X>::get(rx[i], k);
       if constexpr (kCodes) v[i][k] *= xs[i];
-      if constexpr (KIND == 2 || NORM) v[i][k] *= b[i][k];
+      if constexpr (KIND == 2) {
+        v[i][k] *= gate_open(gate[i][k]);
+        forget(gate[i][k]);   // one register, not s beside it
+      }
+      if constexpr (NORM) v[i][k] *= kn[k];
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -239,9 +243,15 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
         } else {
           float in = -prev[i - half * HS][k];
           ox_[k] = G;
-          if constexpr (KIND == 2 || NORM) ox_[k] *= b[i][k];
-          if constexpr (KIND == 2) og[k] = G * v[i][k] * (1.f - (NORM ? b[i][k] * kn[k] : b[i][k]));
-          if constexpr (NORM) in = fmaf(v[i][k] * kn[k], ak * kn[k], in);   // v a / m
+          if constexpr (KIND == 2) {
+            ox_[k] *= gate_open(gate[i][k]);
+            og[k] = G * v[i][k] * gate_shut(gate[i][k]);
+          }
+          if constexpr (NORM) {
+            ox_[k] *= kn[k];
+            const float inv = __builtin_fminf(__builtin_amdgcn_rcpf(kn[k]), kMostInv);
+            in = fmaf(v[i][k] * inv, ak * inv, in);   // v a / m
+          }
           float du = K[k] * in;
           if (ragged && r0 + i >= rows) du = 0.f;   // no part of grad_decay_a, also where the state is NaN
           sum[k] = fmaf(du, sp[i][k], sum[k]);

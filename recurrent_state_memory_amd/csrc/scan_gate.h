@@ -15,6 +15,7 @@
 // channel.
 #pragma once
 #include <hip/hip_runtime.h>
+#include <stdint.h>
 
 namespace gdr {
 namespace scan {
@@ -64,6 +65,20 @@ __device__ inline float one_minus_sq(const Scale& A, float sp, float a) {
 __device__ inline float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -kLog2e));
 }
+
+// A gate's s = sigmoid(g) and 1 - s in one number, each with its full relative
+// accuracy: the smaller of the two, min(s, 1 - s) = e / (1 + e) with e = e^-|g|, and
+// g's sign, which says which one it is.  Its fraction x - floor(x) is 1 - s, that of its
+// negative s.  An open gate's number stays off 0, whose negative has no fraction: at
+// least 2^-126 (the larger of the bits, of which a closed gate's have the sign set), so a
+// closed gate's s is exactly 0.
+__device__ inline float gate_pair(float g) {
+  const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(g) * kLog2e);
+  const uint32_t bits = __float_as_uint(__builtin_copysignf(e * __builtin_amdgcn_rcpf(1.f + e), g));
+  return __uint_as_float(bits > 0x00800000u ? bits : 0x00800000u);
+}
+__device__ inline float gate_open(float pair) { return __builtin_amdgcn_fractf(-pair); }
+__device__ inline float gate_shut(float pair) { return __builtin_amdgcn_fractf(pair); }
 
 }  // namespace scan
 }  // namespace gdr
