@@ -289,7 +289,7 @@ template <int NW>
 struct Joins {
   float2 run[NW][kTileC];        // (P, H) of each wave, in the order of joining
   float2 pre[kSuper - 1][kTileC];   // of the tiles before this one in its super
-  float start[kTileC];           // the state before the tile
+  float start[kTileC];           // the state before the chain, then the tile
   float from[NW][kTileC];        // and before each wave
 };
 
@@ -321,12 +321,18 @@ __device__ inline Words<NW> look_ahead(const Chains& ch, const Place& q, int nt,
 // From the waves' maps (j.run, written before the call) to the state before each
 // wave, for channel `lane` (returned) and in j.from for the wave's own threads.
 // `pos` is the wave's place in the order of joining, `first` the state before the
-// chain (read by the last wave in order), `last` receives the state behind the
+// chain (in the last wave in order), `last` receives the state behind the
 // tile in that wave.  Every thread of the workgroup calls it.
+//
+// The chain's last tile may write its final state over the start state (h_out = h0), once
+// it has the maps of the tiles before it.  So `first` goes to LDS ahead of the barrier
+// that the map's publication follows: a load of it is complete by then, in whichever
+// wave it is.
 template <int NW>
 __device__ inline float join_tiles(Joins<NW>& j, const Chains& ch, const Place& q, const Words<NW>& words, int nt,
                                    int pos, float first, float& last) {
   const int lane = q.lane, r = q.tt % kSuper, su = q.tt / kSuper;
+  if (pos == q.nw - 1) j.start[lane] = first;
   __syncthreads();
   if (ch.ticket) {
     if (q.wave == 0 && r < kSuper - 1 && q.tt + 1 < nt) {
@@ -350,7 +356,7 @@ __device__ inline float join_tiles(Joins<NW>& j, const Chains& ch, const Place& 
 #pragma unroll
     for (int w = 0; w < NW; ++w)
       if (w < q.nw) own = after(j.run[w][lane], own);
-    const float in = su > 0 ? get_state(words.super, words.state) : first;
+    const float in = su > 0 ? get_state(words.super, words.state) : j.start[lane];
     const float h = fmaf(before.x, in, before.y);
     last = fmaf(own.x, h, own.y);
     if (r == kSuper - 1 && q.tt + 1 < nt) put_state(words.super + kTileC, last);
