@@ -421,6 +421,28 @@ constexpr Shape bwd_shape(int runs, int N) {
   if (N == 4 && runs <= 3 * 1024) return {1024, 3};
   return {1024, 0};   // norm_bwd_long_kernel
 }
+#define GDR_NORM_SHAPES(X) X(2, 1) X(4, 1) X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(512, 3)
+#define GDR_NORM_FWD_SHAPES(X) \
+  X(64, 2) X(64, 3) X(64, 4) X(128, 2) X(128, 3) X(256, 2) X(256, 3) X(256, 4) X(512, 4) X(1024, 4) X(1024, 8) X(1024, 16)
+#define GDR_NORM_BWD_SHAPES(X) X(128, 1) X(256, 1) X(512, 1) X(512, 2) X(1024, 1) X(1024, 2) X(1024, 3)
+
+// How often the launches below name a shape: each that a row has, once.
+constexpr int fwd_listed(Shape s) {
+#define GDR_COUNT(LL, NN) + (s.L == LL && s.NV == NN)
+  return 0 GDR_NORM_SHAPES(GDR_COUNT) GDR_NORM_FWD_SHAPES(GDR_COUNT);
+}
+constexpr int bwd_listed(Shape s) {
+  return 0 GDR_NORM_SHAPES(GDR_COUNT) GDR_NORM_BWD_SHAPES(GDR_COUNT);
+#undef GDR_COUNT
+}
+constexpr bool all_listed(int N) {
+  for (int runs = 1; runs <= 65536 / N; runs += runs < 64 ? 1 : 64) {   // shapes change after multiples of 64
+    const Shape f = fwd_shape(runs, false), k = fwd_shape(runs, true), b = bwd_shape(runs, N);
+    if (fwd_listed(f) != 1 || (k.NV > 0 && fwd_listed(k) != 1) || (b.NV > 0 && bwd_listed(b) != 1)) return false;
+  }
+  return true;
+}
+static_assert(all_listed(4) && all_listed(8), "every row's shape has a kernel");
 // Whether some row of runs of N values has this shape.
 constexpr bool bwd_has(int N, int L, int NV) {
   for (int runs = 1; runs <= 3 * 1024; ++runs)
@@ -428,7 +450,7 @@ constexpr bool bwd_has(int N, int L, int NV) {
   return false;
 }
 constexpr bool fwd_has(int N, int L, int NV, bool ck) {
-  for (int runs = 1; runs <= 65536 / N; runs += runs < 64 ? 1 : 64)   // shapes change after multiples of 64
+  for (int runs = 1; runs <= 65536 / N; runs += runs < 64 ? 1 : 64)
     if (fwd_shape(runs, ck).L == L && fwd_shape(runs, ck).NV == NV) return true;
   return false;
 }
@@ -445,11 +467,6 @@ size_t bwd_workspace(int64_t R, int D) {
   (void)R;
   return (size_t)kParts * 2 * D * sizeof(float);
 }
-
-#define GDR_NORM_SHAPES(X) X(2, 1) X(4, 1) X(8, 1) X(16, 1) X(32, 1) X(64, 1) X(512, 3)
-#define GDR_NORM_FWD_SHAPES(X) \
-  X(64, 2) X(64, 3) X(64, 4) X(128, 2) X(128, 3) X(256, 2) X(256, 3) X(256, 4) X(512, 4) X(1024, 4) X(1024, 8) X(1024, 16)
-#define GDR_NORM_BWD_SHAPES(X) X(128, 1) X(256, 1) X(512, 1) X(512, 2) X(1024, 1) X(1024, 2) X(1024, 3)
 
 template <typename T>
 static hipError_t fwd(const gdr_norm_args& a, hipStream_t s) {
