@@ -62,6 +62,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, 2) void scan_bwd_kernel(BwdP p) {
   constexpr int kKept = (KIND != 0 ? 1 : 0) + (NORM ? 1 : 0);   // sigmoid(decay_x), sqrt(1 - a^2)
   __shared__ f32x4 kept[kKept == 0 ? 1 : kKept][kKept == 0 ? 1 : S][kKept == 0 ? 1 : 64 * kBwdWaves];
   const Place q = take_place(p.C, p.nchain, p.nct, p.nt, p.team, p.ch.ticket);
+  if (q.chain < 0) return;
   const int tile = p.nt - 1 - q.tt;         // the last tokens come first
   const int C = p.C, t0 = tile * kBwdWaves * GDR_SCAN_BLOCK;
   const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);

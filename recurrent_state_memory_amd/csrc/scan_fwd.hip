@@ -40,6 +40,7 @@ __global__ __launch_bounds__(64 * kFwdWaves) void scan_fwd_kernel(FwdP p) {
   constexpr bool kCodes = !__is_same(X, T);
   __shared__ Joins<kFwdWaves> j;
   const Place q = take_place(p.C, p.nchain, p.nct, p.nt, p.team, p.ch.ticket);
+  if (q.chain < 0) return;
   const int C = p.C, t0 = q.tt * kFwdWaves * GDR_SCAN_BLOCK;
   const int rows = min(q.nw * GDR_SCAN_BLOCK, p.T - t0);   // of the tile that exist
   const int r0 = q.wave * GDR_SCAN_BLOCK + q.grp * S;      // the thread's first row

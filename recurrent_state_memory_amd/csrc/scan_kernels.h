@@ -35,6 +35,22 @@ constexpr size_t chains_of(int B, int C) { return (size_t)B * ((C + kTileC - 1) 
 constexpr size_t kMaxTiles = (size_t)1 << 23;
 constexpr bool too_many_tiles(int B, int T, int C) { return chains_of(B, C) * tiles_t(T, kBwdWaves) >= kMaxTiles; }
 
+// Which tile the number drawn stands for: chains are taken in teams, and within a team
+// the first tiles of all its chains come before the second ones, so a tile's number is
+// larger than those of the tiles before it in its chain.  There are nchain * nt numbers;
+// one behind them, which only a ticket that another call draws from as well can give,
+// stands for no tile (chain -1).
+struct Turn {
+  int chain, tt;   // chain, and the tile's place along it in the order of joining
+};
+__host__ __device__ constexpr Turn turn_of(uint32_t number, int nchain, int nt, int team_size) {
+  if (number >= (uint32_t)nchain * (uint32_t)nt) return Turn{-1, 0};
+  const uint32_t full = (uint32_t)team_size * (uint32_t)nt, team = number / full, in = number - team * full;
+  const uint32_t left = (uint32_t)nchain - team * (uint32_t)team_size;   // of the last team
+  const uint32_t size = left < (uint32_t)team_size ? left : (uint32_t)team_size, tt = in / size;
+  return Turn{(int)(team * (uint32_t)team_size + (in - tt * size)), (int)tt};
+}
+
 // Workspace of the forward and of the backward (bytes; 0: none needed).
 size_t fwd_workspace(int B, int T, int C);
 size_t bwd_workspace(int B, int T, int C, bool gated, bool ckpt);

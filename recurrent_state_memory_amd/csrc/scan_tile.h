@@ -18,8 +18,9 @@
 // Tile numbers are drawn from a ticket.  Chains are taken in teams, and a team's
 // first tiles come before its second ones: a tile waits only for tiles whose
 // workgroups have already started, and each publishes its map before it waits, so
-// every wait ends; were one not to (a workspace in use elsewhere), it gives up after
-// kSpinLimit polls with NaN.
+// every wait ends.  Where the workspace is in use elsewhere, against the rules, the
+// results are lost but nothing else is: a wait gives up after kSpinLimit polls with NaN,
+// and a number that no tile has ends its workgroup.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -191,7 +192,7 @@ struct Place {
 };
 
 // The next tile in ticket order (or the workgroup's own, when no tile waits for
-// another).  Contains barriers: every thread of the workgroup calls it.
+// another); chain -1: none.  Contains barriers: every thread of the workgroup calls it.
 __device__ inline Place take_place(int C, int nchain, int nct, int nt, int team_size, uint32_t* ticket) {
   __shared__ uint32_t drawn;
   uint32_t tile = blockIdx.x;
@@ -201,11 +202,10 @@ __device__ inline Place take_place(int C, int nchain, int nct, int nt, int team_
     tile = drawn;
   }
   tile = __builtin_amdgcn_readfirstlane(tile);
+  const Turn turn = turn_of(tile, nchain, nt, team_size);
   Place q;
-  const uint32_t full = (uint32_t)team_size * nt, team = tile / full, in = tile - team * full;
-  const uint32_t size = min((uint32_t)team_size, nchain - team * team_size);
-  q.tt = in / size;
-  q.chain = team * team_size + (in - q.tt * size);
+  q.tt = turn.tt;
+  q.chain = turn.chain;
   q.b = q.chain / nct;
   q.c0 = (q.chain % nct) * kTileC;
   q.lane = threadIdx.x & 63;
