@@ -37,3 +37,9 @@ def test_norm_fwd_rows_of_two_waves(R, D, io):
 @pytest.mark.parametrize("R,D", SHAPES)
 def test_norm_bwd_rows_of_two_waves(R, D, io, x8):
     check_norm_bwd(R, D, io, x8)
+
+
+@pytest.mark.parametrize("R,D", [(3, 10000), (300, 9001)])
+def test_norm_bwd_three_runs_of_1024_threads(R, D):
+    for x8 in (False, True):
+        check_norm_bwd(R, D, "f32", x8)
