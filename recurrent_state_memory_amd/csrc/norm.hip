@@ -190,24 +190,21 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(gdr_norm_bwd_args p, flo
   constexpr int TH = 1024;
   constexpr int N = Run<T>::N;
   constexpr int kPer = TH / L;
-  constexpr bool kHold = NV * N <= 16;   // weights stay in registers
   constexpr int kJoin = SUMS && L < TH ? TH / (L < 64 ? 64 : L) : 1;   // sets of sums that meet in LDS
   __shared__ RowSums<TH, 2> sums;
   __shared__ float join[kJoin][kJoin > 1 ? L * N : 1];
   int turn = 0;
   const int l = threadIdx.x % L, D = p.D;
   const int64_t step = (int64_t)gridDim.x * kPer;
-  float sw[SUMS ? NV : 1][N], sb[SUMS ? NV : 1][N], w[kHold ? NV : 1][N];
+  float sw[SUMS ? NV : 1][N], sb[SUMS ? NV : 1][N], w[NV][N];   // the weights stay in registers
   if constexpr (SUMS) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int k = 0; k < N; ++k) sw[j][k] = sb[j][k] = 0.f;
   }
-  if constexpr (kHold) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_weight<N>(p, (j * L + l) * N, w[j]);
-  }
+  for (int j = 0; j < NV; ++j) load_weight<N>(p, (j * L + l) * N, w[j]);
   BwdRow<T, CODES, NV> r;
   int64_t row = (int64_t)blockIdx.x * kPer + threadIdx.x / L;
   if (row < p.R) load_row<T, CODES, L, NV>(p, row, l, r);
@@ -222,11 +219,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(gdr_norm_bwd_args p, flo
       for (int j = 0; j < NV; ++j) {
         float x[N];
         r.get_x(j, x);
-        if constexpr (!kHold) load_weight<N>(p, (j * L + l) * N, w[0]);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           // behind the row's end grad_y and the weight read as 0
-          const float dy = Run<T>::get(r.y[j], k), g = dy * w[kHold ? j : 0][k];
+          const float dy = Run<T>::get(r.y[j], k), g = dy * w[j][k];
           const float xh = (x[k] - r.mean) * r.rstd;
           s[0] += g;
           s[1] = fmaf(g, xh, s[1]);
@@ -246,11 +242,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(gdr_norm_bwd_args p, flo
         const int c0 = (j * L + l) * N;
         float x[N], o[N];
         r.get_x(j, x);
-        if constexpr (!kHold) load_weight<N>(p, c0, w[0]);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const float xh = (x[k] - r.mean) * r.rstd;
-          o[k] = r.rstd * (fmaf(Run<T>::get(r.y[j], k), w[kHold ? j : 0][k], -s[0]) - xh * s[1]);
+          o[k] = r.rstd * (fmaf(Run<T>::get(r.y[j], k), w[j][k], -s[0]) - xh * s[1]);
         }
         Run<T>::store((T*)p.grad_x + (size_t)row * D + c0, D - c0, o);
       }
