@@ -12,8 +12,8 @@
  *     grad_weight = sum over rows of grad_y xh,  grad_bias = sum over rows of grad_y
  *
  * Sizes: any R >= 1 rows of 1 <= D <= 65536, R * D < 2^40, R < 2^31.  Every
- * pointer is aligned to its element; rows whose D is a multiple of 16 bytes, in
- * 16-byte aligned buffers, move 16 bytes at a time.  Outputs overlap neither
+ * pointer is aligned to its element; rows move 16 bytes at a time, fastest where they
+ * begin at multiples of 16 bytes.  Outputs overlap neither
  * inputs nor each other (GDR_ERR_ARG).  Sums are fp32, in an order that depends
  * on the sizes alone; y and grad_x are rounded once (RNE) to io_dtype.  NaN and
  * Inf stay within their row (and reach grad_weight and grad_bias).

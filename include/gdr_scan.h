@@ -18,13 +18,16 @@
  *
  * Decays: alpha in [0, 1] and decay_a >= 0 are not checked.  A decay of 0
  * (alpha = 0, decay_x = +Inf) is an exact reset: it starts a new sequence packed
- * behind another.  alpha = 1 with x = 0, or decay_x = -Inf with normalise, leaves the
- * state as it is (padding).  NaN, and Inf in x, h0 and the gradients, propagate.
+ * behind another.  alpha = 1 with x = 0, or decay_x = -Inf with normalise and a finite x,
+ * leaves the state as it is (padding).  NaN, and Inf in x, h0 and the gradients, propagate
+ * along their channel: what depends on them is not finite, through a reset (0 times Inf)
+ * as well.  An Inf may come out as NaN: states pass on through products of many decays,
+ * which may underflow.
  *
  * Sizes: any B, C and T >= 1 with B * T * C < 2^40, C <= 2^18 and
  * B * ceil(C/64) * ceil(T/128) < 2^23.  Every pointer is
- * aligned to its element; rows whose C is a multiple of 4, in buffers aligned
- * to 4 elements, move 4 channels at a time.  Outputs overlap neither inputs nor
+ * aligned to its element; channels move 4 at a time, fastest where C is a multiple of 4
+ * and the buffers are aligned to 4 elements.  Outputs overlap neither inputs nor
  * each other (GDR_ERR_ARG), except that h_out may equal h0 (and the step's
  * h_out its h).  All arithmetic and states are fp32; y and the gradients of the
  * activations are rounded once (RNE) to io_dtype.  Results do not depend on

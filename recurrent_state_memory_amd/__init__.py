@@ -872,7 +872,9 @@ def gdr_scan_fwd(x, alpha, *, h0=None, y=None, h_out=None, ckpt=None, return_sta
     [B,C] or None (zero).  Returns (y [B,T,C] like x, h_out fp32 [B,C], ckpt) --
     h_out None unless ``return_state`` or given (it may be h0), ckpt fp32
     [B,ceil(T/32),C] (the states before each 32 tokens, for the backward) None
-    unless ``return_ckpt`` or given.
+    unless ``return_ckpt`` or given.  The workspace (``gdr_scan_fwd_workspace``
+    bytes) is allocated here unless a large enough uint8 tensor is passed, which
+    serves one call at a time.
     """
     if alpha is None:
         raise ValueError("gdr: alpha is required")
@@ -955,7 +957,8 @@ def gdr_scan_bwd(x, alpha, grad_y, *, h0=None, grad_h=None, ckpt=None, need_grad
     recurrence.  x may be an 8-bit checkpoint, the tuple ``gdr_ckpt8_pack``
     returned.  Returns a dict: x (like grad_y), alpha (fp32) and, when
     ``need_grad_h0``, h0 (fp32).  The workspace (``gdr_scan_bwd_workspace``
-    bytes) is allocated here unless a large enough uint8 tensor is passed.
+    bytes) is allocated here unless a large enough uint8 tensor is passed, which
+    serves one call at a time.
     """
     if alpha is None:
         raise ValueError("gdr: alpha is required")

@@ -6,8 +6,10 @@
 // in a wave, no barrier), a wave, or up to 1024 threads: few runs a thread, since what
 // is under way at once hides the latency (backward of 64 Mi bf16 elements in rows of
 // 8192: one run of each of 1024 threads 82 us, four of 256 142 us).  Both kernels are
-// bound by HBM: forward of 32768 x 2048 bf16 51 us (5.3 TB/s), with the 8-bit copy 69 us
-// (4.9 TB/s), backward 81 us (5.0 TB/s); per-head rows of 128 channels 57 and 81 us.
+// bound by HBM: forward of 32768 x 2048 bf16 53 us (5.1 TB/s), with the 8-bit copy 69 us
+// (4.9 TB/s), backward 79 us (5.1 TB/s); per-head rows of 128 channels 57 and 80 us.
+// Registers spill in the forward of fp32 rows above 32768 (512 x 65536: 110 us, 2.4 TB/s)
+// and, a few of them, in the backward from codes at the longest rows held.
 #include "chan_device.h"
 #include "norm_kernels.h"
 
@@ -291,7 +293,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(gdr_norm_bwd_args p, flo
 }
 
 // Rows longer than 1024 threads hold beside their sums: a workgroup a row, read twice,
-// the second time mostly from the caches (fp32 512 x 65536: 232 us; held in registers,
+// the second time mostly from the caches (fp32 512 x 65536: 229 us; held in registers,
 // which spilled, 537).
 template <typename T, bool CODES>
 __global__ __launch_bounds__(1024) void norm_bwd_long_kernel(gdr_norm_bwd_args p) {

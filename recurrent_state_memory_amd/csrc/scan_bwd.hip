@@ -11,11 +11,11 @@
 // token, no barrier), so that no exponential is evaluated twice.  The input gate is
 // kept as the pair of s and 1 - s (scan_gate.h): grad_gate_x has the factor 1 - s, which
 // from s alone, or from b = s n, has no correct digit left behind gate_x = 17.  That and
-// 1 / n taken again from n cost 4 % (223 to 231 us below); the exponential taken again from
+// 1 / n taken again from n cost 4 % (223 to 232 us below); the exponential taken again from
 // gate_x instead cost a little more, and spilled in fp32.
 //
 // With given decays it is bound by HBM (8 x 4096 x 2048: 944 MB of least traffic in
-// 181 us).  Gated in bf16 (882 MB, x in 8 bits) it takes 231 us: about 75 vector
+// 181 us).  Gated in bf16 (882 MB, x in 8 bits) it takes 232 us: about 75 vector
 // instructions an element keep the vector units busy in two thirds of the cycles at
 // two waves per SIMD (the registers' limit).  Before the gate was kept as a pair, four
 // tokens a thread at four waves per SIMD took 249 us and workgroups that stay for further

@@ -5,7 +5,7 @@
 // its run and writing the outputs, so every input is read and every gate evaluated
 // once.  Bound by HBM: with given decays 537 MB of least traffic (1 x 32785 x 2048)
 // take 103 us, the rate of a device copy; with the gates in the kernel (8 x 4096 x
-// 2048, 545 MB) 119 us, the vector units busy in two thirds of the cycles.  Each
+// 2048, 545 MB) 122 us, the vector units busy in two thirds of the cycles.  Each
 // thread per channel walking the tokens took 3.6 ms there, and tiles that hand the
 // state over one by one 140 us on the long sequence.
 #include "scan_gate.h"

@@ -9,7 +9,7 @@
 // - 1) exactly, log1p(w) = log s + c / s, and c / s = c to within 2^-24 of the
 // result: where c matters s is near 1).  And m is z q(z) below z = 2u = 1/2, with
 // q a degree-4 fit of (1 - e^-z) / z at the Chebyshev nodes of [0, 1/2] (relative
-// error 8.4e-8), and 1 - a a above it, where the rounding of a is at most 2 in m.
+// error 1.04e-7), and 1 - a a above it, where the rounding of a is at most 2 in m.
 // exp, log, rcp and sqrt are the hardware's, 1 ulp each.  The scan kernels spend
 // about as long on these as on memory, so the scale's products are formed once a
 // channel.

@@ -5,7 +5,7 @@ import pytest
 
 from _chan import E, check, dev, gate_bounds, half_step, scan_inputs
 from oracle import scan
-from test_gpu_scan import check_bwd, check_fwd
+from test_gpu_scan import call_fwd, check_bwd, check_fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,19 @@ def test_scan_step_of_many_states(N, C, kind, io):
     tol = q["a"] * np.abs(d["h"]) * (ra + 2) * E + np.abs(q["b"] * d["x"]) * (rb + 2) * E + E * np.abs(want)
     check(f"step {N}x{C} {kind}/{io} h", h, want, tol)
     check(f"step {N}x{C} {kind}/{io} y", y, want, tol + half_step(io) * np.abs(want))
+
+
+@pytest.mark.parametrize("kind", ["alpha", "gate+norm"])
+def test_scan_inf_stays_in_its_channel(kind):
+    """An Inf in x or in the start state: its channel is not finite from there on, and
+    every other value is the one without it, bit for bit."""
+    import torch
+    d = scan_inputs((2, 700), 70, "f32", kind, seed=10)
+    clean = call_fwd(d, "f32", h0=dev(d["h"]))
+    d["x"][1, 50, 33] = np.inf
+    d["h"][0, 5] = -np.inf
+    y, h, _ = call_fwd(d, "f32", h0=dev(d["h"]))
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[1, 50:, 33] = bad[0, :, 5] = True
+    assert not torch.isfinite(y[bad]).any() and torch.equal(y[~bad], clean[0][~bad])
+    assert torch.equal(torch.isfinite(h), ~bad[:, -1]) and torch.equal(h[~bad[:, -1]], clean[1][~bad[:, -1]])
