@@ -30,7 +30,8 @@
  * and the buffers are aligned to 4 elements.  Outputs overlap neither inputs nor
  * each other (GDR_ERR_ARG), except that h_out may equal h0 (and the step's
  * h_out its h).  All arithmetic and states are fp32; y and the gradients of the
- * activations are rounded once (RNE) to io_dtype.  Results do not depend on
+ * activations are rounded once (RNE) to io_dtype; exponentials below fp32's least normal
+ * number (of a pre-activation below -87) count as 0.  Results do not depend on
  * timing: no atomics add numbers.
  */
 #ifndef GDR_SCAN_H
