@@ -22,8 +22,14 @@ Entry points (same names as the C ABI):
 * ``gdr_norm_fwd``, ``gdr_norm_bwd`` -- layer norm (include/gdr_norm.h)
 * ``gdr_ckpt8_pack``, ``gdr_ckpt8_unpack`` -- activations kept in 8 bits for the
   backward (include/gdr_ckpt8.h)
+* ``gdr_conv_fwd``, ``gdr_conv_bwd``, ``gdr_conv_step`` -- short causal convolution
+  (include/gdr_conv.h)
+* ``gdr_ssm_fwd``, ``gdr_ssm_bwd``, ``gdr_ssm_step`` -- selective state space scan
+  (include/gdr_ssm.h)
+* ``gdr_gnorm_fwd``, ``gdr_gnorm_bwd`` -- group norm with its activation or gate
+  (include/gdr_gnorm.h)
 
-The channelwise operators (the last three lines) run on the device of their
+The channelwise operators (the last six lines) run on the device of their
 tensors, on its current stream or on ``stream``, and allocate what they return
 and their workspaces on that stream.
 """
@@ -674,6 +680,7 @@ def gdr_perm_fwd(q, k, v, w, src, beta, *, S0=None, o=None, S_out=None, return_s
 # ------------------------------------------------------------ channelwise operators
 GDR_SCAN_BLOCK = 32       # tokens between two saved states (include/gdr_scan.h)
 GDR_CKPT8_GROUP = 128     # values that share one exponent (include/gdr_ckpt8.h)
+GDR_SSM_BLOCK = 32        # tokens between two saved states (include/gdr_ssm.h)
 
 
 class ScanArgs(ctypes.Structure):
@@ -738,18 +745,99 @@ class Ckpt8UnpackArgs(ctypes.Structure):
                 ("code", _vp), ("exp", _vp), ("x", _vp)]
 
 
+class ConvArgs(ctypes.Structure):
+    """Mirror of ``gdr_conv_args`` (include/gdr_conv.h)."""
+    _fields_ = [
+        ("B", _i32), ("T", _i32), ("C", _i32), ("K", _i32), ("io_dtype", _i32), ("silu", _i32),
+        ("x", _vp), ("weight", _vp), ("bias", _vp), ("state", _vp), ("lens", _vp), ("y", _vp), ("state_out", _vp),
+    ]
+
+
+class ConvBwdArgs(ctypes.Structure):
+    """Mirror of ``gdr_conv_bwd_args`` (include/gdr_conv.h)."""
+    _fields_ = [
+        ("B", _i32), ("T", _i32), ("C", _i32), ("K", _i32), ("io_dtype", _i32), ("silu", _i32),
+        ("x", _vp), ("weight", _vp), ("bias", _vp), ("state", _vp), ("lens", _vp), ("grad_y", _vp),
+        ("grad_state_out", _vp), ("grad_x", _vp), ("grad_weight", _vp), ("grad_bias", _vp), ("grad_state", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ConvStepArgs(ctypes.Structure):
+    """Mirror of ``gdr_conv_step_args`` (include/gdr_conv.h)."""
+    _fields_ = [
+        ("N", _i32), ("C", _i32), ("K", _i32), ("io_dtype", _i32), ("silu", _i32), ("reserved", _i32),
+        ("x", _vp), ("weight", _vp), ("bias", _vp), ("state", _vp), ("state_out", _vp), ("y", _vp),
+    ]
+
+
+class SsmArgs(ctypes.Structure):
+    """Mirror of ``gdr_ssm_args`` (include/gdr_ssm.h)."""
+    _fields_ = [
+        ("B", _i32), ("T", _i32), ("C", _i32), ("N", _i32), ("G", _i32), ("io_dtype", _i32), ("softplus", _i32),
+        ("reserved", _i32), ("x", _vp), ("dt", _vp), ("A", _vp), ("Bv", _vp), ("Cv", _vp), ("D", _vp), ("z", _vp),
+        ("dt_bias", _vp), ("h0", _vp), ("lens", _vp), ("y", _vp), ("h_out", _vp), ("ckpt", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SsmBwdArgs(ctypes.Structure):
+    """Mirror of ``gdr_ssm_bwd_args`` (include/gdr_ssm.h)."""
+    _fields_ = [
+        ("B", _i32), ("T", _i32), ("C", _i32), ("N", _i32), ("G", _i32), ("io_dtype", _i32), ("softplus", _i32),
+        ("reserved", _i32), ("x", _vp), ("dt", _vp), ("A", _vp), ("Bv", _vp), ("Cv", _vp), ("D", _vp), ("z", _vp),
+        ("dt_bias", _vp), ("h0", _vp), ("ckpt", _vp), ("lens", _vp), ("grad_y", _vp), ("grad_h", _vp),
+        ("grad_x", _vp), ("grad_dt", _vp), ("grad_A", _vp), ("grad_Bv", _vp), ("grad_Cv", _vp), ("grad_D", _vp),
+        ("grad_z", _vp), ("grad_dt_bias", _vp), ("grad_h0", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class SsmStepArgs(ctypes.Structure):
+    """Mirror of ``gdr_ssm_step_args`` (include/gdr_ssm.h)."""
+    _fields_ = [
+        ("R", _i32), ("C", _i32), ("N", _i32), ("G", _i32), ("io_dtype", _i32), ("softplus", _i32),
+        ("x", _vp), ("dt", _vp), ("A", _vp), ("Bv", _vp), ("Cv", _vp), ("D", _vp), ("z", _vp), ("dt_bias", _vp),
+        ("h", _vp), ("h_out", _vp), ("y", _vp),
+    ]
+
+
+class GnormArgs(ctypes.Structure):
+    """Mirror of ``gdr_gnorm_args`` (include/gdr_gnorm.h)."""
+    _fields_ = [
+        ("R", ctypes.c_int64), ("C", _i32), ("G", _i32), ("io_dtype", _i32), ("center", _i32), ("silu", _i32),
+        ("eps", ctypes.c_float), ("x", _vp), ("z", _vp), ("weight", _vp), ("bias", _vp), ("y", _vp),
+        ("mean", _vp), ("rstd", _vp),
+    ]
+
+
+class GnormBwdArgs(ctypes.Structure):
+    """Mirror of ``gdr_gnorm_bwd_args`` (include/gdr_gnorm.h)."""
+    _fields_ = [
+        ("R", ctypes.c_int64), ("C", _i32), ("G", _i32), ("io_dtype", _i32), ("silu", _i32),
+        ("x", _vp), ("z", _vp), ("mean", _vp), ("rstd", _vp), ("weight", _vp), ("bias", _vp), ("grad_y", _vp),
+        ("grad_x", _vp), ("grad_z", _vp), ("grad_weight", _vp), ("grad_bias", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _CHANNELWISE = {"gdr_scan_fwd": ScanArgs, "gdr_scan_bwd": ScanBwdArgs,
                 "gdr_scan_step": ScanStepArgs, "gdr_norm_fwd": NormArgs,
                 "gdr_norm_bwd": NormBwdArgs, "gdr_ckpt8_pack": Ckpt8PackArgs,
-                "gdr_ckpt8_unpack": Ckpt8UnpackArgs}
+                "gdr_ckpt8_unpack": Ckpt8UnpackArgs,
+                "gdr_conv_fwd": ConvArgs, "gdr_conv_bwd": ConvBwdArgs, "gdr_conv_step": ConvStepArgs,
+                "gdr_ssm_fwd": SsmArgs, "gdr_ssm_bwd": SsmBwdArgs, "gdr_ssm_step": SsmStepArgs,
+                "gdr_gnorm_fwd": GnormArgs, "gdr_gnorm_bwd": GnormBwdArgs}
 _CHANNELWISE_WS = {"gdr_scan_fwd_workspace": ScanArgs, "gdr_scan_bwd_workspace": ScanBwdArgs,
-                   "gdr_norm_bwd_workspace": NormBwdArgs}
+                   "gdr_norm_bwd_workspace": NormBwdArgs, "gdr_conv_bwd_workspace": ConvBwdArgs,
+                   "gdr_ssm_fwd_workspace": SsmArgs, "gdr_ssm_bwd_workspace": SsmBwdArgs,
+                   "gdr_gnorm_bwd_workspace": GnormBwdArgs}
 
 
 def call_channelwise(name: str, args, stream=None) -> int:
-    """Raw call of a channelwise entry point (``gdr_scan_fwd``, ``gdr_scan_bwd``,
-    ``gdr_scan_step``, ``gdr_norm_fwd``, ``gdr_norm_bwd``, ``gdr_ckpt8_pack``,
-    ``gdr_ckpt8_unpack``) with its filled struct; returns the status code."""
+    """Raw call of a channelwise entry point (the keys of ``_CHANNELWISE``:
+    ``gdr_scan_fwd``, ``gdr_norm_fwd``, ``gdr_conv_fwd``, ``gdr_ssm_fwd``, ...) with its
+    filled struct; returns the status code."""
     s = stream if isinstance(stream, ctypes.c_void_p) else (
         ctypes.c_void_p(0) if stream is None else _stream(stream))
     return getattr(load_library(), name)(ctypes.byref(args), s)
@@ -1148,3 +1236,370 @@ def gdr_ckpt8_unpack(code, exp, *, dtype=None, x=None, stream=None):
     a = Ckpt8UnpackArgs(math.prod(lead), D, _io(x), cp, ep, xp)
     _launch(load_library().gdr_ckpt8_unpack, a, dev)
     return x
+
+
+# ------------------------------------------------------------ short causal convolution
+def _taps(weight, bias, C, dev):
+    """(K, pointers of weight and bias) of a convolution over C channels."""
+    import torch
+    if weight is None or weight.dim() != 2:
+        raise ValueError("gdr: weight must be [C,K]")
+    K = weight.shape[1]
+    return K, _in(weight, "weight", (C, K), torch.float32, dev), _opt(bias, "bias", (C,), torch.float32, dev)
+
+
+def _edge(K):
+    """Rows of a convolution's state (the C layer refuses the taps that have none)."""
+    return max(K - 1, 0)
+
+
+def gdr_conv_fwd(x, weight, bias=None, *, state=None, lens=None, silu=True, y=None, state_out=None,
+                 return_state=True, stream=None):
+    """Short causal convolution of every channel over its last K tokens, with silu unless
+    ``silu`` is false (see ``gdr_conv_fwd`` in include/gdr_conv.h).
+
+    x [B,T,C] bf16 or fp32; weight fp32 [C,K], 2 <= K <= 8, its last column for the token
+    itself; bias fp32 [C] or None; state [B,K-1,C] like x, the tokens before the first, or
+    None (zeros); lens int32 [B], the tokens of each row of a padded batch, or None (T).
+    Returns (y like x, state_out [B,K-1,C]: the last K-1 inputs of each row, None unless
+    ``return_state`` or given; it may be state)."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("gdr: x must be [B,T,C]")
+    shape, io, dev = x.shape, x.dtype, x.device
+    B, T, C = shape
+    code_io = _io(x)
+    xp = _in(x, "x", shape, io, dev)
+    K, wp, bp = _taps(weight, bias, C, dev)
+    edge = (B, _edge(K), C)
+    sp = _opt(state, "state", edge, io, dev)
+    lp = _opt(lens, "lens", (B,), torch.int32, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_conv_fwd(x, weight, bias, state=state, lens=lens, silu=silu, y=y, state_out=state_out,
+                                return_state=return_state)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _in(y, "y", shape, io, dev)
+    op = None
+    if state_out is not None:
+        op = _in(state_out, "state_out", edge, io, dev)
+    elif return_state:
+        state_out = torch.empty(edge, dtype=io, device=dev)
+        op = state_out.data_ptr()
+    a = ConvArgs(B, T, C, K, code_io, int(bool(silu)), xp, wp, bp, sp, lp, yp, op)
+    _launch(load_library().gdr_conv_fwd, a, dev)
+    return y, state_out
+
+
+def gdr_conv_bwd(grad_y, x, weight, bias=None, *, state=None, lens=None, silu=True, grad_state=None,
+                 need_grad_state=True, workspace=None, stream=None):
+    """Gradients of ``gdr_conv_fwd`` (``gdr_conv_bwd`` in include/gdr_conv.h); x to silu as
+    the forward's, grad_y like x, grad_state like state: the gradient of state_out, or None.
+
+    Returns a dict: x like grad_y, weight fp32 [C,K], bias fp32 [C] (with bias) and, when
+    ``need_grad_state``, state like grad_y [B,K-1,C].  The workspace
+    (``gdr_conv_bwd_workspace`` bytes) is allocated here unless a large enough uint8 tensor
+    is passed, which serves one call at a time."""
+    import torch
+    if grad_y.dim() != 3:
+        raise ValueError("gdr: grad_y must be [B,T,C]")
+    shape, io, f32, dev = grad_y.shape, grad_y.dtype, torch.float32, grad_y.device
+    B, T, C = shape
+    code_io = _io(grad_y)
+    gp = _in(grad_y, "grad_y", shape, io, dev)
+    xp = _in(x, "x", shape, io, dev)
+    K, wp, bp = _taps(weight, bias, C, dev)
+    edge = (B, _edge(K), C)
+    sp = _opt(state, "state", edge, io, dev)
+    lp = _opt(lens, "lens", (B,), torch.int32, dev)
+    gsp = _opt(grad_state, "grad_state", edge, io, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_conv_bwd(grad_y, x, weight, bias, state=state, lens=lens, silu=silu, grad_state=grad_state,
+                                need_grad_state=need_grad_state, workspace=workspace)
+    g = {"x": torch.empty_like(grad_y), "weight": torch.empty((C, K), dtype=f32, device=dev)}
+    gbp = gop = None
+    if bias is not None:
+        g["bias"] = torch.empty((C,), dtype=f32, device=dev)
+        gbp = g["bias"].data_ptr()
+    if need_grad_state:
+        g["state"] = torch.empty(edge, dtype=io, device=dev)
+        gop = g["state"].data_ptr()
+    lib = load_library()
+    a = ConvBwdArgs(B, T, C, K, code_io, int(bool(silu)), xp, wp, bp, sp, lp, gp, gsp, g["x"].data_ptr(),
+                    g["weight"].data_ptr(), gbp, gop)
+    a.workspace, a.workspace_bytes, keep = _workspace(
+        lib.gdr_conv_bwd_workspace(ctypes.byref(a)), workspace, dev)
+    _launch(lib.gdr_conv_bwd, a, dev)
+    return g
+
+
+def gdr_conv_step(state, x, weight, bias=None, *, silu=True, state_out=None, y=None, stream=None):
+    """One token of ``gdr_conv_fwd`` on N states (``gdr_conv_step`` in include/gdr_conv.h).
+    state [N,K-1,C] like x [N,C], overwritten unless ``state_out`` is given; weight fp32
+    [C,K], bias fp32 [C] or None.  Returns y like x."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("gdr: x must be [N,C]")
+    shape, io, dev = x.shape, x.dtype, x.device
+    N, C = shape
+    code_io = _io(x)
+    xp = _in(x, "x", shape, io, dev)
+    K, wp, bp = _taps(weight, bias, C, dev)
+    edge = (N, _edge(K), C)
+    sp = _in(state, "state", edge, io, dev)
+    op = sp if state_out is None or state_out is state else _in(state_out, "state_out", edge, io, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_conv_step(state, x, weight, bias, silu=silu, state_out=state_out, y=y)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _in(y, "y", shape, io, dev)
+    a = ConvStepArgs(N, C, K, code_io, int(bool(silu)), 0, xp, wp, bp, sp, op, yp)
+    _launch(load_library().gdr_conv_step, a, dev)
+    return y
+
+
+# ------------------------------------------------------------ selective state space scan
+def _ssm_inputs(ref, lead, x, dt, A, B, C, D, z, dt_bias):
+    """(N, G, pointers in the structs' order) of a scan whose rows are ``lead`` and whose
+    activations are like ``ref``."""
+    import torch
+    io, f32, dev = ref.dtype, torch.float32, ref.device
+    chans = ref.shape[-1]
+    if A is None or A.dim() != 2:
+        raise ValueError("gdr: A must be [C,N]")
+    if B is None or B.dim() != len(lead) + 2:
+        raise ValueError("gdr: B must be [%s,G,N]" % ("B,T" if len(lead) == 2 else "R"))
+    N, G = A.shape[1], B.shape[-2]
+    vec = (*lead, G, N)
+    return N, G, (_in(x, "x", ref.shape, io, dev), _in(dt, "dt", ref.shape, io, dev), _in(A, "A", (chans, N), f32, dev),
+                  _in(B, "B", vec, io, dev), _in(C, "C", vec, io, dev), _opt(D, "D", (chans,), f32, dev),
+                  _opt(z, "z", ref.shape, io, dev), _opt(dt_bias, "dt_bias", (chans,), f32, dev))
+
+
+def gdr_ssm_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=True, h0=None, lens=None, y=None,
+                h_out=None, ckpt=None, return_state=True, return_ckpt=False, workspace=None, stream=None):
+    """Selective state space scan (see ``gdr_ssm_fwd`` in include/gdr_ssm.h): with
+    d = softplus(dt + dt_bias), h_t = exp(d_t A) h_{t-1} + d_t x_t B_t and
+    y_t = (C_t . h_t + D x_t) silu(z_t).
+
+    x, dt, z [B,T,C] and B, C [B,T,G,N], all bf16 or all fp32 (each group's vectors serve
+    C / G neighbouring channels); A fp32 [C,N], N <= 64; D, dt_bias fp32 [C] or None; h0 fp32
+    [B,C,N] or None (zero); lens int32 [B], the tokens of each row of a padded batch, or
+    None (T).  Without ``softplus`` d is dt + dt_bias.  Returns (y like x, h_out fp32
+    [B,C,N], ckpt) -- h_out None unless ``return_state`` or given (it may be h0), ckpt fp32
+    [B,ceil(T/32),N,C] (the states before each 32 tokens, for the backward) None unless
+    ``return_ckpt`` or given.  The workspace (``gdr_ssm_fwd_workspace`` bytes) is allocated
+    here unless a large enough uint8 tensor is passed, which serves one call at a time."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("gdr: x must be [B,T,C]")
+    shape, io, f32, dev = x.shape, x.dtype, torch.float32, x.device
+    nb, T, chans = shape
+    code_io = _io(x)
+    N, G, ins = _ssm_inputs(x, (nb, T), x, dt, A, B, C, D, z, dt_bias)
+    hshape = (nb, chans, N)
+    hp = _opt(h0, "h0", hshape, f32, dev)
+    lp = _opt(lens, "lens", (nb,), torch.int32, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_ssm_fwd(x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, softplus=softplus, h0=h0, lens=lens, y=y,
+                               h_out=h_out, ckpt=ckpt, return_state=return_state, return_ckpt=return_ckpt,
+                               workspace=workspace)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _in(y, "y", shape, io, dev)
+    op = cp = None
+    if h_out is not None:
+        op = _in(h_out, "h_out", hshape, f32, dev)
+    elif return_state:
+        h_out = torch.empty(hshape, dtype=f32, device=dev)
+        op = h_out.data_ptr()
+    cshape = (nb, -(-T // GDR_SSM_BLOCK), N, chans)
+    if ckpt is not None:
+        cp = _in(ckpt, "ckpt", cshape, f32, dev)
+    elif return_ckpt:
+        ckpt = torch.empty(cshape, dtype=f32, device=dev)
+        cp = ckpt.data_ptr()
+    lib = load_library()
+    a = SsmArgs(nb, T, chans, N, G, code_io, int(bool(softplus)), 0, *ins, hp, lp, yp, op, cp)
+    a.workspace, a.workspace_bytes, keep = _workspace(
+        lib.gdr_ssm_fwd_workspace(ctypes.byref(a)), workspace, dev)
+    _launch(lib.gdr_ssm_fwd, a, dev)
+    return y, h_out, ckpt
+
+
+def gdr_ssm_bwd(grad_y, x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=True, h0=None, lens=None,
+                grad_h=None, ckpt=None, need_grad_h0=True, workspace=None, stream=None):
+    """Gradients of ``gdr_ssm_fwd`` (``gdr_ssm_bwd`` in include/gdr_ssm.h); x to lens as the
+    forward's, grad_y like x, grad_h fp32 [B,C,N] (of h_out) or None.  ``ckpt`` (the
+    forward's, in place of h0) saves the second run of the recurrence.
+
+    Returns a dict: x, dt, B, C and (with z) z like the inputs; A fp32 [C,N] and (with them)
+    D, dt_bias fp32 [C]; when ``need_grad_h0``, h0 fp32 [B,C,N].  The workspace
+    (``gdr_ssm_bwd_workspace`` bytes) is allocated here unless a large enough uint8 tensor
+    is passed, which serves one call at a time."""
+    import torch
+    if grad_y.dim() != 3:
+        raise ValueError("gdr: grad_y must be [B,T,C]")
+    shape, io, f32, dev = grad_y.shape, grad_y.dtype, torch.float32, grad_y.device
+    nb, T, chans = shape
+    code_io = _io(grad_y)
+    N, G, ins = _ssm_inputs(grad_y, (nb, T), x, dt, A, B, C, D, z, dt_bias)
+    hshape = (nb, chans, N)
+    if ckpt is not None and h0 is not None:
+        raise ValueError("gdr: pass either ckpt or h0, not both (ckpt holds the start state)")
+    hp = _opt(h0, "h0", hshape, f32, dev)
+    cp = _opt(ckpt, "ckpt", (nb, -(-T // GDR_SSM_BLOCK), N, chans), f32, dev)
+    lp = _opt(lens, "lens", (nb,), torch.int32, dev)
+    gp = _in(grad_y, "grad_y", shape, io, dev)
+    ghp = _opt(grad_h, "grad_h", hshape, f32, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_ssm_bwd(grad_y, x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, softplus=softplus, h0=h0, lens=lens,
+                               grad_h=grad_h, ckpt=ckpt, need_grad_h0=need_grad_h0, workspace=workspace)
+    g = {"x": torch.empty_like(grad_y), "dt": torch.empty_like(grad_y), "A": torch.empty_like(A),
+         "B": torch.empty_like(B), "C": torch.empty_like(B)}
+    gD = gz = gb = gh0 = None
+    if D is not None:
+        g["D"] = torch.empty_like(D)
+        gD = g["D"].data_ptr()
+    if z is not None:
+        g["z"] = torch.empty_like(z)
+        gz = g["z"].data_ptr()
+    if dt_bias is not None:
+        g["dt_bias"] = torch.empty_like(dt_bias)
+        gb = g["dt_bias"].data_ptr()
+    if need_grad_h0:
+        g["h0"] = torch.empty(hshape, dtype=f32, device=dev)
+        gh0 = g["h0"].data_ptr()
+    lib = load_library()
+    a = SsmBwdArgs(nb, T, chans, N, G, code_io, int(bool(softplus)), 0, *ins, hp, cp, lp, gp, ghp,
+                   g["x"].data_ptr(), g["dt"].data_ptr(), g["A"].data_ptr(), g["B"].data_ptr(), g["C"].data_ptr(),
+                   gD, gz, gb, gh0)
+    a.workspace, a.workspace_bytes, keep = _workspace(
+        lib.gdr_ssm_bwd_workspace(ctypes.byref(a)), workspace, dev)
+    _launch(lib.gdr_ssm_bwd, a, dev)
+    return g
+
+
+def gdr_ssm_step(h, x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=True, h_out=None, y=None, stream=None):
+    """One token of ``gdr_ssm_fwd`` on R states (``gdr_ssm_step`` in include/gdr_ssm.h).
+    h fp32 [R,C,N], overwritten unless ``h_out`` is given; x, dt, z [R,C], B, C [R,G,N], the
+    rest as there.  Returns y like x."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("gdr: x must be [R,C]")
+    shape, io, f32, dev = x.shape, x.dtype, torch.float32, x.device
+    R, chans = shape
+    code_io = _io(x)
+    N, G, ins = _ssm_inputs(x, (R,), x, dt, A, B, C, D, z, dt_bias)
+    hp = _in(h, "h", (R, chans, N), f32, dev)
+    op = hp if h_out is None or h_out is h else _in(h_out, "h_out", (R, chans, N), f32, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_ssm_step(h, x, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, softplus=softplus, h_out=h_out, y=y)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _in(y, "y", shape, io, dev)
+    a = SsmStepArgs(R, chans, N, G, code_io, int(bool(softplus)), *ins, hp, op, yp)
+    _launch(load_library().gdr_ssm_step, a, dev)
+    return y
+
+
+# ------------------------------------------------------------ gated group norm
+def gdr_gnorm_fwd(x, groups, weight=None, bias=None, *, z=None, silu=False, center=True, eps=1e-5, y=None,
+                  return_stats=True, stream=None):
+    """Group norm over ``groups`` equal runs of the last dimension, with an activation or a
+    gate (see ``gdr_gnorm_fwd`` in include/gdr_gnorm.h): u = xh weight + bias, and
+    y = u act(z) with z, else act(u), where act is silu or nothing.  Without ``center`` no
+    mean is taken off.
+
+    x, z [...,C] bf16 or fp32; weight, bias fp32 [C] or None.  Returns (y like x, mean,
+    rstd): the statistics fp32 [...,groups] (None without ``return_stats``, mean None
+    without ``center``)."""
+    import torch
+    if x.dim() < 1:
+        raise ValueError("gdr: x must be [...,C]")
+    shape, io, f32, dev = x.shape, x.dtype, torch.float32, x.device
+    lead, chans, G = shape[:-1], shape[-1], int(groups)
+    R, code_io = math.prod(lead), _io(x)
+    xp = _in(x, "x", shape, io, dev)
+    zp = _opt(z, "z", shape, io, dev)
+    wp = _opt(weight, "weight", (chans,), f32, dev)
+    bp = _opt(bias, "bias", (chans,), f32, dev)
+    if G < 1 or chans % G:
+        raise ValueError(f"gdr: {chans} channels do not fall into {groups} groups")
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_gnorm_fwd(x, groups, weight, bias, z=z, silu=silu, center=center, eps=eps, y=y,
+                                 return_stats=return_stats)
+    if y is None:
+        y = torch.empty_like(x)
+        yp = y.data_ptr()
+    else:
+        yp = _in(y, "y", shape, io, dev)
+    mean = rstd = mp = rp = None
+    if return_stats:
+        rstd = torch.empty((*lead, G), dtype=f32, device=dev)
+        rp = rstd.data_ptr()
+        if center:
+            mean = torch.empty((*lead, G), dtype=f32, device=dev)
+            mp = mean.data_ptr()
+    a = GnormArgs(R, chans, G, code_io, int(bool(center)), int(bool(silu)), eps, xp, zp, wp, bp, yp, mp, rp)
+    _launch(load_library().gdr_gnorm_fwd, a, dev)
+    return y, mean, rstd
+
+
+def gdr_gnorm_bwd(grad_y, x, mean, rstd, groups, weight=None, bias=None, *, z=None, silu=False,
+                  need_grad_weight=True, need_grad_bias=True, workspace=None, stream=None):
+    """Gradients of ``gdr_gnorm_fwd`` (``gdr_gnorm_bwd`` in include/gdr_gnorm.h); grad_y like
+    x, the statistics as the forward returned them (mean None: it took none off), the rest
+    as the forward's.  Returns a dict: x and (with z) z like grad_y, and weight and bias
+    fp32 [C] unless not needed.  The workspace (``gdr_gnorm_bwd_workspace`` bytes) is
+    allocated here unless a large enough uint8 tensor is passed."""
+    import torch
+    if grad_y.dim() < 1:
+        raise ValueError("gdr: grad_y must be [...,C]")
+    shape, io, f32, dev = grad_y.shape, grad_y.dtype, torch.float32, grad_y.device
+    lead, chans, G = shape[:-1], shape[-1], int(groups)
+    R, code_io = math.prod(lead), _io(grad_y)
+    if G < 1 or chans % G:
+        raise ValueError(f"gdr: {chans} channels do not fall into {groups} groups")
+    gp = _in(grad_y, "grad_y", shape, io, dev)
+    xp = _in(x, "x", shape, io, dev)
+    mp, rp = _opt(mean, "mean", (*lead, G), f32, dev), _in(rstd, "rstd", (*lead, G), f32, dev)
+    wp = _opt(weight, "weight", (chans,), f32, dev)
+    bp = _opt(bias, "bias", (chans,), f32, dev)
+    zp = _opt(z, "z", shape, io, dev)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return gdr_gnorm_bwd(grad_y, x, mean, rstd, groups, weight, bias, z=z, silu=silu,
+                                 need_grad_weight=need_grad_weight, need_grad_bias=need_grad_bias, workspace=workspace)
+    g = {"x": torch.empty_like(grad_y)}
+    gzp = gwp = gbp = None
+    if z is not None:
+        g["z"] = torch.empty_like(grad_y)
+        gzp = g["z"].data_ptr()
+    if need_grad_weight:
+        g["weight"] = torch.empty((chans,), dtype=f32, device=dev)
+        gwp = g["weight"].data_ptr()
+    if need_grad_bias:
+        g["bias"] = torch.empty((chans,), dtype=f32, device=dev)
+        gbp = g["bias"].data_ptr()
+    lib = load_library()
+    a = GnormBwdArgs(R, chans, G, code_io, int(bool(silu)), xp, zp, mp, rp, wp, bp, gp, g["x"].data_ptr(), gzp, gwp, gbp)
+    a.workspace, a.workspace_bytes, keep = _workspace(
+        lib.gdr_gnorm_bwd_workspace(ctypes.byref(a)), workspace, dev)
+    _launch(lib.gdr_gnorm_bwd, a, dev)
+    return g

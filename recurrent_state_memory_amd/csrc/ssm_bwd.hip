@@ -1,0 +1,437 @@
+// ssm_bwd.hip -- selective state space scan: backward, gfx950.
+//
+// Workgroups as in the forward, through the blocks of 32 tokens from the last to the first.
+// A block's decays and states are computed again from its saved start state, then the
+// adjoint H runs back through it.  Sums over a channel's states: each wave's parts meet in
+// LDS.  Sums over the channels (grad_Bv, grad_Cv): over the 64 lanes by lane swaps and DPP, 64
+// values at a time, then over the workgroups through partial results that
+// ssm_vector_join_kernel adds up.  Bound by the vector units: about 20 issue slots a state
+// and token.
+#include "col_join.h"
+#include "ssm_tile.h"
+
+namespace gdr {
+namespace ssm {
+
+using chan::ld;
+
+// ---------------------------------------------------------------- sums over lanes
+// 64 values of every lane in, lane_value(v)'s sum over the 64 lanes out, by halves: each
+// step adds two registers' halves into one that holds both sums.
+__device__ inline float swap32_add(float x, float y) {   // lanes 0-31: x, 32-63: y
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ inline float swap16_add(float x, float y) {   // even rows of 16 lanes: x, odd ones: y
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+template <int CTRL, int BANKS>
+__device__ inline float dpp_into(float old, float src) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(src), CTRL, 0xf, BANKS, false));
+}
+__device__ inline float half8_add(float x, float y) {    // lanes 0-7 of a row: x, 8-15: y
+  return dpp_into<0x128, 0x3>(y, x) + dpp_into<0x128, 0xc>(x, y);
+}
+__device__ inline float half4_add(float x, float y) {    // lanes 0-3 of 8: x, 4-7: y
+  return dpp_into<0x141, 0x5>(y, x) + dpp_into<0x141, 0xa>(x, y);
+}
+template <int CTRL>
+__device__ inline float pick_add(bool second, float x, float y) {
+  return (second ? y : x) + dpp_into<CTRL, 0xf>(0.f, second ? x : y);
+}
+// Of four registers that hold 16 lanes' quads: quad lane i has register perm(i)'s sum.
+__device__ inline float quads_add(const float (&r)[4]) {   // lane & 2: r[1], r[3]; lane & 1: r[2], r[3]
+  const bool b1 = threadIdx.x & 2, b0 = threadIdx.x & 1;
+  const float lo = pick_add<0x4E>(b1, r[0], r[1]), hi = pick_add<0x4E>(b1, r[2], r[3]);
+  return pick_add<0xB1>(b0, lo, hi);
+}
+
+// ---------------------------------------------------------------- reverse segments
+// What a segment does to the adjoint: a_t (C_t g_t + ...) from its end (zero; grad_h at the
+// last segment's) to its start, and the sum of its time steps.
+template <typename T, int NW, int NS>
+__global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p, Geo q, const float* vec, float* ends,
+                                                              float* sums) {
+  constexpr int kTile = 16, J = kTile / NW, U = 16 / NS;
+  __shared__ float2 in[kTile][kLanes];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Place s = place_of(q);
+  ++s.seg;   // the first one's start has no use
+  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(min(t0 + q.seg, q.T), len);
+  const size_t nc = (size_t)q.N * q.C;
+  float A2[NS], K[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int n = w * NS + i;
+    A2[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] * scan::kLog2e : 0.f;
+    K[i] = n < q.N && p.grad_h && s.seg == q.segs - 1 ? p.grad_h[((size_t)s.b * q.C + s.c) * q.N + n] : 0.f;
+  }
+  Vectors v[NS / 2];
+#pragma unroll
+  for (int i = 0; i < NS / 2; ++i) v[i] = vectors_at(vec, q, s.b, s.g, w * (NS / 2) + i);
+  const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f;
+  const size_t row0 = (size_t)s.b * q.T * q.C + s.c;
+  float total = 0.f;
+  for (int tt = t0 + (t1 > t0 ? (t1 - 1 - t0) / kTile * kTile : -kTile); tt >= t0; tt -= kTile) {
+    float tile = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int t = j * NW + w;
+      float d = 0.f, g = 0.f;
+      if (tt + t < t1) {
+        const size_t at = row0 + (size_t)(tt + t) * q.C;
+        d = time_step(ld((const T*)p.dt + at) + bias, p.softplus != 0);
+        g = ld((const T*)p.grad_y + at);
+        if (p.z) {
+          const float z = ld((const T*)p.z + at);
+          g *= z * scan::sigmoid(z);
+        }
+      }
+      in[t][lane] = float2{d, g};
+      tile += d;
+    }
+    total += tile;
+    __syncthreads();
+#pragma unroll
+    for (int t = kTile - U; t >= 0; t -= U) {
+#pragma unroll
+      for (int u = U - 1; u >= 0; --u) {
+        const float2 d = in[t + u][lane];
+#pragma unroll
+        for (int i = 0; i < NS; i += 2) {
+          const f4 bc = v[i / 2][tt + t + u];
+          K[i] = __builtin_amdgcn_exp2f(d.x * A2[i]) * fmaf(bc.z, d.y, K[i]);
+          K[i + 1] = __builtin_amdgcn_exp2f(d.x * A2[i + 1]) * fmaf(bc.w, d.y, K[i + 1]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  in[w][lane].x = total;
+  __syncthreads();
+  if (w == 0 && s.on) {
+    total = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) total += in[k][lane].x;
+    sums[((size_t)s.b * q.segs + s.seg) * q.C + s.c] = total;
+  }
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    if (w * NS + i < q.N && s.on) ends[((size_t)s.b * q.segs + s.seg) * nc + (size_t)(w * NS + i) * q.C + s.c] = K[i];
+}
+
+// ---------------------------------------------------------------- backward
+// NW waves of two states; channels of more than 2 NW states take them in NCH turns, whose
+// adjoints and grad_A then wait in LDS.  SUB tokens of a block are worked on at a time.
+template <typename T, int NW, int NCH>
+__global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Geo q, const float* vec, const float* ckpt,
+                                                          const float* ends, const float* sums, float* vpart, float* rows) {
+  constexpr int SUB = 16, J = SUB / NW;
+  __shared__ float2 in[kBlock][kLanes];      // d, d x
+  __shared__ float gs[kBlock][kLanes];       // g
+  __shared__ float part[3][NW][SUB][kLanes]; // each wave's share of p, sum A q, sum C h
+  __shared__ float later[NCH > 1 ? NCH * 4 : 1][NW][kLanes];   // K0, K1, grad_A0, grad_A1 of each turn
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place s = place_of(q);
+  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T);
+  const size_t nc = (size_t)q.N * q.C;
+  const int blocks = q.Tp / kBlock;
+  float A[2], A2[2], K[2], gA[2] = {0.f, 0.f};
+  auto load_turn = [&](int ch) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = (ch * NW + w) * 2 + i;
+      A[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] : 0.f;
+      A2[i] = A[i] * scan::kLog2e;
+    }
+  };
+#pragma unroll
+  for (int ch = 0; ch < NCH; ++ch) {
+    load_turn(ch);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = (ch * NW + w) * 2 + i;
+      K[i] = 0.f;
+      if (n < q.N && s.on) {
+        if (s.seg == q.segs - 1) {
+          if (p.grad_h) K[i] = p.grad_h[((size_t)s.b * q.C + s.c) * q.N + n];
+        } else {
+          const size_t slot = (size_t)s.b * q.segs * nc + (size_t)n * q.C + s.c;
+          K[i] = ends[slot + (size_t)(q.segs - 1) * nc];
+          for (int k = q.segs - 2; k > s.seg; --k)
+            K[i] = fmaf(__builtin_amdgcn_exp2f(A2[i] * sums[((size_t)s.b * q.segs + k) * q.C + s.c]), K[i], ends[slot + k * nc]);
+        }
+      }
+      if (NCH > 1) later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = 0.f;
+    }
+  }
+  const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
+  const bool softplus = p.softplus != 0, gate = p.z != nullptr;
+  const size_t row0 = (size_t)s.b * q.T * q.C + s.c;
+  const T *x = (const T*)p.x + row0, *dt = (const T*)p.dt + row0, *z = (const T*)p.z + row0, *gy = (const T*)p.grad_y + row0;
+  T *gx = (T*)p.grad_x + row0, *gdt = (T*)p.grad_dt + row0, *gz = (T*)p.grad_z + row0;
+  // the lane's place among the 64 sums of a half block: token and which of B0, B1, C0, C1
+  const int mine = ((lane >> 3 & 1) | (lane >> 2 & 1) << 1 | (lane >> 1 & 1) << 2 | (lane & 1) << 3) * 4 + (lane >> 5 | (lane >> 4 & 1) << 1);
+  float gD = 0.f, gbias = 0.f;
+
+  for (int tt = t0 + (t1 - 1 - t0) / kBlock * kBlock; tt >= t0; tt -= kBlock) {
+    if (tt >= len) {   // behind the row's end
+#pragma unroll
+      for (int j = 0; j < kBlock / NW; ++j) {
+        const int t = tt + j * NW + w;
+        if (t < t1 && s.on) {
+          chan::st(gx + (size_t)t * q.C, 0.f);
+          chan::st(gdt + (size_t)t * q.C, 0.f);
+          if (gate) chan::st(gz + (size_t)t * q.C, 0.f);
+        }
+      }
+      continue;
+    }
+    float xs[2 * J], slope[2 * J], zs[2 * J], gys[2 * J];
+#pragma unroll
+    for (int j = 0; j < 2 * J; ++j) {
+      const int t = j * NW + w;
+      const bool live = tt + t < min(t1, len) && s.on;   // lanes without a channel add nothing to the sums
+      float d = 0.f, g = 0.f;
+      xs[j] = zs[j] = gys[j] = 0.f;
+      slope[j] = 1.f;
+      if (live) {
+        const size_t at = (size_t)(tt + t) * q.C;
+        xs[j] = ld(x + at);
+        gys[j] = g = ld(gy + at);
+        d = ld(dt + at) + bias;
+        if (softplus) d = scan::softplus(d, slope[j]);
+        if (gate) {
+          zs[j] = ld(z + at);
+          g *= zs[j] * scan::sigmoid(zs[j]);
+        }
+      }
+      in[t][lane] = float2{d, d * xs[j]};
+      gs[t][lane] = g;
+    }
+    __syncthreads();
+    for (int sub = 1; sub >= 0; --sub) {
+      const int st = sub * SUB;
+#pragma unroll
+      for (int ch = 0; ch < NCH; ++ch) {
+        if (NCH > 1) {
+          load_turn(ch);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
+        }
+        const Vectors v = vectors_at(vec, q, s.b, s.g, ch * NW + w) + tt;
+        float h[SUB + 1][2], a[SUB][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = (ch * NW + w) * 2 + i;
+          h[0][i] = n < q.N && s.on ? ckpt[((size_t)s.b * blocks + tt / kBlock) * nc + (size_t)n * q.C + s.c] : 0.f;
+        }
+        if (sub == 1) {
+#pragma unroll 4
+          for (int t = 0; t < SUB; ++t) {
+            const float2 d = in[t][lane];
+            const f4 bc = v[t];
+            h[0][0] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[0]), h[0][0], d.y * bc.x);
+            h[0][1] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[1]), h[0][1], d.y * bc.y);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < SUB; ++t) {
+          const float2 d = in[st + t][lane];
+          const f4 bc = v[st + t];
+          a[t][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
+          a[t][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
+          h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * bc.x);
+          h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * bc.y);
+          if (gate) {
+            const float u = fmaf(bc.w, h[t + 1][1], bc.z * h[t + 1][0]);
+            float* at = &part[2][w][t][lane];
+            *at = ch == 0 ? u : *at + u;
+          }
+        }
+        float r2[2], r4[2], r8[4];
+#pragma unroll
+        for (int t = SUB - 1; t >= 0; --t) {
+          const float2 d = in[st + t][lane];
+          const float g = gs[st + t][lane];
+          const f4 bc = v[st + t];
+          const float H0 = fmaf(bc.z, g, K[0]), H1 = fmaf(bc.w, g, K[1]);
+          const float b = swap32_add(H0 * d.y, H1 * d.y), c = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
+          const float bc4 = swap16_add(b, c);
+          const float pp = fmaf(bc.y, H1, bc.x * H0);
+          K[0] = H0 * a[t][0];
+          K[1] = H1 * a[t][1];
+          const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];
+          gA[0] = fmaf(d.x, q0, gA[0]);
+          gA[1] = fmaf(d.x, q1, gA[1]);
+          const float dd = fmaf(A[1], q1, A[0] * q0);
+          float *pp_at = &part[0][w][t][lane], *dd_at = &part[1][w][t][lane];
+          *pp_at = ch == 0 ? pp : *pp_at + pp;
+          *dd_at = ch == 0 ? dd : *dd_at + dd;
+          // tokens 2m + 1 and 2m, then pairs of them, then the four quarters
+          r2[t & 1] = bc4;
+          if ((t & 1) == 0) r4[t >> 1 & 1] = half8_add(r2[0], r2[1]);
+          if ((t & 3) == 0) r8[t >> 2] = half4_add(r4[0], r4[1]);
+        }
+        vpart[((((size_t)s.cb * q.B + s.b) * q.pairs + ch * NW + w) * q.Tp + tt + st) * 4 + mine] =
+            quads_add(r8);
+        if (NCH > 1) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = gA[i];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int jj = 0; jj < 2 * J; ++jj) {
+        if (jj / J != sub) continue;
+        const int t = jj * NW + w, ts = t - st;
+        float pp = 0.f, dd = 0.f, u = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+          pp += part[0][k][ts][lane];
+          dd += part[1][k][ts][lane];
+          if (gate) u += part[2][k][ts][lane];
+        }
+        const float d = in[t][lane].x, g = gs[t][lane];
+        const bool live = tt + t < len;
+        const float gd = live ? fmaf(pp, xs[jj], dd) * slope[jj] : 0.f;
+        gbias += gd;
+        gD = fmaf(g, xs[jj], gD);
+        if (tt + t < t1 && s.on) {
+          const size_t at = (size_t)(tt + t) * q.C;
+          chan::st(gx + at, live ? fmaf(pp, d, D * g) : 0.f);
+          chan::st(gdt + at, gd);
+          if (gate) {
+            const float sg = scan::sigmoid(zs[jj]);
+            u = fmaf(D, xs[jj], u);
+            chan::st(gz + at, live ? gys[jj] * u * sg * fmaf(zs[jj], 1.f - sg, 1.f) : 0.f);
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+  // parameters' gradients: a row [N + 2][C] of this batch row and segment
+  float* out = rows + ((size_t)s.b * q.segs + s.seg) * (q.N + 2) * q.C + s.c;
+#pragma unroll
+  for (int ch = 0; ch < NCH; ++ch) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = (ch * NW + w) * 2 + i;
+      if (NCH > 1) K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
+      if (n < q.N && s.on) {
+        out[(size_t)n * q.C] = gA[i];
+        if (p.grad_h0 && s.seg == 0) p.grad_h0[((size_t)s.b * q.C + s.c) * q.N + n] = K[i];
+      }
+    }
+  }
+  in[w][lane] = float2{gD, gbias};
+  __syncthreads();
+  if (w == 0 && s.on) {
+    gD = gbias = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) gD += in[k][lane].x, gbias += in[k][lane].y;
+    out[(size_t)q.N * q.C] = gD;
+    out[(size_t)(q.N + 1) * q.C] = gbias;
+  }
+}
+
+// The vectors' gradients: over the workgroups of a group's channels.
+template <typename T>
+__global__ __launch_bounds__(256) void ssm_vector_join_kernel(const f4* part, Geo q, const int32_t* lens, T* gB, T* gC) {
+  const size_t total = (size_t)q.B * q.G * q.pairs * q.Tp, step = (size_t)q.B * q.pairs * q.Tp;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
+    const size_t row = i / q.Tp, gb = row / q.pairs, g = gb / q.B, b = gb - g * q.B;
+    const int t = (int)(i - row * q.Tp), pair = (int)(row - gb * q.pairs), n = pair * 2;
+    if (t >= q.T || n >= q.N) continue;
+    f4 a = {0.f, 0.f, 0.f, 0.f};
+    if (t < row_len(lens, (int)b, q.T)) {
+      const f4* at = part + ((g * q.nb * q.B + b) * q.pairs + pair) * q.Tp + t;
+      for (int k = 0; k < q.nb; ++k) {
+        const f4 r = at[k * step];
+        a.x += r.x, a.y += r.y, a.z += r.z, a.w += r.w;
+      }
+    }
+    const size_t o = ((b * q.T + t) * q.G + g) * q.N + n;
+    chan::st(gB + o, a.x);
+    chan::st(gC + o, a.z);
+    if (n + 1 < q.N) {
+      chan::st(gB + o + 1, a.y);
+      chan::st(gC + o + 1, a.w);
+    }
+  }
+}
+
+struct ParamGrads {
+  int C, N;
+  float *A, *D, *bias;
+  __device__ void operator()(size_t i, float v) const {
+    const int n = (int)(i / C), c = (int)(i - (size_t)n * C);
+    if (n < N) A[(size_t)c * N + n] = v;
+    else if (n == N ? D != nullptr : bias != nullptr) (n == N ? D : bias)[c] = v;
+  }
+};
+
+// The parts of a workspace: vectors, the segments' ends and sums, partial gradients of the
+// vectors and of the parameters, block-start states where none were saved.
+struct Parts {
+  size_t ends, sums, vpart, rows, ckpt, bytes;
+};
+static Parts parts_of(const Geo& q, bool ckpt) {
+  Parts w;
+  w.ends = vector_bytes(q);
+  w.sums = w.ends + ends_bytes(q);
+  w.vpart = w.sums + sums_bytes(q);
+  w.rows = w.vpart + pad256((size_t)q.G * q.nb * q.B * q.pairs * q.Tp * 16);
+  w.ckpt = w.rows + pad256((size_t)q.B * q.segs * (q.N + 2) * q.C * 4);
+  w.bytes = w.ckpt + (ckpt ? 0 : pad256((size_t)q.B * (q.Tp / kBlock) * q.N * q.C * 4));
+  return w;
+}
+
+size_t bwd_workspace(int B, int T, int C, int N, int G, bool ckpt) { return parts_of(geo_of(B, T, C, N, G), ckpt).bytes; }
+
+template <typename T>
+static hipError_t bwd(const gdr_ssm_bwd_args& a, hipStream_t s) {
+  const Geo q = geo_of(a.B, a.T, a.C, a.N, a.G);
+  const Parts w = parts_of(q, a.ckpt != nullptr);
+  char* ws = (char*)a.workspace;
+  float *vec = (float*)ws, *ends = (float*)(ws + w.ends), *sums = (float*)(ws + w.sums), *vpart = (float*)(ws + w.vpart),
+        *rows = (float*)(ws + w.rows);
+  const float* ckpt = a.ckpt;
+  hipError_t e = launch_vectors(a.io_dtype, a.Bv, a.Cv, a.lens, q, vec, s);
+  if (e != hipSuccess) return e;
+  if (!ckpt) {
+    gdr_ssm_args f{};
+    f.io_dtype = a.io_dtype, f.softplus = a.softplus;
+    f.x = a.x, f.dt = a.dt, f.A = a.A, f.dt_bias = a.dt_bias, f.h0 = a.h0, f.lens = a.lens;
+    f.ckpt = (float*)(ws + w.ckpt);
+    ckpt = f.ckpt;
+    e = launch_states(f, q, vec, ends, sums, s);
+    if (e != hipSuccess) return e;
+  }
+  if (q.segs > 1) {
+    const dim3 grid(q.blocks() / q.segs * (q.segs - 1));
+    if (q.N <= 8) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 4, 2>), grid, dim3(256), 0, s, a, q, vec, ends, sums);
+    else if (q.N <= 16) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 2>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
+    else if (q.N <= 32) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 4>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
+    else hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 8>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
+  }
+  const dim3 grid(q.blocks());
+  if (q.N <= 8) hipLaunchKernelGGL((ssm_bwd_kernel<T, 4, 1>), grid, dim3(256), 0, s, a, q, vec, ckpt, ends, sums, vpart, rows);
+  else if (q.N <= 16) hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 1>), grid, dim3(512), 0, s, a, q, vec, ckpt, ends, sums, vpart, rows);
+  else if (q.N <= 32) hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 2>), grid, dim3(512), 0, s, a, q, vec, ckpt, ends, sums, vpart, rows);
+  else hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 4>), grid, dim3(512), 0, s, a, q, vec, ckpt, ends, sums, vpart, rows);
+  const size_t blocks = ((size_t)q.B * q.G * q.pairs * q.Tp + 255) / 256;
+  hipLaunchKernelGGL(ssm_vector_join_kernel<T>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s,
+                     (const f4*)vpart, q, a.lens, (T*)a.grad_Bv, (T*)a.grad_Cv);
+  launch_col_join(rows, (size_t)q.B * q.segs, (size_t)(q.N + 2) * q.C, ParamGrads{q.C, q.N, a.grad_A, a.grad_D, a.grad_dt_bias}, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_ssm_bwd(const gdr_ssm_bwd_args& a, hipStream_t s) {
+  return a.io_dtype == GDR_BF16 ? bwd<__bf16>(a, s) : bwd<float>(a, s);
+}
+
+}  // namespace ssm
+}  // namespace gdr
