@@ -62,7 +62,7 @@ typedef struct gdr_ssm_args {
   size_t workspace_bytes; /* contents need not be set and are not kept         */
 } gdr_ssm_args;
 
-/* Bytes gdr_ssm_fwd needs at `workspace` (0 for arguments that it refuses); a
+/* Bytes gdr_ssm_fwd needs at `workspace` (0: none, or refused arguments); a
  * workspace serves one call at a time (calls on one stream, or a graph replayed on it,
  * may share one). */
 size_t gdr_ssm_fwd_workspace(const gdr_ssm_args *args);

@@ -95,8 +95,8 @@ size_t gdr_ssm_fwd_workspace(const gdr_ssm_args* a) {
 gdr_status gdr_ssm_fwd(const gdr_ssm_args* a, void* stream) {
   const gdr_status st = check_fwd(a);
   if (st != GDR_OK) return st;
-  if (!a->workspace || a->workspace_bytes < gdr::ssm::fwd_workspace(a->B, a->T, a->C, a->N, a->G))
-    return GDR_ERR_WORKSPACE;
+  const size_t need = gdr::ssm::fwd_workspace(a->B, a->T, a->C, a->N, a->G);
+  if (need && (!a->workspace || a->workspace_bytes < need)) return GDR_ERR_WORKSPACE;
   return done(gdr::ssm::launch_ssm_fwd(*a, static_cast<hipStream_t>(stream)));
 }
 

@@ -15,6 +15,8 @@ namespace ssm {
 
 using chan::ld;
 
+typedef float f4 __attribute__((ext_vector_type(4)));
+
 // ---------------------------------------------------------------- sums over lanes
 // 64 values of every lane in, lane_value(v)'s sum over the 64 lanes out, by halves: each
 // step adds two registers' halves into one that holds both sums.
@@ -51,14 +53,13 @@ __device__ inline float quads_add(const float (&r)[4]) {   // lane & 2: r[1], r[
 // What a segment does to the adjoint: a_t (C_t g_t + ...) from its end (zero; grad_h at the
 // last segment's) to its start, and the sum of its time steps.
 template <typename T, int NW, int NS>
-__global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p, Geo q, const float* vec, float* ends,
-                                                              float* sums) {
-  constexpr int kTile = 16, J = kTile / NW, U = 16 / NS;
-  __shared__ float2 in[kTile][kLanes];
+__global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p, Geo q, float* ends, float* sums) {
+  constexpr int kTile = 16, J = kTile / NW;
+  __shared__ float2 in[2][kTile][kLanes];   // d, g
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place s = place_of(q);
   ++s.seg;   // the first one's start has no use
-  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(min(t0 + q.seg, q.T), len);
+  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, end = min(min(t0 + q.seg, q.T), len);
   const size_t nc = (size_t)q.N * q.C;
   float A2[NS], K[NS];
 #pragma unroll
@@ -67,53 +68,69 @@ __global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p
     A2[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] * scan::kLog2e : 0.f;
     K[i] = n < q.N && p.grad_h && s.seg == q.segs - 1 ? p.grad_h[((size_t)s.b * q.C + s.c) * q.N + n] : 0.f;
   }
-  Vectors v[NS / 2];
-#pragma unroll
-  for (int i = 0; i < NS / 2; ++i) v[i] = vectors_at(vec, q, s.b, s.g, w * (NS / 2) + i);
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f;
-  const size_t row0 = (size_t)s.b * q.T * q.C + s.c;
+  const bool softplus = p.softplus != 0, gate = p.z != nullptr;
+  const size_t row0 = (size_t)s.b * q.T * q.C;
+  const T *dt = (const T*)p.dt + row0, *z = (const T*)p.z + row0, *gy = (const T*)p.grad_y + row0;
+  const unsigned cbytes = (unsigned)s.c * sizeof(T);
+  // One step of vectors (only C_t is used) and inputs ahead; tiles from the last to the first.
+  const Vectors<T, NS, kTile> vectors((const T*)p.Bv, (const T*)p.Cv, q, s, w * (NS / 2));
+  typename Vectors<T, NS, kTile>::Raw vr;
+  T nd[J], ng[J], nz[J];
+  auto load = [&](int i) {
+    if (i < 0) return;
+    const unsigned off = lane_offset(cbytes);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const size_t at = (size_t)min(t0 + i * kTile + j * NW + w, end - 1) * q.C;
+      nd[j] = at_offset(dt + at, off);
+      ng[j] = at_offset(gy + at, off);
+    }
+    if (gate) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) nz[j] = at_offset(z + (size_t)min(t0 + i * kTile + j * NW + w, end - 1) * q.C, off);
+    }
+  };
+  const int n = end > t0 ? (end - t0 + kTile - 1) / kTile : 0;
   float total = 0.f;
-  for (int tt = t0 + (t1 > t0 ? (t1 - 1 - t0) / kTile * kTile : -kTile); tt >= t0; tt -= kTile) {
-    float tile = 0.f;
+  if (n > 0) load(n - 1), vectors.load(t0 + (n - 1) * kTile, end, vr);
+  for (int i = n - 1; i >= 0; --i) {
+    const int tt = t0 + i * kTile;
+    float v[NS / 2][kTile / 4], tile = 0.f;
+    vectors.take(tt, end, vr, v);
+    if (i > 0) vectors.load(tt - kTile, end, vr);
+    float2(*to)[kLanes] = in[i & 1];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int t = j * NW + w;
-      float d = 0.f, g = 0.f;
-      if (tt + t < t1) {
-        const size_t at = row0 + (size_t)(tt + t) * q.C;
-        d = time_step(ld((const T*)p.dt + at) + bias, p.softplus != 0);
-        g = ld((const T*)p.grad_y + at);
-        if (p.z) {
-          const float z = ld((const T*)p.z + at);
-          g *= z * scan::sigmoid(z);
-        }
-      }
-      in[t][lane] = float2{d, g};
+      const bool live = tt + t < end;
+      const float d = live ? time_step((float)nd[j] + bias, softplus) : 0.f, zf = (float)nz[j];
+      float g = (float)ng[j];
+      if (gate) g *= zf * scan::sigmoid(zf);
+      to[t][lane] = float2{d, live ? g : 0.f};
       tile += d;
     }
     total += tile;
-    __syncthreads();
+    load(i - 1);
+    __syncthreads();   // the tile before last is read no more
+    each<kTile>([&](auto back) {
+      constexpr int t = kTile - 1 - decltype(back)::value, L = t % 4 * 4;
+      const float2 d = to[t][lane];
 #pragma unroll
-    for (int t = kTile - U; t >= 0; t -= U) {
-#pragma unroll
-      for (int u = U - 1; u >= 0; --u) {
-        const float2 d = in[t + u][lane];
-#pragma unroll
-        for (int i = 0; i < NS; i += 2) {
-          const f4 bc = v[i / 2][tt + t + u];
-          K[i] = __builtin_amdgcn_exp2f(d.x * A2[i]) * fmaf(bc.z, d.y, K[i]);
-          K[i + 1] = __builtin_amdgcn_exp2f(d.x * A2[i + 1]) * fmaf(bc.w, d.y, K[i + 1]);
-        }
+      for (int k = 0; k < NS; k += 2) {
+        const float bc = v[k / 2][t / 4];
+        K[k] = __builtin_amdgcn_exp2f(d.x * A2[k]) * fmaf(row_lane<L + 2>(bc), d.y, K[k]);
+        K[k + 1] = __builtin_amdgcn_exp2f(d.x * A2[k + 1]) * fmaf(row_lane<L + 3>(bc), d.y, K[k + 1]);
       }
-    }
-    __syncthreads();
+    });
   }
-  in[w][lane].x = total;
+  __syncthreads();
+  in[0][w][lane].x = total;
   __syncthreads();
   if (w == 0 && s.on) {
     total = 0.f;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) total += in[k][lane].x;
+    for (int k = 0; k < NW; ++k) total += in[0][k][lane].x;
     sums[((size_t)s.b * q.segs + s.seg) * q.C + s.c] = total;
   }
 #pragma unroll
@@ -125,7 +142,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p
 // NW waves of two states; channels of more than 2 NW states take them in NCH turns, whose
 // adjoints and grad_A then wait in LDS.  SUB tokens of a block are worked on at a time.
 template <typename T, int NW, int NCH>
-__global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Geo q, const float* vec, const float* ckpt,
+__global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt,
                                                           const float* ends, const float* sums, float* vpart, float* rows) {
   constexpr int SUB = 16, J = SUB / NW;
   __shared__ float2 in[kBlock][kLanes];      // d, d x
@@ -134,7 +151,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
   __shared__ float later[NCH > 1 ? NCH * 4 : 1][NW][kLanes];   // K0, K1, grad_A0, grad_A1 of each turn
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place s = place_of(q);
-  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T);
+  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T), end = min(t1, len);
   const size_t nc = (size_t)q.N * q.C;
   const int blocks = q.Tp / kBlock;
   float A[2], A2[2], K[2], gA[2] = {0.f, 0.f};
@@ -220,7 +237,9 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
 #pragma unroll
           for (int i = 0; i < 2; ++i) K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
         }
-        const Vectors v = vectors_at(vec, q, s.b, s.g, ch * NW + w) + tt;
+        const Vectors<T, 2, SUB> vectors((const T*)p.Bv, (const T*)p.Cv, q, s, ch * NW + w);
+        typename Vectors<T, 2, SUB>::Raw vr;
+        float v[1][SUB / 4];
         float h[SUB + 1][2], a[SUB][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -228,38 +247,41 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
           h[0][i] = n < q.N && s.on ? ckpt[((size_t)s.b * blocks + tt / kBlock) * nc + (size_t)n * q.C + s.c] : 0.f;
         }
         if (sub == 1) {
-#pragma unroll 4
-          for (int t = 0; t < SUB; ++t) {
+          vectors.load(tt, end, vr);
+          vectors.take(tt, end, vr, v);
+          each<SUB>([&](auto ti) {
+            constexpr int t = decltype(ti)::value, L = t % 4 * 4;
             const float2 d = in[t][lane];
-            const f4 bc = v[t];
-            h[0][0] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[0]), h[0][0], d.y * bc.x);
-            h[0][1] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[1]), h[0][1], d.y * bc.y);
-          }
+            const float bc = v[0][t / 4];
+            h[0][0] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[0]), h[0][0], d.y * row_lane<L>(bc));
+            h[0][1] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[1]), h[0][1], d.y * row_lane<L + 1>(bc));
+          });
         }
-#pragma unroll
-        for (int t = 0; t < SUB; ++t) {
+        vectors.load(tt + st, end, vr);
+        vectors.take(tt + st, end, vr, v);
+        each<SUB>([&](auto ti) {
+          constexpr int t = decltype(ti)::value, L = t % 4 * 4;
           const float2 d = in[st + t][lane];
-          const f4 bc = v[st + t];
+          const float bc = v[0][t / 4];
           a[t][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
           a[t][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
-          h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * bc.x);
-          h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * bc.y);
+          h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bc));
+          h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bc));
           if (gate) {
-            const float u = fmaf(bc.w, h[t + 1][1], bc.z * h[t + 1][0]);
+            const float u = fmaf(row_lane<L + 3>(bc), h[t + 1][1], row_lane<L + 2>(bc) * h[t + 1][0]);
             float* at = &part[2][w][t][lane];
             *at = ch == 0 ? u : *at + u;
           }
-        }
+        });
         float r2[2], r4[2], r8[4];
-#pragma unroll
-        for (int t = SUB - 1; t >= 0; --t) {
+        each<SUB>([&](auto back) {
+          constexpr int t = SUB - 1 - decltype(back)::value, L = t % 4 * 4;
           const float2 d = in[st + t][lane];
-          const float g = gs[st + t][lane];
-          const f4 bc = v[st + t];
-          const float H0 = fmaf(bc.z, g, K[0]), H1 = fmaf(bc.w, g, K[1]);
+          const float g = gs[st + t][lane], bc = v[0][t / 4];
+          const float H0 = fmaf(row_lane<L + 2>(bc), g, K[0]), H1 = fmaf(row_lane<L + 3>(bc), g, K[1]);
           const float b = swap32_add(H0 * d.y, H1 * d.y), c = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
           const float bc4 = swap16_add(b, c);
-          const float pp = fmaf(bc.y, H1, bc.x * H0);
+          const float pp = fmaf(row_lane<L + 1>(bc), H1, row_lane<L>(bc) * H0);
           K[0] = H0 * a[t][0];
           K[1] = H1 * a[t][1];
           const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];
@@ -271,9 +293,9 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
           *dd_at = ch == 0 ? dd : *dd_at + dd;
           // tokens 2m + 1 and 2m, then pairs of them, then the four quarters
           r2[t & 1] = bc4;
-          if ((t & 1) == 0) r4[t >> 1 & 1] = half8_add(r2[0], r2[1]);
-          if ((t & 3) == 0) r8[t >> 2] = half4_add(r4[0], r4[1]);
-        }
+          if constexpr ((t & 1) == 0) r4[t >> 1 & 1] = half8_add(r2[0], r2[1]);
+          if constexpr ((t & 3) == 0) r8[t >> 2] = half4_add(r4[0], r4[1]);
+        });
         vpart[((((size_t)s.cb * q.B + s.b) * q.pairs + ch * NW + w) * q.Tp + tt + st) * 4 + mine] =
             quads_add(r8);
         if (NCH > 1) {
@@ -373,14 +395,14 @@ struct ParamGrads {
   }
 };
 
-// The parts of a workspace: vectors, the segments' ends and sums, partial gradients of the
+// The parts of a workspace: the segments' ends and sums, partial gradients of the
 // vectors and of the parameters, block-start states where none were saved.
 struct Parts {
   size_t ends, sums, vpart, rows, ckpt, bytes;
 };
 static Parts parts_of(const Geo& q, bool ckpt) {
   Parts w;
-  w.ends = vector_bytes(q);
+  w.ends = 0;
   w.sums = w.ends + ends_bytes(q);
   w.vpart = w.sums + sums_bytes(q);
   w.rows = w.vpart + pad256((size_t)q.G * q.nb * q.B * q.pairs * q.Tp * 16);
@@ -396,32 +418,31 @@ static hipError_t bwd(const gdr_ssm_bwd_args& a, hipStream_t s) {
   const Geo q = geo_of(a.B, a.T, a.C, a.N, a.G);
   const Parts w = parts_of(q, a.ckpt != nullptr);
   char* ws = (char*)a.workspace;
-  float *vec = (float*)ws, *ends = (float*)(ws + w.ends), *sums = (float*)(ws + w.sums), *vpart = (float*)(ws + w.vpart),
+  float *ends = (float*)(ws + w.ends), *sums = (float*)(ws + w.sums), *vpart = (float*)(ws + w.vpart),
         *rows = (float*)(ws + w.rows);
   const float* ckpt = a.ckpt;
-  hipError_t e = launch_vectors(a.io_dtype, a.Bv, a.Cv, a.lens, q, vec, s);
-  if (e != hipSuccess) return e;
   if (!ckpt) {
     gdr_ssm_args f{};
     f.io_dtype = a.io_dtype, f.softplus = a.softplus;
     f.x = a.x, f.dt = a.dt, f.A = a.A, f.dt_bias = a.dt_bias, f.h0 = a.h0, f.lens = a.lens;
     f.ckpt = (float*)(ws + w.ckpt);
     ckpt = f.ckpt;
-    e = launch_states(f, q, vec, ends, sums, s);
+    f.Bv = a.Bv, f.Cv = a.Cv;
+    const hipError_t e = launch_states(f, q, ends, sums, s);
     if (e != hipSuccess) return e;
   }
   if (q.segs > 1) {
     const dim3 grid(q.blocks() / q.segs * (q.segs - 1));
-    if (q.N <= 8) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 4, 2>), grid, dim3(256), 0, s, a, q, vec, ends, sums);
-    else if (q.N <= 16) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 2>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
-    else if (q.N <= 32) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 4>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
-    else hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 8>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
+    if (q.N <= 8) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 4, 2>), grid, dim3(256), 0, s, a, q, ends, sums);
+    else if (q.N <= 16) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 2>), grid, dim3(512), 0, s, a, q, ends, sums);
+    else if (q.N <= 32) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 4>), grid, dim3(512), 0, s, a, q, ends, sums);
+    else hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 8>), grid, dim3(512), 0, s, a, q, ends, sums);
   }
   const dim3 grid(q.blocks());
-  if (q.N <= 8) hipLaunchKernelGGL((ssm_bwd_kernel<T, 4, 1>), grid, dim3(256), 0, s, a, q, vec, ckpt, ends, sums, vpart, rows);
-  else if (q.N <= 16) hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 1>), grid, dim3(512), 0, s, a, q, vec, ckpt, ends, sums, vpart, rows);
-  else if (q.N <= 32) hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 2>), grid, dim3(512), 0, s, a, q, vec, ckpt, ends, sums, vpart, rows);
-  else hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 4>), grid, dim3(512), 0, s, a, q, vec, ckpt, ends, sums, vpart, rows);
+  if (q.N <= 8) hipLaunchKernelGGL((ssm_bwd_kernel<T, 4, 1>), grid, dim3(256), 0, s, a, q, ckpt, ends, sums, vpart, rows);
+  else if (q.N <= 16) hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 1>), grid, dim3(512), 0, s, a, q, ckpt, ends, sums, vpart, rows);
+  else if (q.N <= 32) hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 2>), grid, dim3(512), 0, s, a, q, ckpt, ends, sums, vpart, rows);
+  else hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 4>), grid, dim3(512), 0, s, a, q, ckpt, ends, sums, vpart, rows);
   const size_t blocks = ((size_t)q.B * q.G * q.pairs * q.Tp + 255) / 256;
   hipLaunchKernelGGL(ssm_vector_join_kernel<T>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s,
                      (const f4*)vpart, q, a.lens, (T*)a.grad_Bv, (T*)a.grad_Cv);

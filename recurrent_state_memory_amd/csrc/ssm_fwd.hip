@@ -1,9 +1,11 @@
 // ssm_fwd.hip -- selective state space scan: forward and single-token step, gfx950.
 //
-// Tiles of 16 tokens x 64 channels.  All waves turn the tile's inputs into (d, d x) in
-// LDS, each wave runs its states through the tile (per state and token: d A, exp2, d x B, two
-// fma; B and C from scalar registers) and leaves its part of y in LDS, and all waves add the
-// parts, D x and the gate.  Bound by the vector units: 6 issue slots a state and token.
+// Tiles of 16 tokens x 64 channels, in three steps: all waves turn the tile's inputs into
+// (d, d x) in LDS; each wave runs its states through the tile (per state and token: d A,
+// exp2, d x B, two fma) and leaves its part of y in LDS; all
+// waves add the parts, D x and the gate.  Between two barriers the last step of one tile,
+// the first of the next but one and the middle one of the tile between are done.  Bound by
+// the vector units: 6 issue slots a state and token.
 #include "ssm_tile.h"
 
 namespace gdr {
@@ -15,48 +17,17 @@ using chan::Run;
 
 constexpr int kTile = 16;
 
-// ---------------------------------------------------------------- vectors
-template <typename T>
-__global__ __launch_bounds__(256) void ssm_vector_kernel(const T* Bv, const T* Cv, const int32_t* lens, Geo q, f4* out) {
-  const size_t total = (size_t)q.B * q.G * q.pairs * q.Tp;
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
-    const size_t row = i / q.Tp, bg = row / q.pairs, b = bg / q.G, g = bg - b * q.G;
-    const int t = (int)(i - row * q.Tp), n = (int)(row - bg * q.pairs) * 2;
-    f4 v = {0.f, 0.f, 0.f, 0.f};
-    if (t < row_len(lens, (int)b, q.T)) {
-      const size_t at = ((b * q.T + t) * q.G + g) * q.N + n;
-      if (n < q.N) v.x = ld(Bv + at), v.z = ld(Cv + at);
-      if (n + 1 < q.N) v.y = ld(Bv + at + 1), v.w = ld(Cv + at + 1);
-    }
-    out[i] = v;
-  }
-}
-
-hipError_t launch_vectors(int io_dtype, const void* Bv, const void* Cv, const int32_t* lens, const Geo& q, float* out,
-                          hipStream_t s) {
-  const size_t blocks = ((size_t)q.B * q.G * q.pairs * q.Tp + 255) / 256;
-  const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
-  if (io_dtype == GDR_BF16)
-    hipLaunchKernelGGL(ssm_vector_kernel<__bf16>, grid, dim3(256), 0, s, (const __bf16*)Bv, (const __bf16*)Cv,
-                       lens, q, (f4*)out);
-  else
-    hipLaunchKernelGGL(ssm_vector_kernel<float>, grid, dim3(256), 0, s, (const float*)Bv, (const float*)Cv, lens, q,
-                       (f4*)out);
-  return hipGetLastError();
-}
-
 // ---------------------------------------------------------------- forward
 // MODE 0: y and everything else; 1: states alone (ckpt, h_out); 2: what a segment does to
 // the state: its end from zero (the first one's from h0) and the sum of its time steps.
 template <typename T, int NW, int NS, int MODE>
-__global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q, const float* vec, float* ends, float* sums) {
+__global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q, float* ends, float* sums) {
   constexpr int J = kTile / NW;   // tokens of a tile that a wave prepares and finishes
-  constexpr int U = 16 / NS;
-  __shared__ float2 in[kTile][kLanes];
-  __shared__ float part[MODE == 0 ? NW : 1][kTile][kLanes];
+  __shared__ float2 in[2][kTile][kLanes];
+  __shared__ float part[MODE == 0 ? 2 : 1][MODE == 0 ? NW : 1][kTile][kLanes];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place s = place_of(q);
-  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T);
+  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T), end = min(t1, len);
   const size_t nc = (size_t)q.N * q.C;
   float A2[NS], h[NS];
 #pragma unroll
@@ -78,98 +49,154 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
       }
     }
   }
-  Vectors v[NS / 2];
-#pragma unroll
-  for (int i = 0; i < NS / 2; ++i) v[i] = vectors_at(vec, q, s.b, s.g, w * (NS / 2) + i);
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
   const bool softplus = p.softplus != 0, gate = p.z != nullptr;
-  const size_t row0 = (size_t)s.b * q.T * q.C + s.c;
+  // rows begin at scalar addresses, the lane's channel is an offset to them
+  const size_t row0 = (size_t)s.b * q.T * q.C;
   const T *x = (const T*)p.x + row0, *dt = (const T*)p.dt + row0, *z = (const T*)p.z + row0;
   T* y = (T*)p.y + row0;
+  const unsigned cbytes = (unsigned)s.c * sizeof(T);
+  const int n = end > t0 ? (end - t0 + kTile - 1) / kTile : 0;   // tiles
 
-  float nx[J], nd[J], nz[J];   // the next tile's inputs
-  auto load = [&](int tt) {
+  // Inputs as they come, of the tiles i + 1 and i + 2 while tile i is worked on (behind the
+  // end the last row once more), and x and z of the tiles under way.
+  T nx[2][J], nd[2][J], nz[2][J];
+  float cx[2][J], cz[2][J];
+  auto load = [&](int i, T(&ax)[J], T(&ad)[J], T(&az)[J]) {
+    const unsigned off = lane_offset(cbytes);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int t = tt + j * NW + w;
-      nx[j] = nd[j] = nz[j] = 0.f;
-      if (t < min(t1, len)) {
-        nx[j] = ld(x + (size_t)t * q.C);
-        nd[j] = ld(dt + (size_t)t * q.C);
-        if (MODE == 0 && gate) nz[j] = ld(z + (size_t)t * q.C);
-      }
+      const size_t at = (size_t)min(t0 + i * kTile + j * NW + w, end - 1) * q.C;
+      ax[j] = at_offset(x + at, off);
+      ad[j] = at_offset(dt + at, off);
+    }
+    if (MODE == 0 && gate) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) az[j] = at_offset(z + (size_t)min(t0 + i * kTile + j * NW + w, end - 1) * q.C, off);
     }
   };
-  load(t0);
   float total = 0.f;
-  for (int tt = t0; tt < t1; tt += kTile) {
-    if (MODE != 2 && p.ckpt && tt % kBlock == 0 && s.on) {
-      float* ck = p.ckpt + ((size_t)s.b * (q.Tp / kBlock) + tt / kBlock) * nc + s.c;
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (w * NS + i < q.N) ck[(size_t)(w * NS + i) * q.C] = h[i];
-    }
-    if (tt >= len) {   // behind the row's end
-      if (MODE == 0) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int t = tt + j * NW + w;
-          if (t < t1 && s.on) chan::st(y + (size_t)t * q.C, 0.f);
-        }
-      }
-      continue;
-    }
-    float cx[J], cz[J];
+  auto prepare = [&](int i, const T(&ax)[J], const T(&ad)[J], const T(&az)[J], float(&bx)[J], float(&bz)[J],
+                     float2(*to)[kLanes]) {
     float tile = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int t = j * NW + w;
-      const float d = tt + t < min(t1, len) ? time_step(nd[j] + bias, softplus) : 0.f;
-      in[t][lane] = float2{d, d * nx[j]};
+      const bool live = t0 + i * kTile + t < end;
+      const float d = live ? time_step((float)ad[j] + bias, softplus) : 0.f;
+      bx[j] = live ? (float)ax[j] : 0.f;
+      bz[j] = MODE == 0 && gate ? (float)az[j] : 0.f;
+      to[t][lane] = float2{d, d * bx[j]};
       tile += d;
-      cx[j] = nx[j];
-      cz[j] = nz[j];
     }
-    total += tile;
-    __syncthreads();
-    load(tt + kTile);
+    if (MODE == 2) total += tile;
+  };
+  auto finish = [&](int i, const float(&bx)[J], const float(&bz)[J], const float(*from)[kTile][kLanes]) {
+    const unsigned off = lane_offset(cbytes);
 #pragma unroll
-    for (int t = 0; t < kTile; t += U) {
+    for (int j = 0; j < J; ++j) {
+      const int t = j * NW + w, at = t0 + i * kTile + t;
+      float u = D * bx[j];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float2 d = in[t + u][lane];
+      for (int k = 0; k < NW; ++k) u += from[k][t][lane];
+      if (gate) u *= bz[j] * scan::sigmoid(bz[j]);
+      if (at < end && s.on) chan::st(&at_offset(y + (size_t)at * q.C, off), u);
+    }
+  };
+  const Vectors<T, NS, kTile> vectors((const T*)p.Bv, (const T*)p.Cv, q, s, w * (NS / 2));
+  typename Vectors<T, NS, kTile>::Raw vr[2];
+  auto run = [&](const float(&v)[NS / 2][kTile / 4], const float2(*from)[kLanes], float(*to)[kTile][kLanes]) {
+    // four tokens at a time: what does not wait for the state before, then what does
+    float2 d[4], dn[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) d[u] = from[u][lane];
+    each<kTile / 4>([&](auto gg) {
+      constexpr int t = decltype(gg)::value * 4;
+      if constexpr (t + 4 < kTile) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) dn[u] = from[t + 4 + u][lane];
+      }
+      float a[4][NS], b[4][NS];
+      each<4>([&](auto uu) {
+        constexpr int u = decltype(uu)::value, K = u * 4;
+#pragma unroll
+        for (int i = 0; i < NS; i += 2) {
+          const float bc = v[i / 2][t / 4];
+          a[u][i] = __builtin_amdgcn_exp2f(d[u].x * A2[i]);
+          a[u][i + 1] = __builtin_amdgcn_exp2f(d[u].x * A2[i + 1]);
+          b[u][i] = d[u].y * row_lane<K>(bc);
+          b[u][i + 1] = d[u].y * row_lane<K + 1>(bc);
+        }
+      });
+      __builtin_amdgcn_sched_barrier(0);
+      each<4>([&](auto uu) {
+        constexpr int u = decltype(uu)::value, K = u * 4;
         float acc = 0.f;
 #pragma unroll
         for (int i = 0; i < NS; i += 2) {
-          const f4 bc = v[i / 2][tt + t + u];
-          h[i] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[i]), h[i], d.y * bc.x);
-          h[i + 1] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[i + 1]), h[i + 1], d.y * bc.y);
-          if (MODE == 0) acc = fmaf(bc.w, h[i + 1], fmaf(bc.z, h[i], acc));
+          const float bc = v[i / 2][t / 4];
+          h[i] = fmaf(a[u][i], h[i], b[u][i]);
+          h[i + 1] = fmaf(a[u][i + 1], h[i + 1], b[u][i + 1]);
+          if (MODE == 0) {
+            acc = i == 0 ? row_lane<K + 2>(bc) * h[0] : fmaf(row_lane<K + 2>(bc), h[i], acc);
+            acc = fmaf(row_lane<K + 3>(bc), h[i + 1], acc);
+          }
         }
-        if (MODE == 0) part[w][t + u][lane] = acc;
-      }
-    }
+        if (MODE == 0) to[w][t + u][lane] = acc;
+        d[u] = dn[u];
+      });
+    });
+  };
+  auto save = [&](int tt) {
+    float* ck = p.ckpt + ((size_t)s.b * (q.Tp / kBlock) + tt / kBlock) * nc + s.c;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (w * NS + i < q.N && s.on) ck[(size_t)(w * NS + i) * q.C] = h[i];
+  };
+  // Tile i of parity P.
+  auto turn = [&](auto parity, int i) {
+    constexpr int P = decltype(parity)::value;
+    const int tt = t0 + i * kTile;
+    float v[NS / 2][kTile / 4];
+    vectors.take(tt, end, vr[P], v);
+    vectors.load(tt + 2 * kTile, end, vr[P]);
+    if (MODE == 0 && i > 0) finish(i - 1, cx[P ^ 1], cz[P ^ 1], part[MODE == 0 ? P ^ 1 : 0]);
+    prepare(i + 1, nx[P ^ 1], nd[P ^ 1], nz[P ^ 1], cx[P ^ 1], cz[P ^ 1], in[P ^ 1]);
+    load(i + 3, nx[P ^ 1], nd[P ^ 1], nz[P ^ 1]);
+    if (MODE != 2 && p.ckpt && tt % kBlock == 0) save(tt);
+    run(v, in[P], part[MODE == 0 ? P : 0]);
     __syncthreads();
+  };
+  if (n > 0) {
+    load(0, nx[0], nd[0], nz[0]);
+    load(1, nx[1], nd[1], nz[1]);
+    vectors.load(t0, end, vr[0]);
+    vectors.load(t0 + kTile, end, vr[1]);
+    prepare(0, nx[0], nd[0], nz[0], cx[0], cz[0], in[0]);
+    load(2, nx[0], nd[0], nz[0]);
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < n; i += 2) {
+      turn(std::integral_constant<int, 0>(), i);
+      if (i + 1 < n) turn(std::integral_constant<int, 1>(), i + 1);
+    }
     if (MODE == 0) {
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int t = j * NW + w;
-        float u = 0.f;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) u += part[k][t][lane];
-        u = fmaf(D, cx[j], u);
-        if (gate) u *= cz[j] * scan::sigmoid(cz[j]);
-        if (tt + t < t1 && s.on) chan::st(y + (size_t)(tt + t) * q.C, tt + t < len ? u : 0.f);
-      }
+      if (n & 1) finish(n - 1, cx[0], cz[0], part[0]);
+      else finish(n - 1, cx[1], cz[1], part[MODE == 0]);
     }
   }
+  // behind the row's end: y is 0 and the state what it is
+  if (MODE == 0 && s.on)
+    for (int t = max(end, t0) + w; t < t1; t += NW) chan::st(&at_offset(y + (size_t)t * q.C, cbytes), 0.f);
+  if (MODE != 2 && p.ckpt)
+    for (int tt = t0 + (n * kTile + kBlock - 1) / kBlock * kBlock; tt < t1; tt += kBlock) save(tt);
   if (MODE == 2) {
-    in[w][lane].x = total;
+    in[0][w][lane].x = total;   // behind a barrier, and no tile is left
     __syncthreads();
     if (w == 0 && s.on) {
       total = 0.f;
 #pragma unroll
-      for (int k = 0; k < NW; ++k) total += in[k][lane].x;
+      for (int k = 0; k < NW; ++k) total += in[0][k][lane].x;
       sums[((size_t)s.b * q.segs + s.seg) * q.C + s.c] = total;
     }
 #pragma unroll
@@ -183,41 +210,39 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
 }
 
 template <typename T, int MODE>
-static void launch_fwd(const gdr_ssm_args& a, const Geo& q, const float* vec, float* ends, float* sums, hipStream_t s) {
+static void launch_fwd(const gdr_ssm_args& a, const Geo& q, float* ends, float* sums, hipStream_t s) {
   const dim3 grid(MODE == 2 ? q.blocks() / q.segs * (q.segs - 1) : q.blocks());   // segments come last
-  if (q.N <= 8) hipLaunchKernelGGL((ssm_fwd_kernel<T, 4, 2, MODE>), grid, dim3(256), 0, s, a, q, vec, ends, sums);
-  else if (q.N <= 16) hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 2, MODE>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
-  else if (q.N <= 32) hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 4, MODE>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
-  else hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 8, MODE>), grid, dim3(512), 0, s, a, q, vec, ends, sums);
+  if (q.N <= 8) hipLaunchKernelGGL((ssm_fwd_kernel<T, 4, 2, MODE>), grid, dim3(256), 0, s, a, q, ends, sums);
+  else if (q.N <= 16) hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 2, MODE>), grid, dim3(512), 0, s, a, q, ends, sums);
+  else if (q.N <= 32) hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 4, MODE>), grid, dim3(512), 0, s, a, q, ends, sums);
+  else hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 8, MODE>), grid, dim3(512), 0, s, a, q, ends, sums);
 }
 
-hipError_t launch_states(const gdr_ssm_args& a, const Geo& q, const float* vec, float* ends, float* sums, hipStream_t s) {
+hipError_t launch_states(const gdr_ssm_args& a, const Geo& q, float* ends, float* sums, hipStream_t s) {
   const bool bf = a.io_dtype == GDR_BF16;
   if (q.segs > 1) {
-    if (bf) launch_fwd<__bf16, 2>(a, q, vec, ends, sums, s);
-    else launch_fwd<float, 2>(a, q, vec, ends, sums, s);
+    if (bf) launch_fwd<__bf16, 2>(a, q, ends, sums, s);
+    else launch_fwd<float, 2>(a, q, ends, sums, s);
   }
   if (a.y) {
-    if (bf) launch_fwd<__bf16, 0>(a, q, vec, ends, sums, s);
-    else launch_fwd<float, 0>(a, q, vec, ends, sums, s);
+    if (bf) launch_fwd<__bf16, 0>(a, q, ends, sums, s);
+    else launch_fwd<float, 0>(a, q, ends, sums, s);
   } else {
-    if (bf) launch_fwd<__bf16, 1>(a, q, vec, ends, sums, s);
-    else launch_fwd<float, 1>(a, q, vec, ends, sums, s);
+    if (bf) launch_fwd<__bf16, 1>(a, q, ends, sums, s);
+    else launch_fwd<float, 1>(a, q, ends, sums, s);
   }
   return hipGetLastError();
 }
 
 size_t fwd_workspace(int B, int T, int C, int N, int G) {
   const Geo q = geo_of(B, T, C, N, G);
-  return vector_bytes(q) + ends_bytes(q) + sums_bytes(q);
+  return ends_bytes(q) + sums_bytes(q);
 }
 
 hipError_t launch_ssm_fwd(const gdr_ssm_args& a, hipStream_t s) {
   const Geo q = geo_of(a.B, a.T, a.C, a.N, a.G);
-  char* ws = (char*)a.workspace;
-  float *vec = (float*)ws, *ends = (float*)(ws + vector_bytes(q)), *sums = (float*)(ws + vector_bytes(q) + ends_bytes(q));
-  const hipError_t e = launch_vectors(a.io_dtype, a.Bv, a.Cv, a.lens, q, vec, s);
-  return e != hipSuccess ? e : launch_states(a, q, vec, ends, sums, s);
+  float* ends = (float*)a.workspace;
+  return launch_states(a, q, ends, (float*)((char*)a.workspace + ends_bytes(q)), s);
 }
 
 // ---------------------------------------------------------------- step
