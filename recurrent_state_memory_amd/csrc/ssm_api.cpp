@@ -13,7 +13,7 @@ using gdr::Span;
 gdr_status check_sizes(int B, int T, int C, int N, int G, int io_dtype, int softplus) {
   if (io_dtype != GDR_F32 && io_dtype != GDR_BF16) return GDR_ERR_DTYPE;
   if (B <= 0 || T <= 0 || C <= 0 || N <= 0 || G <= 0 || C % G != 0) return GDR_ERR_SHAPE;
-  if (C > (1 << 18) || N > gdr::ssm::kMaxN) return GDR_ERR_UNSUPPORTED;
+  if (C > (1 << 18) || N > gdr::ssm::kMaxN || (long long)G * N > (1 << 16)) return GDR_ERR_UNSUPPORTED;
   const long long bt = (long long)B * T;   // < 2^62
   if (bt >= (1LL << 30) || bt >= (1LL << 40) / C) return GDR_ERR_SHAPE;
   return softplus == 0 || softplus == 1 ? GDR_OK : GDR_ERR_ARG;

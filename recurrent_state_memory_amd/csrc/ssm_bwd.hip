@@ -70,57 +70,59 @@ __global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p
   }
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f;
   const bool softplus = p.softplus != 0, gate = p.z != nullptr;
-  const size_t row0 = (size_t)s.b * q.T * q.C;
-  const T *dt = (const T*)p.dt + row0, *z = (const T*)p.z + row0, *gy = (const T*)p.grad_y + row0;
-  const unsigned cbytes = (unsigned)s.c * sizeof(T);
+  const Buffer dt = rows_at<T>(p.dt, q, s.b, t0, end), gy = rows_at<T>(p.grad_y, q, s.b, t0, end),
+               z = rows_at<T>(p.z, q, s.b, t0, gate ? end : t0);
+  const unsigned row_bytes = (unsigned)(q.C * sizeof(T)), col = s.on ? (unsigned)(s.c * sizeof(T)) : kNowhere;
   // One step of vectors (only C_t is used) and inputs ahead; tiles from the last to the first.
-  const Vectors<T, NS, kTile> vectors((const T*)p.Bv, (const T*)p.Cv, q, s, w * (NS / 2));
+  const Vectors<T, NS, kTile> vectors(p.Bv, p.Cv, q, s, t0, end, w * (NS / 2));
   typename Vectors<T, NS, kTile>::Raw vr;
-  T nd[J], ng[J], nz[J];
+  typedef typename Io<T>::Raw Raw;
+  Raw nd[J], ng[J], nz[J];
   auto load = [&](int i) {
-    if (i < 0) return;
-    const unsigned off = lane_offset(cbytes);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const size_t at = (size_t)min(t0 + i * kTile + j * NW + w, end - 1) * q.C;
-      nd[j] = at_offset(dt + at, off);
-      ng[j] = at_offset(gy + at, off);
+      const unsigned at = col + (unsigned)(i * kTile + j * NW + w) * row_bytes;
+      nd[j] = Io<T>::load(dt, at);
+      ng[j] = Io<T>::load(gy, at);
     }
     if (gate) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) nz[j] = at_offset(z + (size_t)min(t0 + i * kTile + j * NW + w, end - 1) * q.C, off);
+      for (int j = 0; j < J; ++j) nz[j] = Io<T>::load(z, col + (unsigned)(i * kTile + j * NW + w) * row_bytes);
     }
   };
   const int n = end > t0 ? (end - t0 + kTile - 1) / kTile : 0;
   float total = 0.f;
-  if (n > 0) load(n - 1), vectors.load(t0 + (n - 1) * kTile, end, vr);
+  if (n > 0) load(n - 1), vectors.load((n - 1) * kTile, vr);
   for (int i = n - 1; i >= 0; --i) {
     const int tt = t0 + i * kTile;
-    float v[NS / 2][kTile / 4], tile = 0.f;
-    vectors.take(tt, end, vr, v);
-    if (i > 0) vectors.load(tt - kTile, end, vr);
+    float tile = 0.f;
+    typename Vectors<T, NS, kTile>::Set v;
+    vectors.take(vr, v);
+    if (i > 0) vectors.load((i - 1) * kTile, vr);
     float2(*to)[kLanes] = in[i & 1];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int t = j * NW + w;
-      const bool live = tt + t < end;
-      const float d = live ? time_step((float)nd[j] + bias, softplus) : 0.f, zf = (float)nz[j];
-      float g = (float)ng[j];
-      if (gate) g *= zf * scan::sigmoid(zf);
-      to[t][lane] = float2{d, live ? g : 0.f};
+      const float d = tt + t < end ? time_step(Io<T>::get(nd[j]) + bias, softplus) : 0.f;
+      float g = Io<T>::get(ng[j]);   // 0 from `end` on, and z with it
+      if (gate) {
+        const float zf = Io<T>::get(nz[j]);
+        g *= zf * scan::sigmoid(zf);
+      }
+      to[t][lane] = float2{d, g};
       tile += d;
     }
     total += tile;
-    load(i - 1);
+    if (i > 0) load(i - 1);
     __syncthreads();   // the tile before last is read no more
     each<kTile>([&](auto back) {
-      constexpr int t = kTile - 1 - decltype(back)::value, L = t % 4 * 4;
+      constexpr int t = kTile - 1 - decltype(back)::value, L = t % 8 * 2;
       const float2 d = to[t][lane];
 #pragma unroll
       for (int k = 0; k < NS; k += 2) {
-        const float bc = v[k / 2][t / 4];
-        K[k] = __builtin_amdgcn_exp2f(d.x * A2[k]) * fmaf(row_lane<L + 2>(bc), d.y, K[k]);
-        K[k + 1] = __builtin_amdgcn_exp2f(d.x * A2[k + 1]) * fmaf(row_lane<L + 3>(bc), d.y, K[k + 1]);
+        const float cv = v.c[k / 2][t / 8];
+        K[k] = __builtin_amdgcn_exp2f(d.x * A2[k]) * fmaf(row_lane<L>(cv), d.y, K[k]);
+        K[k + 1] = __builtin_amdgcn_exp2f(d.x * A2[k + 1]) * fmaf(row_lane<L + 1>(cv), d.y, K[k + 1]);
       }
     });
   }
@@ -237,9 +239,9 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
 #pragma unroll
           for (int i = 0; i < 2; ++i) K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
         }
-        const Vectors<T, 2, SUB> vectors((const T*)p.Bv, (const T*)p.Cv, q, s, ch * NW + w);
+        const Vectors<T, 2, SUB> vectors(p.Bv, p.Cv, q, s, t0, end, ch * NW + w);
         typename Vectors<T, 2, SUB>::Raw vr;
-        float v[1][SUB / 4];
+        typename Vectors<T, 2, SUB>::Set v;
         float h[SUB + 1][2], a[SUB][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -247,41 +249,41 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
           h[0][i] = n < q.N && s.on ? ckpt[((size_t)s.b * blocks + tt / kBlock) * nc + (size_t)n * q.C + s.c] : 0.f;
         }
         if (sub == 1) {
-          vectors.load(tt, end, vr);
-          vectors.take(tt, end, vr, v);
+          vectors.load(tt - t0, vr);
+          vectors.take(vr, v);
           each<SUB>([&](auto ti) {
-            constexpr int t = decltype(ti)::value, L = t % 4 * 4;
+            constexpr int t = decltype(ti)::value, L = t % 8 * 2;
             const float2 d = in[t][lane];
-            const float bc = v[0][t / 4];
-            h[0][0] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[0]), h[0][0], d.y * row_lane<L>(bc));
-            h[0][1] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[1]), h[0][1], d.y * row_lane<L + 1>(bc));
+            const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
+            h[0][0] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[0]), h[0][0], d.y * row_lane<L>(bv));
+            h[0][1] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[1]), h[0][1], d.y * row_lane<L + 1>(bv));
           });
         }
-        vectors.load(tt + st, end, vr);
-        vectors.take(tt + st, end, vr, v);
+        vectors.load(tt + st - t0, vr);
+        vectors.take(vr, v);
         each<SUB>([&](auto ti) {
-          constexpr int t = decltype(ti)::value, L = t % 4 * 4;
+          constexpr int t = decltype(ti)::value, L = t % 8 * 2;
           const float2 d = in[st + t][lane];
-          const float bc = v[0][t / 4];
+          const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
           a[t][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
           a[t][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
-          h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bc));
-          h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bc));
+          h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
+          h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
           if (gate) {
-            const float u = fmaf(row_lane<L + 3>(bc), h[t + 1][1], row_lane<L + 2>(bc) * h[t + 1][0]);
+            const float u = fmaf(row_lane<L + 1>(cv), h[t + 1][1], row_lane<L>(cv) * h[t + 1][0]);
             float* at = &part[2][w][t][lane];
             *at = ch == 0 ? u : *at + u;
           }
         });
         float r2[2], r4[2], r8[4];
         each<SUB>([&](auto back) {
-          constexpr int t = SUB - 1 - decltype(back)::value, L = t % 4 * 4;
+          constexpr int t = SUB - 1 - decltype(back)::value, L = t % 8 * 2;
           const float2 d = in[st + t][lane];
-          const float g = gs[st + t][lane], bc = v[0][t / 4];
-          const float H0 = fmaf(row_lane<L + 2>(bc), g, K[0]), H1 = fmaf(row_lane<L + 3>(bc), g, K[1]);
+          const float g = gs[st + t][lane], bv = v.b[0][t / 8], cv = v.c[0][t / 8];
+          const float H0 = fmaf(row_lane<L>(cv), g, K[0]), H1 = fmaf(row_lane<L + 1>(cv), g, K[1]);
           const float b = swap32_add(H0 * d.y, H1 * d.y), c = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
           const float bc4 = swap16_add(b, c);
-          const float pp = fmaf(row_lane<L + 1>(bc), H1, row_lane<L>(bc) * H0);
+          const float pp = fmaf(row_lane<L + 1>(bv), H1, row_lane<L>(bv) * H0);
           K[0] = H0 * a[t][0];
           K[1] = H1 * a[t][1];
           const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];

@@ -51,61 +51,62 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
   }
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
   const bool softplus = p.softplus != 0, gate = p.z != nullptr;
-  // rows begin at scalar addresses, the lane's channel is an offset to them
-  const size_t row0 = (size_t)s.b * q.T * q.C;
-  const T *x = (const T*)p.x + row0, *dt = (const T*)p.dt + row0, *z = (const T*)p.z + row0;
-  T* y = (T*)p.y + row0;
-  const unsigned cbytes = (unsigned)s.c * sizeof(T);
+  const Buffer x = rows_at<T>(p.x, q, s.b, t0, end), dt = rows_at<T>(p.dt, q, s.b, t0, end),
+               z = rows_at<T>(p.z, q, s.b, t0, gate ? end : t0), y = rows_at<T>(p.y, q, s.b, t0, MODE == 0 ? end : t0);
+  const unsigned row_bytes = (unsigned)(q.C * sizeof(T)), col = s.on ? (unsigned)(s.c * sizeof(T)) : kNowhere;
   const int n = end > t0 ? (end - t0 + kTile - 1) / kTile : 0;   // tiles
 
-  // Inputs as they come, of the tiles i + 1 and i + 2 while tile i is worked on (behind the
-  // end the last row once more), and x and z of the tiles under way.
-  T nx[2][J], nd[2][J], nz[2][J];
+  // Inputs as they come, of the tiles i + 1 and i + 2 while tile i is worked on, and x and
+  // z of the tiles under way.
+  typedef typename Io<T>::Raw Raw;
+  Raw nx[2][J], nd[2][J], nz[2][J];
   float cx[2][J], cz[2][J];
-  auto load = [&](int i, T(&ax)[J], T(&ad)[J], T(&az)[J]) {
-    const unsigned off = lane_offset(cbytes);
+  auto load = [&](int i, Raw(&ax)[J], Raw(&ad)[J], Raw(&az)[J]) {
+    unsigned at[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const size_t at = (size_t)min(t0 + i * kTile + j * NW + w, end - 1) * q.C;
-      ax[j] = at_offset(x + at, off);
-      ad[j] = at_offset(dt + at, off);
+      at[j] = col + (unsigned)(i * kTile + j * NW + w) * row_bytes;
+      ax[j] = Io<T>::load(x, at[j]);
+      ad[j] = Io<T>::load(dt, at[j]);
     }
     if (MODE == 0 && gate) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) az[j] = at_offset(z + (size_t)min(t0 + i * kTile + j * NW + w, end - 1) * q.C, off);
+      for (int j = 0; j < J; ++j) az[j] = Io<T>::load(z, at[j]);
     }
   };
   float total = 0.f;
-  auto prepare = [&](int i, const T(&ax)[J], const T(&ad)[J], const T(&az)[J], float(&bx)[J], float(&bz)[J],
+  auto prepare = [&](int i, const Raw(&ax)[J], const Raw(&ad)[J], const Raw(&az)[J], float(&bx)[J], float(&bz)[J],
                      float2(*to)[kLanes]) {
     float tile = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int t = j * NW + w;
-      const bool live = t0 + i * kTile + t < end;
-      const float d = live ? time_step((float)ad[j] + bias, softplus) : 0.f;
-      bx[j] = live ? (float)ax[j] : 0.f;
-      bz[j] = MODE == 0 && gate ? (float)az[j] : 0.f;
+      const float d = t0 + i * kTile + t < end ? time_step(Io<T>::get(ad[j]) + bias, softplus) : 0.f;
+      bx[j] = Io<T>::get(ax[j]);
+      if (MODE == 0 && gate) bz[j] = Io<T>::get(az[j]);
       to[t][lane] = float2{d, d * bx[j]};
       tile += d;
     }
     if (MODE == 2) total += tile;
   };
   auto finish = [&](int i, const float(&bx)[J], const float(&bz)[J], const float(*from)[kTile][kLanes]) {
-    const unsigned off = lane_offset(cbytes);
+    float u[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int t = j * NW + w, at = t0 + i * kTile + t;
-      float u = D * bx[j];
+      u[j] = D * bx[j];
 #pragma unroll
-      for (int k = 0; k < NW; ++k) u += from[k][t][lane];
-      if (gate) u *= bz[j] * scan::sigmoid(bz[j]);
-      if (at < end && s.on) chan::st(&at_offset(y + (size_t)at * q.C, off), u);
+      for (int k = 0; k < NW; ++k) u[j] += from[k][j * NW + w][lane];
     }
+    if (gate) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) u[j] *= bz[j] * scan::sigmoid(bz[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) Io<T>::store(y, col + (unsigned)(i * kTile + j * NW + w) * row_bytes, u[j]);
   };
-  const Vectors<T, NS, kTile> vectors((const T*)p.Bv, (const T*)p.Cv, q, s, w * (NS / 2));
+  const Vectors<T, NS, kTile> vectors(p.Bv, p.Cv, q, s, t0, end, w * (NS / 2));
   typename Vectors<T, NS, kTile>::Raw vr[2];
-  auto run = [&](const float(&v)[NS / 2][kTile / 4], const float2(*from)[kLanes], float(*to)[kTile][kLanes]) {
+  auto run = [&](const typename Vectors<T, NS, kTile>::Set& v, const float2(*from)[kLanes], float(*to)[kTile][kLanes]) {
     // four tokens at a time: what does not wait for the state before, then what does
     float2 d[4], dn[4];
 #pragma unroll
@@ -118,28 +119,28 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
       }
       float a[4][NS], b[4][NS];
       each<4>([&](auto uu) {
-        constexpr int u = decltype(uu)::value, K = u * 4;
+        constexpr int u = decltype(uu)::value, L = (t + u) % 8 * 2;
 #pragma unroll
         for (int i = 0; i < NS; i += 2) {
-          const float bc = v[i / 2][t / 4];
+          const float bv = v.b[i / 2][t / 8];
           a[u][i] = __builtin_amdgcn_exp2f(d[u].x * A2[i]);
           a[u][i + 1] = __builtin_amdgcn_exp2f(d[u].x * A2[i + 1]);
-          b[u][i] = d[u].y * row_lane<K>(bc);
-          b[u][i + 1] = d[u].y * row_lane<K + 1>(bc);
+          b[u][i] = d[u].y * row_lane<L>(bv);
+          b[u][i + 1] = d[u].y * row_lane<L + 1>(bv);
         }
       });
       __builtin_amdgcn_sched_barrier(0);
       each<4>([&](auto uu) {
-        constexpr int u = decltype(uu)::value, K = u * 4;
+        constexpr int u = decltype(uu)::value, L = (t + u) % 8 * 2;
         float acc = 0.f;
 #pragma unroll
         for (int i = 0; i < NS; i += 2) {
-          const float bc = v[i / 2][t / 4];
+          const float cv = v.c[i / 2][t / 8];
           h[i] = fmaf(a[u][i], h[i], b[u][i]);
           h[i + 1] = fmaf(a[u][i + 1], h[i + 1], b[u][i + 1]);
           if (MODE == 0) {
-            acc = i == 0 ? row_lane<K + 2>(bc) * h[0] : fmaf(row_lane<K + 2>(bc), h[i], acc);
-            acc = fmaf(row_lane<K + 3>(bc), h[i + 1], acc);
+            acc = i == 0 ? row_lane<L>(cv) * h[0] : fmaf(row_lane<L>(cv), h[i], acc);
+            acc = fmaf(row_lane<L + 1>(cv), h[i + 1], acc);
           }
         }
         if (MODE == 0) to[w][t + u][lane] = acc;
@@ -157,9 +158,9 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
   auto turn = [&](auto parity, int i) {
     constexpr int P = decltype(parity)::value;
     const int tt = t0 + i * kTile;
-    float v[NS / 2][kTile / 4];
-    vectors.take(tt, end, vr[P], v);
-    vectors.load(tt + 2 * kTile, end, vr[P]);
+    typename Vectors<T, NS, kTile>::Set v;
+    vectors.take(vr[P], v);
+    vectors.load((i + 2) * kTile, vr[P]);
     if (MODE == 0 && i > 0) finish(i - 1, cx[P ^ 1], cz[P ^ 1], part[MODE == 0 ? P ^ 1 : 0]);
     prepare(i + 1, nx[P ^ 1], nd[P ^ 1], nz[P ^ 1], cx[P ^ 1], cz[P ^ 1], in[P ^ 1]);
     load(i + 3, nx[P ^ 1], nd[P ^ 1], nz[P ^ 1]);
@@ -170,8 +171,8 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
   if (n > 0) {
     load(0, nx[0], nd[0], nz[0]);
     load(1, nx[1], nd[1], nz[1]);
-    vectors.load(t0, end, vr[0]);
-    vectors.load(t0 + kTile, end, vr[1]);
+    vectors.load(0, vr[0]);
+    vectors.load(kTile, vr[1]);
     prepare(0, nx[0], nd[0], nz[0], cx[0], cz[0], in[0]);
     load(2, nx[0], nd[0], nz[0]);
     __syncthreads();
@@ -187,7 +188,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
   }
   // behind the row's end: y is 0 and the state what it is
   if (MODE == 0 && s.on)
-    for (int t = max(end, t0) + w; t < t1; t += NW) chan::st(&at_offset(y + (size_t)t * q.C, cbytes), 0.f);
+    for (int t = max(end, t0) + w; t < t1; t += NW) chan::st((T*)p.y + ((size_t)s.b * q.T + t) * q.C + s.c, 0.f);
   if (MODE != 2 && p.ckpt)
     for (int tt = t0 + (n * kTile + kBlock - 1) / kBlock * kBlock; tt < t1; tt += kBlock) save(tt);
   if (MODE == 2) {

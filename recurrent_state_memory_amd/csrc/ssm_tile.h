@@ -49,6 +49,10 @@ inline Geo geo_of(int B, int T, int C, int N, int G) {
   long long want = chains <= 128 && T >= 256 ? 512 / chains : 1;
   if (want > T / 64) want = T / 64;
   if (want < 1) want = 1;
+  // and a segment's rows, and some behind it, stay within a buffer descriptor's 2^31 bytes
+  const long long wide = (long long)(C > G * N ? C : G * N) * 4, most = ((1LL << 31) / wide - 128) / kBlock;
+  const long long least = ((long long)blocks_of(T) + most - 1) / most;
+  if (want < least) want = least;
   q.seg = (int)((blocks_of(T) + want - 1) / want) * kBlock;
   q.segs = (q.Tp + q.seg - 1) / q.seg;
   return q;
@@ -88,86 +92,95 @@ __device__ inline void each(F f) {
   each_of(std::make_integer_sequence<int, N>(), f);
 }
 
-// B_t and C_t of a wave's states.  Each row of 16 lanes holds those of four tokens for one
-// pair of states, lane 4 (t % 4) + k the k-th of {B 2p, B 2p+1, C 2p, C 2p+1}, and the
-// arithmetic takes them from there by DPP (row_newbcast), at no instruction of its own.
-// (From scalar registers: every scalar load misses its cache, as 64 bytes are four tokens, and
-// returns out of order, so each wait is for the last one: 403 us in place of @@ on 8 x 4096
-// x 2048 with 16 states.)
+// A segment's rows of an activation through a buffer descriptor: its base is a scalar, a
+// lane's place in it a 32-bit offset (so no 64-bit arithmetic), reads behind its end give 0
+// and writes there are dropped (so no masks at a row's end or for lanes without a channel,
+// whose offset is kNowhere).  Offsets behind the end stay below 2^31 as well (geo_of).
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr unsigned kNowhere = 0x80000000u;
+__device__ inline Buffer buffer_at(const void* p, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+template <typename T>
+struct Io;
+template <>
+struct Io<float> {
+  typedef uint32_t Raw;
+  static __device__ inline Raw load(Buffer b, unsigned at) { return __builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0); }
+  static __device__ inline float get(Raw r) { return __uint_as_float(r); }
+  static __device__ inline void store(Buffer b, unsigned at, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), b, at, 0, 0);
+  }
+};
+template <>
+struct Io<__bf16> {
+  typedef uint16_t Raw;
+  static __device__ inline Raw load(Buffer b, unsigned at) { return __builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0); }
+  static __device__ inline float get(Raw r) { return __uint_as_float((uint32_t)r << 16); }
+  static __device__ inline void store(Buffer b, unsigned at, float v) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), b, at, 0, 0);
+  }
+};
+// Rows t to end - 1 (none: an empty buffer) of batch row b of a [B][T][C] array.
+template <typename T>
+__device__ inline Buffer rows_at(const void* base, const Geo& q, int b, int t, int end) {
+  return buffer_at((const T*)base + ((size_t)b * q.T + t) * q.C, t < end ? (size_t)(end - t) * q.C * sizeof(T) : 0);
+}
+
+// B_t and C_t of a wave's states, two registers for eight tokens and a pair of states: each
+// row of 16 lanes holds B's (C's) of both states for the eight, lane 2 (t % 8) + i, and the
+// arithmetic takes them from there by DPP (row_newbcast), mostly at no instruction of its
+// own.  (From scalar registers: every scalar load misses its cache, as 64 bytes are four
+// tokens, and returns out of order, so that each wait is for the last one.)
 template <int K>
 __device__ inline float row_lane(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + K, 0xf, 0xf, true));
 }
 template <typename T, int NS, int TILE>
 struct Vectors {
-  static constexpr int P = NS / 2, Q = TILE / 4;
+  static constexpr int P = NS / 2, Q = TILE / 8;
   struct Raw {
-    T v[P][Q];
+    typename Io<T>::Raw b[P][Q], c[P][Q];
   };
-  const T* at[P];     // the lane's element of tokens 0 to 3
-  size_t step;        // elements between tokens
-  int tk;             // the lane's token of four
-  bool ok[P];         // whether the state exists
-  bool all;           // whether all of the wave's do
+  struct Set {
+    float b[P][Q], c[P][Q];
+  };
+  Buffer Bv, Cv;      // of tokens t0 to end - 1; the last one's row ends with its group's vector
+  unsigned step;      // bytes between tokens
+  unsigned at[P];     // the lane's offset behind a multiple of eight tokens
   // of pairs first, first + 1, ... (state 2 first + 2 i)
-  __device__ inline Vectors(const T* Bv, const T* Cv, const Geo& q, const Place& s, int first) {
+  __device__ inline Vectors(const void* b, const void* c, const Geo& q, const Place& s, int t0, int end, int first) {
+    const size_t row = (size_t)q.G * q.N, base = (((size_t)s.b * q.T + t0) * q.G + s.g) * q.N;
+    const size_t bytes = t0 < end ? ((size_t)(end - 1 - t0) * row + q.N) * sizeof(T) : 0;
+    step = (unsigned)(row * sizeof(T));
+    Bv = buffer_at((const T*)b + base, bytes);
+    Cv = buffer_at((const T*)c + base, bytes);
     const int j = threadIdx.x & 15;
-    tk = j >> 2;
-    step = (size_t)q.G * q.N;
-    all = 2 * (first + P) <= q.N;
-    const T* base = ((j & 2) ? Cv : Bv) + ((size_t)s.b * q.T * q.G + s.g) * q.N + (size_t)tk * step;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int n = 2 * (first + i) + (j & 1);
-      ok[i] = n < q.N;
-      at[i] = base + (ok[i] ? n : 0);
+      at[i] = n < q.N ? (j >> 1) * step + n * (unsigned)sizeof(T) : kNowhere;
     }
   }
-  // Tokens t ... t + TILE - 1; behind the last one (end - 1) that one once more.
-  __device__ inline void load(int t, int end, Raw& r) const {
-    if (t + TILE <= end) {
+  // Tokens t ... t + TILE - 1 (counted from t0), zeros behind the last one and where there
+  // is no state.
+  __device__ inline void load(int t, Raw& r) const {
 #pragma unroll
-      for (int i = 0; i < P; ++i)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int k = 0; k < Q; ++k) r.v[i][k] = at[i][(size_t)(t + 4 * k) * step];
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-#pragma unroll
-        for (int k = 0; k < Q; ++k) r.v[i][k] = at[i][(ptrdiff_t)(min(t + 4 * k + tk, end - 1) - tk) * (ptrdiff_t)step];
-    }
+      for (int k = 0; k < Q; ++k) {
+        const unsigned o = at[i] + (unsigned)(t + 8 * k) * step;
+        r.b[i][k] = Io<T>::load(Bv, o);
+        r.c[i][k] = Io<T>::load(Cv, o);
+      }
   }
-  // In fp32, 0 where there is no state or token.
-  __device__ inline void take(int t, int end, const Raw& r, float (&v)[P][Q]) const {
-    if (all && t + TILE <= end) {
+  static __device__ inline void take(const Raw& r, Set& v) {
 #pragma unroll
-      for (int i = 0; i < P; ++i)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int k = 0; k < Q; ++k) v[i][k] = (float)r.v[i][k];
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-#pragma unroll
-        for (int k = 0; k < Q; ++k) v[i][k] = ok[i] && t + 4 * k + tk < end ? (float)r.v[i][k] : 0.f;
-    }
+      for (int k = 0; k < Q; ++k) v.b[i][k] = Io<T>::get(r.b[i][k]), v.c[i][k] = Io<T>::get(r.c[i][k]);
   }
 };
-
-// A lane's byte offset into a row that begins at a scalar address.  The compiler would
-// add it to every row's base and keep the sums in vector registers, with 64-bit vector
-// additions for each access; so it is told nothing about its value.
-__device__ inline unsigned lane_offset(unsigned bytes) {
-  asm volatile("" : "+v"(bytes));
-  return bytes;
-}
-template <typename T>
-__device__ inline const T& at_offset(const T* row, unsigned bytes) {
-  return *(const T*)((const char*)row + bytes);
-}
-template <typename T>
-__device__ inline T& at_offset(T* row, unsigned bytes) {
-  return *(T*)((char*)row + bytes);
-}
 
 // d = softplus(pre) or pre.
 __device__ inline float time_step(float pre, bool softplus) { return softplus ? scan::softplus(pre) : pre; }
