@@ -141,22 +141,246 @@ __global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p
 }
 
 // ---------------------------------------------------------------- backward
-// NW waves of two states; channels of more than 2 NW states take them in NCH turns, whose
-// adjoints and grad_A then wait in LDS.  SUB tokens of a block are worked on at a time.
-template <typename T, int NW, int NCH>
-__global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt,
+// What both kernels below start with: the state's adjoint behind a segment.
+__device__ inline float adjoint_behind(const gdr_ssm_bwd_args& p, const Geo& q, const Place& s, int n, float A2,
+                                       const float* ends, const float* sums) {
+  if (n >= q.N || !s.on) return 0.f;
+  if (s.seg == q.segs - 1) return p.grad_h ? p.grad_h[((size_t)s.b * q.C + s.c) * q.N + n] : 0.f;
+  const size_t nc = (size_t)q.N * q.C, slot = (size_t)s.b * q.segs * nc + (size_t)n * q.C + s.c;
+  float K = ends[slot + (size_t)(q.segs - 1) * nc];
+  for (int k = q.segs - 2; k > s.seg; --k)
+    K = fmaf(__builtin_amdgcn_exp2f(A2 * sums[((size_t)s.b * q.segs + k) * q.C + s.c]), K, ends[slot + k * nc]);
+  return K;
+}
+// The lane's place among the 64 sums of 16 tokens: token and which of B0, B1, C0, C1.
+__device__ inline int sum_place() {
+  const int l = threadIdx.x & 63;
+  return ((l >> 3 & 1) | (l >> 2 & 1) << 1 | (l >> 1 & 1) << 2 | (l & 1) << 3) * 4 + (l >> 5 | (l >> 4 & 1) << 1);
+}
+// What a channel's token is prepared to.
+struct Token {
+  float x, z, gy, slope;   // slope of softplus
+};
+
+// Up to 16 states: NW waves of two each.  A block's 32 states and decays stay in registers.
+// The adjoint passes through it in four quarters; while one is worked on, the one before
+// is finished (the waves' parts added, gradients written), and the next block's inputs are
+// on their way.
+template <typename T, int NW, bool GATE>
+__global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt, const float* ends,
+                                                          const float* sums, float* vpart, float* rows) {
+  constexpr int J = kBlock / NW, QT = 8, JQ = QT / NW > 0 ? QT / NW : 1;
+  static_assert(NW <= QT, "a token of a quarter for every wave");
+  __shared__ float2 in[kBlock][kLanes];                        // d, d x
+  __shared__ float gs[kBlock][kLanes];                         // g
+  __shared__ float part[2][2][NW][QT][kLanes];                 // each wave's share of p and sum A q, two quarters
+  __shared__ float upart[GATE ? NW : 1][GATE ? kBlock : 1][kLanes];   // of sum C h
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place s = place_of(q);
+  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T), end = min(t1, len);
+  const size_t nc = (size_t)q.N * q.C;
+  float A[2], A2[2], K[2], gA[2] = {0.f, 0.f};
+  const float* ck[2];   // the states' checkpoints
+  bool has[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int n = w * 2 + i;
+    has[i] = n < q.N && s.on;
+    A[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] : 0.f;
+    A2[i] = A[i] * scan::kLog2e;
+    K[i] = adjoint_behind(p, q, s, n, A2[i], ends, sums);
+    ck[i] = ckpt + ((size_t)s.b * (q.Tp / kBlock) + t0 / kBlock) * nc + (size_t)(n < q.N ? n : 0) * q.C + s.c;
+  }
+  const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
+  const bool softplus = p.softplus != 0;
+  const Buffer x = rows_at<T>(p.x, q, s.b, t0, end), dt = rows_at<T>(p.dt, q, s.b, t0, end),
+               gy = rows_at<T>(p.grad_y, q, s.b, t0, end), z = rows_at<T>(p.z, q, s.b, t0, GATE ? end : t0),
+               gx = rows_at<T>(p.grad_x, q, s.b, t0, end), gdt = rows_at<T>(p.grad_dt, q, s.b, t0, end),
+               gz = rows_at<T>(p.grad_z, q, s.b, t0, GATE ? end : t0);
+  const unsigned row_bytes = (unsigned)(q.C * sizeof(T)), col = s.on ? (unsigned)(s.c * sizeof(T)) : kNowhere;
+  const Vectors<T, 2, kBlock> vectors(p.Bv, p.Cv, q, s, t0, end, w);
+  float* vout = vpart + ((((size_t)s.cb * q.B + s.b) * q.pairs + w) * q.Tp + t0) * 4 + sum_place();
+
+  // the next block's inputs as they come
+  typedef typename Io<T>::Raw Raw;
+  Raw nx[J], nd[J], ng[J], nz[J];
+  typename Vectors<T, 2, kBlock>::Raw vr;
+  float nh[2];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const unsigned at = col + (unsigned)(i * kBlock + j * NW + w) * row_bytes;
+      nx[j] = Io<T>::load(x, at);
+      nd[j] = Io<T>::load(dt, at);
+      ng[j] = Io<T>::load(gy, at);
+      if (GATE) nz[j] = Io<T>::load(z, at);
+    }
+    vectors.load(i * kBlock, vr);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) nh[k] = has[k] ? ck[k][i * nc] : 0.f;
+  };
+  float gD = 0.f, gbias = 0.f;
+  const int n = end > t0 ? (end - t0 + kBlock - 1) / kBlock : 0;   // blocks
+  if (n > 0) load(n - 1);
+#pragma unroll 1
+  for (int i = n - 1; i >= 0; --i) {
+    const int tt = t0 + i * kBlock;
+    Token own[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int t = j * NW + w;
+      own[j].slope = 1.f;
+      float d = Io<T>::get(nd[j]) + bias, g = Io<T>::get(ng[j]);   // zeros from `end` on
+      if (softplus) d = scan::softplus(d, own[j].slope);
+      if (tt + t >= end) d = own[j].slope = 0.f;
+      own[j].x = Io<T>::get(nx[j]);
+      if (GATE) {
+        own[j].gy = g;
+        own[j].z = Io<T>::get(nz[j]);
+        g *= own[j].z * scan::sigmoid(own[j].z);
+      }
+      if (!s.on) d = 0.f;   // lanes without a channel add nothing to the sums
+      in[t][lane] = float2{d, d * own[j].x};
+      gs[t][lane] = g;
+    }
+    typename Vectors<T, 2, kBlock>::Set v;
+    vectors.take(vr, v);
+    // the decays of half a block: all of them would spill registers
+    float h[kBlock + 1][2], a[kBlock / 2][2];
+    h[0][0] = nh[0], h[0][1] = nh[1];
+    __syncthreads();
+    if (i > 0) load(i - 1);
+    each<kBlock>([&](auto ti) {
+      constexpr int t = decltype(ti)::value, L = t % 8 * 2;
+      const float2 d = in[t][lane];
+      const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
+      constexpr int H = t % (kBlock / 2);
+      a[H][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
+      a[H][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
+      h[t + 1][0] = fmaf(a[H][0], h[t][0], d.y * row_lane<L>(bv));
+      h[t + 1][1] = fmaf(a[H][1], h[t][1], d.y * row_lane<L + 1>(bv));
+      if constexpr (GATE) upart[w][t][lane] = fmaf(row_lane<L + 1>(cv), h[t + 1][1], row_lane<L>(cv) * h[t + 1][0]);
+      if constexpr ((t & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // else loads of many tokens take the registers
+    });
+    vectors.forget(v);
+    float r2[2], r4[2], r8[4], gAb[2] = {0.f, 0.f};
+    auto quarter = [&](auto qi) {
+      constexpr int Q = decltype(qi)::value;
+      each<QT>([&](auto back) {
+        constexpr int ts = QT - 1 - decltype(back)::value, t = Q * QT + ts, L = t % 8 * 2, H = t % (kBlock / 2);
+        const float2 d = in[t][lane];
+        const float g = gs[t][lane], bv = v.b[0][t / 8], cv = v.c[0][t / 8];
+        const float H0 = fmaf(row_lane<L>(cv), g, K[0]), H1 = fmaf(row_lane<L + 1>(cv), g, K[1]);
+        const float vb = swap32_add(H0 * d.y, H1 * d.y), vc = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
+        part[Q & 1][0][w][ts][lane] = fmaf(row_lane<L + 1>(bv), H1, row_lane<L>(bv) * H0);
+        K[0] = H0 * a[H][0];
+        K[1] = H1 * a[H][1];
+        const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];
+        gAb[0] = fmaf(d.x, q0, gAb[0]);
+        gAb[1] = fmaf(d.x, q1, gAb[1]);
+        part[Q & 1][1][w][ts][lane] = fmaf(A[1], q1, A[0] * q0);
+        // tokens 2m + 1 and 2m, then pairs of them, then the four quarters of 16
+        r2[t & 1] = swap16_add(vb, vc);
+        if constexpr ((t & 1) == 0) r4[t >> 1 & 1] = half8_add(r2[0], r2[1]);
+        if constexpr ((t & 3) == 0) r8[t >> 2 & 3] = half4_add(r4[0], r4[1]);
+        if constexpr ((t & 15) == 0) vout[(size_t)(i * kBlock + t) * 4] = quads_add(r8);
+        if constexpr ((t & 1) == 0) __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    auto finish = [&](auto qi) {
+      constexpr int Q = decltype(qi)::value;
+#pragma unroll
+      for (int k = 0; k < JQ; ++k) {
+        const int j = Q * JQ + k, t = j * NW + w, ts = t - Q * QT;
+        float pp = 0.f, dd = 0.f;
+#pragma unroll
+        for (int m = 0; m < NW; ++m) pp += part[Q & 1][0][m][ts][lane], dd += part[Q & 1][1][m][ts][lane];
+        const float d = in[t][lane].x, g = gs[t][lane], gd = fmaf(pp, own[j].x, dd) * own[j].slope;
+        const unsigned at = col + (unsigned)(i * kBlock + t) * row_bytes;
+        gbias += gd;
+        gD = fmaf(g, own[j].x, gD);
+        Io<T>::store(gx, at, fmaf(pp, d, D * g));
+        Io<T>::store(gdt, at, gd);
+        if (GATE) {
+          float u = D * own[j].x;
+#pragma unroll
+          for (int m = 0; m < NW; ++m) u += upart[GATE ? m : 0][GATE ? t : 0][lane];
+          const float sg = scan::sigmoid(own[j].z);
+          Io<T>::store(gz, at, own[j].gy * u * sg * fmaf(own[j].z, 1.f - sg, 1.f));
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    quarter(std::integral_constant<int, 3>());
+    __syncthreads();
+    finish(std::integral_constant<int, 3>());
+    quarter(std::integral_constant<int, 2>());
+    __syncthreads();
+    finish(std::integral_constant<int, 2>());
+    each<kBlock / 2>([&](auto ti) {   // the first half's
+      constexpr int t = decltype(ti)::value;
+      const float d = in[t][lane].x;
+      a[t][0] = __builtin_amdgcn_exp2f(d * A2[0]);
+      a[t][1] = __builtin_amdgcn_exp2f(d * A2[1]);
+    });
+    quarter(std::integral_constant<int, 1>());
+    __syncthreads();
+    finish(std::integral_constant<int, 1>());
+    quarter(std::integral_constant<int, 0>());
+    __syncthreads();
+    // in, gs and own are this wave's own tokens' here, so the next block's may follow
+    finish(std::integral_constant<int, 0>());
+    gA[0] += gAb[0];   // block by block: fewer additions behind a sum
+    gA[1] += gAb[1];
+  }
+  // behind the row's end the gradients are 0
+  if (s.on) {
+    for (int t = max(end, t0) + w; t < t1; t += NW) {
+      const size_t at = ((size_t)s.b * q.T + t) * q.C + s.c;
+      chan::st((T*)p.grad_x + at, 0.f);
+      chan::st((T*)p.grad_dt + at, 0.f);
+      if (GATE) chan::st((T*)p.grad_z + at, 0.f);
+    }
+  }
+  // parameters' gradients: a row [N + 2][C] of this batch row and segment
+  float* out = rows + ((size_t)s.b * q.segs + s.seg) * (q.N + 2) * q.C + s.c;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int n = w * 2 + i;
+    if (has[i]) {
+      out[(size_t)n * q.C] = gA[i];
+      if (p.grad_h0 && s.seg == 0) p.grad_h0[((size_t)s.b * q.C + s.c) * q.N + n] = K[i];
+    }
+  }
+  __syncthreads();
+  in[w][lane] = float2{gD, gbias};
+  __syncthreads();
+  if (w == 0 && s.on) {
+    gD = gbias = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) gD += in[k][lane].x, gbias += in[k][lane].y;
+    out[(size_t)q.N * q.C] = gD;
+    out[(size_t)(q.N + 1) * q.C] = gbias;
+  }
+}
+
+// More states: eight waves take them two at a time in NCH turns, whose adjoints and grad_A
+// wait in LDS.  Half a block is worked on at a time, the states of its second half from
+// the block's start.
+template <typename T, int NCH>
+__global__ __launch_bounds__(512) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt,
                                                           const float* ends, const float* sums, float* vpart, float* rows) {
-  constexpr int SUB = 16, J = SUB / NW;
+  constexpr int NW = 8, SUB = 16, J = SUB / NW;
   __shared__ float2 in[kBlock][kLanes];      // d, d x
   __shared__ float gs[kBlock][kLanes];       // g
   __shared__ float part[3][NW][SUB][kLanes]; // each wave's share of p, sum A q, sum C h
-  __shared__ float later[NCH > 1 ? NCH * 4 : 1][NW][kLanes];   // K0, K1, grad_A0, grad_A1 of each turn
+  __shared__ float later[NCH * 4][NW][kLanes];   // K0, K1, grad_A0, grad_A1 of each turn
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Place s = place_of(q);
   const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T), end = min(t1, len);
   const size_t nc = (size_t)q.N * q.C;
   const int blocks = q.Tp / kBlock;
-  float A[2], A2[2], K[2], gA[2] = {0.f, 0.f};
+  float A[2], A2[2], K[2], gA[2];
   auto load_turn = [&](int ch) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -171,18 +395,8 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int n = (ch * NW + w) * 2 + i;
-      K[i] = 0.f;
-      if (n < q.N && s.on) {
-        if (s.seg == q.segs - 1) {
-          if (p.grad_h) K[i] = p.grad_h[((size_t)s.b * q.C + s.c) * q.N + n];
-        } else {
-          const size_t slot = (size_t)s.b * q.segs * nc + (size_t)n * q.C + s.c;
-          K[i] = ends[slot + (size_t)(q.segs - 1) * nc];
-          for (int k = q.segs - 2; k > s.seg; --k)
-            K[i] = fmaf(__builtin_amdgcn_exp2f(A2[i] * sums[((size_t)s.b * q.segs + k) * q.C + s.c]), K[i], ends[slot + k * nc]);
-        }
-      }
-      if (NCH > 1) later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = 0.f;
+      K[i] = adjoint_behind(p, q, s, n, A2[i], ends, sums);
+      later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = 0.f;
     }
   }
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
@@ -190,8 +404,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
   const size_t row0 = (size_t)s.b * q.T * q.C + s.c;
   const T *x = (const T*)p.x + row0, *dt = (const T*)p.dt + row0, *z = (const T*)p.z + row0, *gy = (const T*)p.grad_y + row0;
   T *gx = (T*)p.grad_x + row0, *gdt = (T*)p.grad_dt + row0, *gz = (T*)p.grad_z + row0;
-  // the lane's place among the 64 sums of a half block: token and which of B0, B1, C0, C1
-  const int mine = ((lane >> 3 & 1) | (lane >> 2 & 1) << 1 | (lane >> 1 & 1) << 2 | (lane & 1) << 3) * 4 + (lane >> 5 | (lane >> 4 & 1) << 1);
+  const int mine = sum_place();
   float gD = 0.f, gbias = 0.f;
 
   for (int tt = t0 + (t1 - 1 - t0) / kBlock * kBlock; tt >= t0; tt -= kBlock) {
@@ -234,7 +447,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
       const int st = sub * SUB;
 #pragma unroll
       for (int ch = 0; ch < NCH; ++ch) {
-        if (NCH > 1) {
+        {
           load_turn(ch);
 #pragma unroll
           for (int i = 0; i < 2; ++i) K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
@@ -300,7 +513,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
         });
         vpart[((((size_t)s.cb * q.B + s.b) * q.pairs + ch * NW + w) * q.Tp + tt + st) * 4 + mine] =
             quads_add(r8);
-        if (NCH > 1) {
+        {
 #pragma unroll
           for (int i = 0; i < 2; ++i) later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = gA[i];
         }
@@ -343,7 +556,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int n = (ch * NW + w) * 2 + i;
-      if (NCH > 1) K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
+      K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
       if (n < q.N && s.on) {
         out[(size_t)n * q.C] = gA[i];
         if (p.grad_h0 && s.seg == 0) p.grad_h0[((size_t)s.b * q.C + s.c) * q.N + n] = K[i];
@@ -441,10 +654,15 @@ static hipError_t bwd(const gdr_ssm_bwd_args& a, hipStream_t s) {
     else hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 8>), grid, dim3(512), 0, s, a, q, ends, sums);
   }
   const dim3 grid(q.blocks());
-  if (q.N <= 8) hipLaunchKernelGGL((ssm_bwd_kernel<T, 4, 1>), grid, dim3(256), 0, s, a, q, ckpt, ends, sums, vpart, rows);
-  else if (q.N <= 16) hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 1>), grid, dim3(512), 0, s, a, q, ckpt, ends, sums, vpart, rows);
-  else if (q.N <= 32) hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 2>), grid, dim3(512), 0, s, a, q, ckpt, ends, sums, vpart, rows);
-  else hipLaunchKernelGGL((ssm_bwd_kernel<T, 8, 4>), grid, dim3(512), 0, s, a, q, ckpt, ends, sums, vpart, rows);
+#define SSM_BWD(KERNEL, THREADS) \
+  hipLaunchKernelGGL((KERNEL), grid, dim3(THREADS), 0, s, a, q, ckpt, ends, sums, vpart, rows)
+  if (q.N <= 8 && a.z) SSM_BWD((ssm_bwd_kernel<T, 4, true>), 256);
+  else if (q.N <= 8) SSM_BWD((ssm_bwd_kernel<T, 4, false>), 256);
+  else if (q.N <= 16 && a.z) SSM_BWD((ssm_bwd_kernel<T, 8, true>), 512);
+  else if (q.N <= 16) SSM_BWD((ssm_bwd_kernel<T, 8, false>), 512);
+  else if (q.N <= 32) SSM_BWD((ssm_bwd_wide_kernel<T, 2>), 512);
+  else SSM_BWD((ssm_bwd_wide_kernel<T, 4>), 512);
+#undef SSM_BWD
   const size_t blocks = ((size_t)q.B * q.G * q.pairs * q.Tp + 255) / 256;
   hipLaunchKernelGGL(ssm_vector_join_kernel<T>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s,
                      (const f4*)vpart, q, a.lens, (T*)a.grad_Bv, (T*)a.grad_Cv);

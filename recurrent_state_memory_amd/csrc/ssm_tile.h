@@ -174,6 +174,14 @@ struct Vectors {
         r.c[i][k] = Io<T>::load(Cv, o);
       }
   }
+  // Between two passes over the same vectors: else the compiler keeps the first one's lane
+  // reads in registers of their own for the second.
+  static __device__ inline void forget(Set& v) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int k = 0; k < Q; ++k) asm volatile("" : "+v"(v.b[i][k]), "+v"(v.c[i][k]));
+  }
   static __device__ inline void take(const Raw& r, Set& v) {
 #pragma unroll
     for (int i = 0; i < P; ++i)
