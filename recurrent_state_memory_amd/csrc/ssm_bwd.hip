@@ -245,8 +245,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
     }
     typename Vectors<T, 2, kBlock>::Set v;
     vectors.take(vr, v);
-    // the decays of half a block: all of them would spill registers
-    float h[kBlock + 1][2], a[kBlock / 2][2];
+    float h[kBlock + 1][2], a[kBlock][2];
     h[0][0] = nh[0], h[0][1] = nh[1];
     __syncthreads();
     if (i > 0) load(i - 1);
@@ -254,11 +253,10 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
       constexpr int t = decltype(ti)::value, L = t % 8 * 2;
       const float2 d = in[t][lane];
       const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
-      constexpr int H = t % (kBlock / 2);
-      a[H][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
-      a[H][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
-      h[t + 1][0] = fmaf(a[H][0], h[t][0], d.y * row_lane<L>(bv));
-      h[t + 1][1] = fmaf(a[H][1], h[t][1], d.y * row_lane<L + 1>(bv));
+      a[t][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
+      a[t][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
+      h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
+      h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
       if constexpr (GATE) upart[w][t][lane] = fmaf(row_lane<L + 1>(cv), h[t + 1][1], row_lane<L>(cv) * h[t + 1][0]);
       if constexpr ((t & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // else loads of many tokens take the registers
     });
@@ -267,14 +265,14 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
     auto quarter = [&](auto qi) {
       constexpr int Q = decltype(qi)::value;
       each<QT>([&](auto back) {
-        constexpr int ts = QT - 1 - decltype(back)::value, t = Q * QT + ts, L = t % 8 * 2, H = t % (kBlock / 2);
+        constexpr int ts = QT - 1 - decltype(back)::value, t = Q * QT + ts, L = t % 8 * 2;
         const float2 d = in[t][lane];
         const float g = gs[t][lane], bv = v.b[0][t / 8], cv = v.c[0][t / 8];
         const float H0 = fmaf(row_lane<L>(cv), g, K[0]), H1 = fmaf(row_lane<L + 1>(cv), g, K[1]);
         const float vb = swap32_add(H0 * d.y, H1 * d.y), vc = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
         part[Q & 1][0][w][ts][lane] = fmaf(row_lane<L + 1>(bv), H1, row_lane<L>(bv) * H0);
-        K[0] = H0 * a[H][0];
-        K[1] = H1 * a[H][1];
+        K[0] = H0 * a[t][0];
+        K[1] = H1 * a[t][1];
         const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];
         gAb[0] = fmaf(d.x, q0, gAb[0]);
         gAb[1] = fmaf(d.x, q1, gAb[1]);
@@ -317,12 +315,6 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
     quarter(std::integral_constant<int, 2>());
     __syncthreads();
     finish(std::integral_constant<int, 2>());
-    each<kBlock / 2>([&](auto ti) {   // the first half's
-      constexpr int t = decltype(ti)::value;
-      const float d = in[t][lane].x;
-      a[t][0] = __builtin_amdgcn_exp2f(d * A2[0]);
-      a[t][1] = __builtin_amdgcn_exp2f(d * A2[1]);
-    });
     quarter(std::integral_constant<int, 1>());
     __syncthreads();
     finish(std::integral_constant<int, 1>());
