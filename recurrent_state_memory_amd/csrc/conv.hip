@@ -1,7 +1,7 @@
 // conv.hip -- short causal convolution, its backward and its single-token step, gfx950.
 //
-// A thread holds one 16-byte run of channels and walks a stretch of tokens with the last
-// K rows in registers, so x is read once (the K - 1 rows ahead of a stretch come from the
+// A thread holds one 16-byte run of channels (four channels in the backward) and walks a
+// stretch of tokens with the last K rows in registers, so x is read once (the K - 1 rows ahead of a stretch come from the
 // caches).  LX threads of a workgroup share a row, the other 256 / LX take further
 // stretches.  Bound by HBM.
 #include <type_traits>
@@ -18,6 +18,40 @@ using chan::Run;
 
 constexpr float kLog2e = 1.44269504f;
 constexpr int kThreads = 256;
+
+// Four channels a thread, 8 bytes of bf16: half the registers of a whole run.
+template <typename T>
+struct Four : Run<T> {};
+template <>
+struct Four<__bf16> {
+  static constexpr int N = 4;
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  typedef chan::raw2 at2 __attribute__((aligned(2), may_alias));
+  static __device__ inline raw4 load(const __bf16* p, int n) {
+    if (n >= N) {
+      const chan::raw2 r = *(const at2*)p;
+      return raw4{r[0], r[1], 0u, 0u};
+    }
+    raw4 r = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < N - 1; ++k)
+      if (k < n) r[k >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, p[k]) << (16 * (k & 1));
+    return r;
+  }
+  static __device__ inline float get(const raw4& r, int k) { return Run<__bf16>::get(r, k); }
+  static __device__ inline void store(__bf16* p, int n, const float (&v)[N]) {
+    if (n >= N) {
+      bf16x4 h;
+#pragma unroll
+      for (int k = 0; k < N; ++k) h[k] = (__bf16)v[k];
+      *(at2*)p = __builtin_bit_cast(chan::raw2, h);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < n) p[k] = (__bf16)v[k];
+    }
+  }
+};
 
 __device__ inline float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e)); }
 
@@ -60,10 +94,10 @@ __device__ inline Spot spot_of(const Plan& q, int T, int C) {
   return s;
 }
 
-template <typename T>
-__device__ inline void unpack(const raw4& r, float (&v)[Run<T>::N]) {
+template <typename R, int N>
+__device__ inline void unpack(const raw4& r, float (&v)[N]) {
 #pragma unroll
-  for (int k = 0; k < Run<T>::N; ++k) v[k] = Run<T>::get(r, k);
+  for (int k = 0; k < N; ++k) v[k] = R::get(r, k);
 }
 
 __device__ inline int row_len(const int32_t* lens, int b, int T) {
@@ -93,21 +127,22 @@ __device__ inline void load_params(const float* weight, const float* bias, const
 
 // The K - 1 rows before token t0, oldest first: of the sequence (0 behind its end), or of
 // the state.
-template <typename T, int K>
+template <typename R, int K, typename T>
 __device__ inline void load_before(const T* x, const T* state, const Spot& s, int len, int C, raw4 (&r)[K - 1]) {
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) {
     const int t = s.t0 - (K - 1) + i;
     r[i] = raw4{0u, 0u, 0u, 0u};
     if (t >= 0) {
-      if (t < len) r[i] = Run<T>::load(x + (ptrdiff_t)t * C, s.n);
-    } else if (state) r[i] = Run<T>::load(state + (ptrdiff_t)(t + K - 1) * C, s.n);
+      if (t < len) r[i] = R::load(x + (ptrdiff_t)t * C, s.n);
+    } else if (state) r[i] = R::load(state + (ptrdiff_t)(t + K - 1) * C, s.n);
   }
 }
 
 template <typename T, int K, int U>
 __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(gdr_conv_args p, Plan q) {
-  constexpr int N = Run<T>::N;
+  typedef Run<T> R;
+  constexpr int N = R::N;
   const int C = p.C;
   const Spot s = spot_of<N>(q, p.T, C);
   if (s.n <= 0 || s.t0 >= p.T) return;
@@ -118,7 +153,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(gdr_conv_args p, Pla
   {
     const T* state = p.state ? (const T*)p.state + (size_t)s.b * (K - 1) * C + s.c0 : nullptr;
     raw4 r[K - 1];
-    load_before<T, K>(x, state, s, len, C, r);
+    load_before<R, K>(x, state, s, len, C, r);
     if (s.t0 == 0 && p.state_out) {
       // the row's last K - 1 inputs; this thread alone reads its part of the state, so it
       // may be overwritten from here on
@@ -128,18 +163,18 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(gdr_conv_args p, Pla
         const int i = len + j;   // among the state's rows and the tokens behind them
         raw4 v = r[K - 2];
         if (i >= K - 1) {
-          v = Run<T>::load(x + (ptrdiff_t)(i - (K - 1)) * C, s.n);
+          v = R::load(x + (ptrdiff_t)(i - (K - 1)) * C, s.n);
         } else {
 #pragma unroll
           for (int k = 0; k < K - 2; ++k) v = i == k ? r[k] : v;
         }
         float o[N];
-        unpack<T>(v, o);
-        Run<T>::store(so + (ptrdiff_t)j * C, s.n, o);
+        unpack<R>(v, o);
+        R::store(so + (ptrdiff_t)j * C, s.n, o);
       }
     }
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) unpack<T>(r[i], f[i]);
+    for (int i = 0; i < K - 1; ++i) unpack<R>(r[i], f[i]);
   }
   float w[K][N], bias[N];
   load_params<N, K>(p.weight, p.bias, s, w, bias);
@@ -147,10 +182,10 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(gdr_conv_args p, Pla
     raw4 r[U];
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      r[i] = t + i < min(t1, len) ? Run<T>::load(x + (ptrdiff_t)(t + i) * C, s.n) : raw4{0u, 0u, 0u, 0u};
+      r[i] = t + i < min(t1, len) ? R::load(x + (ptrdiff_t)(t + i) * C, s.n) : raw4{0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      unpack<T>(r[i], f[K - 1 + i]);
+      unpack<R>(r[i], f[K - 1 + i]);
       if (t + i >= t1) break;
       float o[N];
 #pragma unroll
@@ -161,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(gdr_conv_args p, Pla
         if (p.silu) a *= sigmoid(a);
         o[k] = t + i < len ? a : 0.f;
       }
-      Run<T>::store(y + (ptrdiff_t)(t + i) * C, s.n, o);
+      R::store(y + (ptrdiff_t)(t + i) * C, s.n, o);
     }
 #pragma unroll
     for (int i = 0; i < K - 1; ++i)
@@ -175,7 +210,8 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(gdr_conv_args p, Pla
 // [K + 1][C] of the weight's and the bias' sums for the join.
 template <typename T, int K, int U>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(gdr_conv_bwd_args p, Plan q) {
-  constexpr int N = Run<T>::N;
+  typedef Four<T> R;
+  constexpr int N = R::N;
   const int C = p.C;
   const Spot s = spot_of<N>(q, p.T, C);
   float dw[K + 1][N];   // the last one is the bias'
@@ -196,10 +232,10 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(gdr_conv_bwd_args p,
     float f[K - 1 + U][N], d[K - 1 + U][N];
     {
       raw4 r[K - 1];
-      load_before<T, K>(x, p.state ? (const T*)p.state + edge0 : nullptr, s, len, C, r);
+      load_before<R, K>(x, p.state ? (const T*)p.state + edge0 : nullptr, s, len, C, r);
 #pragma unroll
       for (int i = 0; i < K - 1; ++i) {
-        unpack<T>(r[i], f[i]);
+        unpack<R>(r[i], f[i]);
 #pragma unroll
         for (int k = 0; k < N; ++k) d[i][k] = 0.f;
       }
@@ -209,16 +245,16 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(gdr_conv_bwd_args p,
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const bool on = t + i < min(t1 + K - 1, len);
-        rx[i] = on ? Run<T>::load(x + (ptrdiff_t)(t + i) * C, s.n) : raw4{0u, 0u, 0u, 0u};
-        rg[i] = on ? Run<T>::load(gy + (ptrdiff_t)(t + i) * C, s.n) : raw4{0u, 0u, 0u, 0u};
+        rx[i] = on ? R::load(x + (ptrdiff_t)(t + i) * C, s.n) : raw4{0u, 0u, 0u, 0u};
+        rg[i] = on ? R::load(gy + (ptrdiff_t)(t + i) * C, s.n) : raw4{0u, 0u, 0u, 0u};
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        unpack<T>(rx[i], f[K - 1 + i]);
+        unpack<R>(rx[i], f[K - 1 + i]);
         const bool on = t + i < len;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          float g = Run<T>::get(rg[i], k);
+          float g = R::get(rg[i], k);
           if (p.silu) {
             float u = bias[k];
 #pragma unroll
@@ -250,12 +286,12 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(gdr_conv_bwd_args p,
           }
           const int e = o - len + K - 1;   // its place in state_out
           if (gso && e >= 0 && e < K - 1) {
-            const raw4 r = Run<T>::load(gso + (ptrdiff_t)e * C, s.n);
+            const raw4 r = R::load(gso + (ptrdiff_t)e * C, s.n);
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] += Run<T>::get(r, k);
+            for (int k = 0; k < N; ++k) v[k] += R::get(r, k);
           }
-          if (o >= 0) Run<T>::store(gx + (ptrdiff_t)o * C, s.n, v);
-          else Run<T>::store(gs + (ptrdiff_t)(o + K - 1) * C, s.n, v);
+          if (o >= 0) R::store(gx + (ptrdiff_t)o * C, s.n, v);
+          else R::store(gs + (ptrdiff_t)(o + K - 1) * C, s.n, v);
         }
       }
 #pragma unroll
@@ -310,7 +346,8 @@ struct ParamGrads {
 
 template <typename T, int K>
 __global__ __launch_bounds__(kThreads) void conv_step_kernel(gdr_conv_step_args p, int runs) {
-  constexpr int N = Run<T>::N;
+  typedef Run<T> R;
+  constexpr int N = R::N;
   const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x, row = i / runs;
   if (row >= (size_t)p.N) return;
   Spot s;
@@ -320,11 +357,11 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(gdr_conv_step_args 
   const T* in = (const T*)p.state + at;
   float f[K][N];
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) unpack<T>(Run<T>::load(in + j * C, s.n), f[j]);
-  unpack<T>(Run<T>::load((const T*)p.x + row * C + s.c0, s.n), f[K - 1]);
+  for (int j = 0; j < K - 1; ++j) unpack<R>(R::load(in + j * C, s.n), f[j]);
+  unpack<R>(R::load((const T*)p.x + row * C + s.c0, s.n), f[K - 1]);
   T* out = (T*)p.state_out + at;
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) Run<T>::store(out + j * C, s.n, f[j + 1]);
+  for (int j = 0; j < K - 1; ++j) R::store(out + j * C, s.n, f[j + 1]);
   float w[K][N], o[N];
   load_params<N, K>(p.weight, p.bias, s, w, o);
 #pragma unroll
@@ -333,13 +370,13 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(gdr_conv_step_args 
     for (int j = 0; j < K; ++j) o[k] = fmaf(w[j][k], f[j][k], o[k]);
     if (p.silu) o[k] *= sigmoid(o[k]);
   }
-  Run<T>::store((T*)p.y + row * C + s.c0, s.n, o);
+  R::store((T*)p.y + row * C + s.c0, s.n, o);
 }
 
 constexpr int kLongest = 64;   // tokens of a stretch
 
-size_t bwd_workspace(int B, int T, int C, int K, int io_dtype) {
-  const Plan q = plan_of(B, T, C, io_dtype == GDR_BF16 ? 8 : 4, kLongest);
+size_t bwd_workspace(int B, int T, int C, int K) {
+  const Plan q = plan_of(B, T, C, 4, kLongest);
   return ((size_t)B * q.rows * (K + 1) * C * 4 + 255) / 256 * 256;
 }
 
@@ -369,7 +406,7 @@ hipError_t launch_conv_fwd(const gdr_conv_args& a, hipStream_t s) {
 
 hipError_t launch_conv_bwd(const gdr_conv_bwd_args& a, hipStream_t s) {
   const bool bf = a.io_dtype == GDR_BF16;
-  const Plan q = plan_of(a.B, a.T, a.C, bf ? 8 : 4, kLongest);
+  const Plan q = plan_of(a.B, a.T, a.C, 4, kLongest);
   with_taps(a.K, [&](auto k) {
     constexpr int K = decltype(k)::value, U = K > 4 ? 1 : 4;
     if (bf) hipLaunchKernelGGL((conv_bwd_kernel<__bf16, K, U>), dim3(q.blocks(a.B)), dim3(kThreads), 0, s, a, q);

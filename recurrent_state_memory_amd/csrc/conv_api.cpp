@@ -82,13 +82,13 @@ gdr_status gdr_conv_fwd(const gdr_conv_args* a, void* stream) {
 
 size_t gdr_conv_bwd_workspace(const gdr_conv_bwd_args* a) {
   if (check_bwd(a) != GDR_OK) return 0;
-  return gdr::conv::bwd_workspace(a->B, a->T, a->C, a->K, a->io_dtype);
+  return gdr::conv::bwd_workspace(a->B, a->T, a->C, a->K);
 }
 
 gdr_status gdr_conv_bwd(const gdr_conv_bwd_args* a, void* stream) {
   const gdr_status st = check_bwd(a);
   if (st != GDR_OK) return st;
-  if (!a->workspace || a->workspace_bytes < gdr::conv::bwd_workspace(a->B, a->T, a->C, a->K, a->io_dtype))
+  if (!a->workspace || a->workspace_bytes < gdr::conv::bwd_workspace(a->B, a->T, a->C, a->K))
     return GDR_ERR_WORKSPACE;
   return done(gdr::conv::launch_conv_bwd(*a, static_cast<hipStream_t>(stream)));
 }

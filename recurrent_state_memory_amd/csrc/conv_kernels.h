@@ -16,7 +16,7 @@ constexpr bool too_many_tiles(int B, int T, int C) {
   return (long long)B * ((C + 255) / 256) * ((T + 255) / 256) >= (1LL << 22);
 }
 
-size_t bwd_workspace(int B, int T, int C, int K, int io_dtype);
+size_t bwd_workspace(int B, int T, int C, int K);
 
 // Arguments already checked; a.workspace large enough.
 hipError_t launch_conv_fwd(const gdr_conv_args& a, hipStream_t s);

@@ -1,7 +1,7 @@
 // gnorm.hip -- gated group norm forward and backward, gfx950.
 //
 // A group of a row is held in registers by L threads of NV 16-byte runs each (thread l has
-// runs l, l + L, ...), so everything is read once: the mean, then the squares about it,
+// runs l, l + L, ...; the forward asks for the next row ahead), so everything is read once: the mean, then the squares about it,
 // then the outputs.  L is a part of a wave for short groups (several groups side by side in
 // a wave, no barrier) or up to 1024 threads.  Bound by HBM.
 #include "chan_device.h"
@@ -61,23 +61,47 @@ __device__ inline void load_param(const float* p, int c0, int n, float none, flo
   }
 }
 
+// A thread keeps one group's columns for all its rows, so its weights (and in the backward
+// the columns' sums) stay in registers: a workgroup's TH / L places go to `wide` groups of
+// blockIdx.y, `deep` rows of each at a time.
+struct Lay {
+  int wide, deep;
+  unsigned rows, groups;   // workgroups along the rows and along the groups
+};
+
 template <typename T, int L, int NV>
-__global__ __launch_bounds__(fwd_threads(L)) void gnorm_fwd_kernel(gdr_gnorm_args p) {
-  constexpr int N = Run<T>::N, TH = fwd_threads(L), kPer = TH / L;
+__global__ __launch_bounds__(fwd_threads(L)) void gnorm_fwd_kernel(gdr_gnorm_args p, Lay q) {
+  constexpr int N = Run<T>::N, TH = fwd_threads(L);
   __shared__ Parts<TH, 1> sums;
   int turn = 0;
   const int l = threadIdx.x % L, D = p.C / p.G;
-  const int64_t total = p.R * p.G, step = (int64_t)gridDim.x * kPer;
-  for (int64_t i = (int64_t)blockIdx.x * kPer + threadIdx.x / L; i < total; i += step) {
-    const int g = (int)(i % p.G);
-    const T* x = (const T*)p.x + (size_t)i * D;   // rows and their groups follow each other
-    raw4 r[NV], rz[NV];
+  const int place = threadIdx.x / L, m = place / q.wide, g = (int)blockIdx.y * q.wide + place - m * q.wide;
+  if (m >= q.deep || g >= p.G) return;   // never a part of a group, and no barrier is for more than one
+  float w[NV][N], b[NV][N];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c0 = (j * L + l) * N;
+    load_param<N>(p.weight, g * D + c0, D - c0, 1.f, w[j]);
+    load_param<N>(p.bias, g * D + c0, D - c0, 0.f, b[j]);
+  }
+  const float inv = 1.f / D;
+  const int64_t first = (int64_t)blockIdx.x * q.deep + m, step = (int64_t)gridDim.x * q.deep;
+  raw4 nx[NV], nz[NV];   // the next row
+  auto load = [&](int64_t row) {
+    const size_t at = (size_t)row * p.C + (size_t)g * D;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c0 = (j * L + l) * N;
-      r[j] = Run<T>::load(x + c0, D - c0);
-      rz[j] = p.z ? Run<T>::load((const T*)p.z + (size_t)i * D + c0, D - c0) : raw4{};
+      nx[j] = Run<T>::load((const T*)p.x + at + c0, D - c0);
+      nz[j] = p.z ? Run<T>::load((const T*)p.z + at + c0, D - c0) : raw4{};
     }
+  };
+  if (first < p.R) load(first);
+  for (int64_t row = first; row < p.R; row += step) {
+    raw4 r[NV], rz[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) r[j] = nx[j], rz[j] = nz[j];
+    if (row + step < p.R) load(row + step);
     float mean = 0.f, s[1];
     if (p.center) {
       s[0] = 0.f;
@@ -86,7 +110,7 @@ __global__ __launch_bounds__(fwd_threads(L)) void gnorm_fwd_kernel(gdr_gnorm_arg
 #pragma unroll
         for (int k = 0; k < N; ++k) s[0] += Run<T>::get(r[j], k);   // 0 behind the group's end
       group_sum<TH, L>(s, sums, turn);
-      mean = s[0] / D;
+      mean = s[0] * inv;
     }
     s[0] = 0.f;
 #pragma unroll
@@ -97,37 +121,30 @@ __global__ __launch_bounds__(fwd_threads(L)) void gnorm_fwd_kernel(gdr_gnorm_arg
         s[0] = fmaf(c, c, s[0]);
       }
     group_sum<TH, L>(s, sums, turn);
-    const float rstd = 1.f / sqrtf(s[0] / D + p.eps);
+    const float rstd = 1.f / sqrtf(fmaf(s[0], inv, p.eps));
     if (l == 0) {
-      if (p.mean) p.mean[i] = mean;
-      if (p.rstd) p.rstd[i] = rstd;
+      const size_t st = (size_t)row * p.G + g;
+      if (p.mean) p.mean[st] = mean;
+      if (p.rstd) p.rstd[st] = rstd;
     }
-    T* y = (T*)p.y + (size_t)i * D;
+    T* y = (T*)p.y + (size_t)row * p.C + (size_t)g * D;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c0 = (j * L + l) * N, n = D - c0;
-      float o[N], w[N], b[N];
-      load_param<N>(p.weight, g * D + c0, n, 1.f, w);
-      load_param<N>(p.bias, g * D + c0, n, 0.f, b);
+      const int c0 = (j * L + l) * N;
+      float o[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const float u = fmaf((Run<T>::get(r[j], k) - mean) * rstd, w[k], b[k]);
+        const float u = fmaf((Run<T>::get(r[j], k) - mean) * rstd, w[j][k], b[j][k]);
         const float v = p.z ? Run<T>::get(rz[j], k) : u;
-        float a = p.silu ? v * sigmoid(v) : v;
+        const float a = p.silu ? v * sigmoid(v) : v;
         o[k] = p.z ? u * a : a;
       }
-      Run<T>::store(y + c0, n, o);
+      Run<T>::store(y + c0, D - c0, o);
     }
   }
 }
 
-// Backward.  A thread keeps one group's columns for all its rows, so that the columns'
-// sums stay in registers: a workgroup's TH / L places go to `wide` groups of blockIdx.y,
-// `deep` rows of each at a time.  A workgroup leaves one partial row [2][C] for the join.
-struct Lay {
-  int wide, deep;
-  unsigned rows, groups;   // workgroups along the rows and along the groups
-};
+// Backward.  A workgroup leaves one partial row [2][C] of the columns' sums for the join.
 template <typename T, int L, int NV>
 __global__ __launch_bounds__(bwd_threads(L)) void gnorm_bwd_kernel(gdr_gnorm_bwd_args p, Lay q) {
   constexpr int N = Run<T>::N, TH = bwd_threads(L);
@@ -260,34 +277,36 @@ static Shape shape_of(int D, int n) {
   return s;
 }
 
-static Lay lay_of(int64_t R, int G, const Shape& s) {
-  const int TH = bwd_threads(s.L), places = TH / s.L;
+// Workgroups of TH threads for R rows of G groups, `threads` in all at the most.
+static Lay lay_of(int64_t R, int G, const Shape& s, int TH, int64_t threads) {
+  const int places = TH / s.L;
   Lay q;
   q.wide = places < G ? places : G;
   q.deep = places / q.wide;
   q.groups = (unsigned)((G + q.wide - 1) / q.wide);
-  // 2 x 1024 threads a CU; more rows of partial sums than that cost the join more than
-  // they hide
-  const int64_t want = (R + q.deep - 1) / q.deep, most = (int64_t)(524288 / TH + q.groups - 1) / q.groups;
+  const int64_t want = (R + q.deep - 1) / q.deep, most = (threads / TH + q.groups - 1) / q.groups;
   q.rows = (unsigned)(want < most ? want : most);
   return q;
 }
 
+// 2 x 1024 threads a CU in the backward: more rows of partial sums than that cost the join
+// more than they hide.
+static Lay bwd_lay(int64_t R, int G, const Shape& s) { return lay_of(R, G, s, bwd_threads(s.L), 524288); }
+
 size_t bwd_workspace(int64_t R, int C, int G, int io_dtype) {
-  const Lay q = lay_of(R, G, shape_of(C / G, io_dtype == GDR_BF16 ? 8 : 4));
+  const Lay q = bwd_lay(R, G, shape_of(C / G, io_dtype == GDR_BF16 ? 8 : 4));
   return ((size_t)q.rows * 2 * C * 4 + 255) / 256 * 256;
 }
 
 template <typename T, int L, int NV>
 static void fwd(const gdr_gnorm_args& a, hipStream_t s) {
-  constexpr int TH = fwd_threads(L), kPer = TH / L;
-  const int64_t want = (a.R * a.G + kPer - 1) / kPer;
-  const unsigned blocks = (unsigned)(want < (1 << 16) ? want : (1 << 16));
-  hipLaunchKernelGGL((gnorm_fwd_kernel<T, L, NV>), dim3(blocks), dim3(TH), 0, s, a);
+  constexpr int TH = fwd_threads(L);
+  const Lay q = lay_of(a.R, a.G, Shape{L, NV}, TH, 1 << 20);
+  hipLaunchKernelGGL((gnorm_fwd_kernel<T, L, NV>), dim3(q.rows, q.groups), dim3(TH), 0, s, a, q);
 }
 template <typename T, int L, int NV>
 static void bwd(const gdr_gnorm_bwd_args& a, hipStream_t s) {
-  const Lay q = lay_of(a.R, a.G, Shape{L, NV});
+  const Lay q = bwd_lay(a.R, a.G, Shape{L, NV});
   hipLaunchKernelGGL((gnorm_bwd_kernel<T, L, NV>), dim3(q.rows, q.groups), dim3(bwd_threads(L)), 0, s, a, q);
   if (a.grad_weight || a.grad_bias)
     launch_col_join((const float*)a.workspace, q.rows, (size_t)2 * a.C, ParamGrads{(size_t)a.C, a.grad_weight, a.grad_bias}, s);

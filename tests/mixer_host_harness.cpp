@@ -13,7 +13,7 @@ static int g_launches = 0;
 
 namespace gdr {
 namespace conv {
-size_t bwd_workspace(int, int, int, int, int) { return 4096; }
+size_t bwd_workspace(int, int, int, int) { return 4096; }
 hipError_t launch_conv_fwd(const gdr_conv_args&, hipStream_t) { return ++g_launches, hipSuccess; }
 hipError_t launch_conv_bwd(const gdr_conv_bwd_args&, hipStream_t) { return ++g_launches, hipErrorInvalidValue; }
 hipError_t launch_conv_step(const gdr_conv_step_args&, hipStream_t) { return ++g_launches, hipSuccess; }

@@ -85,7 +85,8 @@ def test_ssm_refusals():
     refuse("gdr_ssm_fwd", gdr.SsmArgs, base, SIZES[:4] + missing + shapes + [
         (dict(y=None), N), (dict(x=P(0, 1)), L), (dict(A=P(2, 2)), L), (dict(D=P(6, 1)), L), (dict(h0=P(7, 2)), L),
         (dict(lens=P(8, 1)), L), (dict(workspace=P(30, 4)), L), (dict(y=P(0)), A), (dict(y=P(3, 2)), A),
-        (dict(h0=P(7), h_out=P(7, 4)), A), (dict(ckpt=P(5, 64)), A), (dict(workspace=None), W), (dict(workspace_bytes=256), W)])
+        (dict(h0=P(7), h_out=P(7, 4)), A), (dict(ckpt=P(5, 64)), A),
+        (dict(T=4096, workspace=None), W), (dict(T=4096, workspace_bytes=256), W)])       # segments side by side
     base = dict(base, y=None, grad_y=P(5), grad_x=P(10), grad_dt=P(11), grad_A=P(12), grad_Bv=P(13), grad_Cv=P(14))
     del base["y"]
     refuse("gdr_ssm_bwd", gdr.SsmBwdArgs, base, SIZES[:4] + missing + shapes + [
@@ -124,6 +125,10 @@ def test_null_structs_and_workspace_queries():
         assert getattr(lib, name)(None, None) == N
     for name in ("gdr_conv_bwd_workspace", "gdr_ssm_fwd_workspace", "gdr_ssm_bwd_workspace", "gdr_gnorm_bwd_workspace"):
         assert getattr(lib, name)(None) == 0
+    q = dict(B=2, C=66, N=16, G=3, io_dtype=1, softplus=1, x=P(0), dt=P(1), A=P(2), Bv=P(3), Cv=P(4), y=P(5))
+    need = lib.gdr_ssm_fwd_workspace
+    assert need(ctypes.byref(gdr.SsmArgs(**q, T=255))) == 0 and need(ctypes.byref(gdr.SsmArgs(**q, T=256))) > 0
+    assert need(ctypes.byref(gdr.SsmArgs(**dict(q, B=200), T=4096))) == 0 and need(ctypes.byref(gdr.SsmArgs(**q, T=0))) == 0
     q = dict(R=5, C=120, G=4, io_dtype=1, silu=0, x=P(0), rstd=P(1), grad_y=P(2), grad_x=P(3))
     need = lib.gdr_gnorm_bwd_workspace
     assert need(ctypes.byref(gdr.GnormBwdArgs(**q))) == 0                       # no columns' sums
