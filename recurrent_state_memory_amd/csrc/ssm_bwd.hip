@@ -249,40 +249,66 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
     h[0][0] = nh[0], h[0][1] = nh[1];
     __syncthreads();
     if (i > 0) load(i - 1);
-    each<kBlock>([&](auto ti) {
-      constexpr int t = decltype(ti)::value, L = t % 8 * 2;
-      const float2 d = in[t][lane];
-      const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
-      a[t][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
-      a[t][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
-      h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
-      h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
-      if constexpr (GATE) upart[w][t][lane] = fmaf(row_lane<L + 1>(cv), h[t + 1][1], row_lane<L>(cv) * h[t + 1][0]);
-      if constexpr ((t & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // else loads of many tokens take the registers
+    // LDS is read a group of tokens ahead; the groups stay apart, else loads of many of
+    // them take the registers
+    float2 dn[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) dn[u] = in[u][lane];
+    each<kBlock / 4>([&](auto gi) {
+      constexpr int t4 = decltype(gi)::value * 4;
+      const float2 d4[4] = {dn[0], dn[1], dn[2], dn[3]};
+      if constexpr (t4 + 4 < kBlock) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) dn[u] = in[t4 + 4 + u][lane];
+      }
+      each<4>([&](auto ui) {
+        constexpr int u = decltype(ui)::value, t = t4 + u, L = t % 8 * 2;
+        const float2 d = d4[u];
+        const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
+        a[t][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
+        a[t][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
+        h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
+        h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
+        if constexpr (GATE) upart[w][t][lane] = fmaf(row_lane<L + 1>(cv), h[t + 1][1], row_lane<L>(cv) * h[t + 1][0]);
+      });
+      __builtin_amdgcn_sched_barrier(0);
     });
     vectors.forget(v);
     float r2[2], r4[2], r8[4], gAb[2] = {0.f, 0.f};
+    float2 rd[2];
+    float rg[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) rd[u] = in[kBlock - 2 + u][lane], rg[u] = gs[kBlock - 2 + u][lane];
     auto quarter = [&](auto qi) {
       constexpr int Q = decltype(qi)::value;
-      each<QT>([&](auto back) {
-        constexpr int ts = QT - 1 - decltype(back)::value, t = Q * QT + ts, L = t % 8 * 2;
-        const float2 d = in[t][lane];
-        const float g = gs[t][lane], bv = v.b[0][t / 8], cv = v.c[0][t / 8];
-        const float H0 = fmaf(row_lane<L>(cv), g, K[0]), H1 = fmaf(row_lane<L + 1>(cv), g, K[1]);
-        const float vb = swap32_add(H0 * d.y, H1 * d.y), vc = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
-        part[Q & 1][0][w][ts][lane] = fmaf(row_lane<L + 1>(bv), H1, row_lane<L>(bv) * H0);
-        K[0] = H0 * a[t][0];
-        K[1] = H1 * a[t][1];
-        const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];
-        gAb[0] = fmaf(d.x, q0, gAb[0]);
-        gAb[1] = fmaf(d.x, q1, gAb[1]);
-        part[Q & 1][1][w][ts][lane] = fmaf(A[1], q1, A[0] * q0);
-        // tokens 2m + 1 and 2m, then pairs of them, then the four quarters of 16
-        r2[t & 1] = swap16_add(vb, vc);
-        if constexpr ((t & 1) == 0) r4[t >> 1 & 1] = half8_add(r2[0], r2[1]);
-        if constexpr ((t & 3) == 0) r8[t >> 2 & 3] = half4_add(r4[0], r4[1]);
-        if constexpr ((t & 15) == 0) vout[(size_t)(i * kBlock + t) * 4] = quads_add(r8);
-        if constexpr ((t & 1) == 0) __builtin_amdgcn_sched_barrier(0);
+      each<QT / 2>([&](auto back) {
+        constexpr int ts2 = QT - 2 - 2 * decltype(back)::value, t2 = Q * QT + ts2;
+        const float2 d2[2] = {rd[0], rd[1]};
+        const float g2[2] = {rg[0], rg[1]};
+        if constexpr (t2 > 0) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) rd[u] = in[t2 - 2 + u][lane], rg[u] = gs[t2 - 2 + u][lane];
+        }
+        each<2>([&](auto ui) {
+          constexpr int u = 1 - decltype(ui)::value, ts = ts2 + u, t = t2 + u, L = t % 8 * 2;
+          const float2 d = d2[u];
+          const float g = g2[u], bv = v.b[0][t / 8], cv = v.c[0][t / 8];
+          const float H0 = fmaf(row_lane<L>(cv), g, K[0]), H1 = fmaf(row_lane<L + 1>(cv), g, K[1]);
+          const float vb = swap32_add(H0 * d.y, H1 * d.y), vc = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
+          part[Q & 1][0][w][ts][lane] = fmaf(row_lane<L + 1>(bv), H1, row_lane<L>(bv) * H0);
+          K[0] = H0 * a[t][0];
+          K[1] = H1 * a[t][1];
+          const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];
+          gAb[0] = fmaf(d.x, q0, gAb[0]);
+          gAb[1] = fmaf(d.x, q1, gAb[1]);
+          part[Q & 1][1][w][ts][lane] = fmaf(A[1], q1, A[0] * q0);
+          // tokens 2m + 1 and 2m, then pairs of them, then the four quarters of 16
+          r2[t & 1] = swap16_add(vb, vc);
+        });
+        r4[t2 >> 1 & 1] = half8_add(r2[0], r2[1]);
+        if constexpr ((t2 & 3) == 0) r8[t2 >> 2 & 3] = half4_add(r4[0], r4[1]);
+        if constexpr ((t2 & 15) == 0) vout[(size_t)(i * kBlock + t2) * 4] = quads_add(r8);
+        __builtin_amdgcn_sched_barrier(0);
       });
     };
     auto finish = [&](auto qi) {
