@@ -15,8 +15,6 @@ namespace ssm {
 
 using chan::ld;
 
-typedef float f4 __attribute__((ext_vector_type(4)));
-
 // ---------------------------------------------------------------- sums over lanes
 // 64 values of every lane in, lane_value(v)'s sum over the 64 lanes out, by halves: each
 // step adds two registers' halves into one that holds both sums.
@@ -52,9 +50,9 @@ __device__ inline float quads_add(const float (&r)[4]) {   // lane & 2: r[1], r[
 // ---------------------------------------------------------------- reverse segments
 // What a segment does to the adjoint: a_t (C_t g_t + ...) from its end (zero; grad_h at the
 // last segment's) to its start, and the sum of its time steps.
-template <typename T, int NW, int NS>
-__global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p, Geo q, float* ends, float* sums) {
-  constexpr int kTile = 16, J = kTile / NW;
+template <typename T, int NS>
+__global__ __launch_bounds__(kWaves * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p, Geo q, float* ends, float* sums) {
+  constexpr int NW = kWaves, kTile = 16, J = kTile / NW;
   __shared__ float2 in[2][kTile][kLanes];   // d, g
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place s = place_of(q);
@@ -74,8 +72,9 @@ __global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p
                z = rows_at<T>(p.z, q, s.b, t0, gate ? end : t0);
   const unsigned row_bytes = (unsigned)(q.C * sizeof(T)), col = s.on ? (unsigned)(s.c * sizeof(T)) : kNowhere;
   // One step of vectors (only C_t is used) and inputs ahead; tiles from the last to the first.
-  const Vectors<T, NS, kTile> vectors(p.Bv, p.Cv, q, s, t0, end, w * (NS / 2));
-  typename Vectors<T, NS, kTile>::Raw vr;
+  typedef Vectors<T, NS, kTile> V;
+  const V vectors(p.Bv, p.Cv, q, s, t0, end, w * NS);
+  typename V::Raw vr;
   typedef typename Io<T>::Raw Raw;
   Raw nd[J], ng[J], nz[J];
   auto load = [&](int i) {
@@ -96,7 +95,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p
   for (int i = n - 1; i >= 0; --i) {
     const int tt = t0 + i * kTile;
     float tile = 0.f;
-    typename Vectors<T, NS, kTile>::Set v;
+    typename V::Set v;
     vectors.take(vr, v);
     if (i > 0) vectors.load((i - 1) * kTile, vr);
     float2(*to)[kLanes] = in[i & 1];
@@ -116,13 +115,15 @@ __global__ __launch_bounds__(NW * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_args p
     if (i > 0) load(i - 1);
     __syncthreads();   // the tile before last is read no more
     each<kTile>([&](auto back) {
-      constexpr int t = kTile - 1 - decltype(back)::value, L = t % 8 * 2;
+      constexpr int t = kTile - 1 - decltype(back)::value, L = t % V::M * V::W;
       const float2 d = to[t][lane];
 #pragma unroll
-      for (int k = 0; k < NS; k += 2) {
-        const float cv = v.c[k / 2][t / 8];
-        K[k] = __builtin_amdgcn_exp2f(d.x * A2[k]) * fmaf(row_lane<L>(cv), d.y, K[k]);
-        K[k + 1] = __builtin_amdgcn_exp2f(d.x * A2[k + 1]) * fmaf(row_lane<L + 1>(cv), d.y, K[k + 1]);
+      for (int k = 0; k < V::P; ++k) {
+        const float cv = v.c[k][t / V::M];
+        float* Kk = K + V::W * k;
+        const float* Ak = A2 + V::W * k;
+        Kk[0] = __builtin_amdgcn_exp2f(d.x * Ak[0]) * fmaf(row_lane<L>(cv), d.y, Kk[0]);
+        if constexpr (V::W == 2) Kk[1] = __builtin_amdgcn_exp2f(d.x * Ak[1]) * fmaf(row_lane<L + 1>(cv), d.y, Kk[1]);
       }
     });
   }
@@ -152,25 +153,29 @@ __device__ inline float adjoint_behind(const gdr_ssm_bwd_args& p, const Geo& q, 
     K = fmaf(__builtin_amdgcn_exp2f(A2 * sums[((size_t)s.b * q.segs + k) * q.C + s.c]), K, ends[slot + k * nc]);
   return K;
 }
-// The lane's place among the 64 sums of 16 tokens: token and which of B0, B1, C0, C1.
-__device__ inline int sum_place() {
-  const int l = threadIdx.x & 63;
-  return ((l >> 3 & 1) | (l >> 2 & 1) << 1 | (l >> 1 & 1) << 2 | (l & 1) << 3) * 4 + (l >> 5 | (l >> 4 & 1) << 1);
+// The lane's place among the 64 sums of a wave: of 16 tokens and two states' B and C, or
+// of 32 tokens and one state's; from the first state's B of the first token on, in a plane
+// [Tp] each: [states][B, C][Tp].
+template <int NS>
+__device__ inline size_t sum_place(int Tp) {
+  const int l = threadIdx.x & 63, b5 = l >> 5, b4 = l >> 4 & 1, b3 = l >> 3 & 1, b2 = l >> 2 & 1, b1 = l >> 1 & 1, b0 = l & 1;
+  if (NS == 2) return (size_t)(b5 * 2 + b4) * Tp + (b3 | b2 << 1 | b1 << 2 | b0 << 3);
+  return (size_t)b5 * Tp + (b4 | b3 << 1 | b2 << 2 | b1 << 3 | b0 << 4);
 }
 // What a channel's token is prepared to.
 struct Token {
   float x, z, gy, slope;   // slope of softplus
 };
 
-// Up to 16 states: NW waves of two each.  A block's 32 states and decays stay in registers.
+// Up to 16 states: eight waves of one or two each.  A block's 32 states and decays stay in registers.
 // The adjoint passes through it in four quarters; while one is worked on, the one before
 // is finished (the waves' parts added, gradients written), and the next block's inputs are
 // on their way.
-template <typename T, int NW, bool GATE>
-__global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt, const float* ends,
+template <typename T, int NS, bool GATE>
+__global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt, const float* ends,
                                                           const float* sums, float* vpart, float* rows) {
-  constexpr int J = kBlock / NW, QT = 8, JQ = QT / NW > 0 ? QT / NW : 1;
-  static_assert(NW <= QT, "a token of a quarter for every wave");
+  constexpr int NW = kWaves, J = kBlock / NW, QT = 8;
+  static_assert(NW == QT && (NS == 1 || NS == 2), "a token of a quarter for every wave");
   __shared__ float2 in[kBlock][kLanes];                        // d, d x
   __shared__ float gs[kBlock][kLanes];                         // g
   __shared__ float part[2][2][NW][QT][kLanes];                 // each wave's share of p and sum A q, two quarters
@@ -179,12 +184,13 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
   const Place s = place_of(q);
   const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T), end = min(t1, len);
   const size_t nc = (size_t)q.N * q.C;
-  float A[2], A2[2], K[2], gA[2] = {0.f, 0.f};
-  const float* ck[2];   // the states' checkpoints
-  bool has[2];
+  float A[NS], A2[NS], K[NS], gA[NS];
+  const float* ck[NS];   // the states' checkpoints
+  bool has[NS];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = w * 2 + i;
+  for (int i = 0; i < NS; ++i) {
+    const int n = w * NS + i;
+    gA[i] = 0.f;
     has[i] = n < q.N && s.on;
     A[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] : 0.f;
     A2[i] = A[i] * scan::kLog2e;
@@ -198,14 +204,15 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
                gx = rows_at<T>(p.grad_x, q, s.b, t0, end), gdt = rows_at<T>(p.grad_dt, q, s.b, t0, end),
                gz = rows_at<T>(p.grad_z, q, s.b, t0, GATE ? end : t0);
   const unsigned row_bytes = (unsigned)(q.C * sizeof(T)), col = s.on ? (unsigned)(s.c * sizeof(T)) : kNowhere;
-  const Vectors<T, 2, kBlock> vectors(p.Bv, p.Cv, q, s, t0, end, w);
-  float* vout = vpart + ((((size_t)s.cb * q.B + s.b) * q.pairs + w) * q.Tp + t0) * 4 + sum_place();
+  typedef Vectors<T, NS, kBlock> V;
+  const V vectors(p.Bv, p.Cv, q, s, t0, end, w * NS);
+  float* vout = vpart + (((size_t)s.cb * q.B + s.b) * q.room + w * NS) * 2 * q.Tp + t0 + sum_place<NS>(q.Tp);
 
   // the next block's inputs as they come
   typedef typename Io<T>::Raw Raw;
   Raw nx[J], nd[J], ng[J], nz[J];
-  typename Vectors<T, 2, kBlock>::Raw vr;
-  float nh[2];
+  typename V::Raw vr;
+  float nh[NS];
   auto load = [&](int i) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -217,7 +224,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
     }
     vectors.load(i * kBlock, vr);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) nh[k] = has[k] ? ck[k][i * nc] : 0.f;
+    for (int k = 0; k < NS; ++k) nh[k] = has[k] ? ck[k][i * nc] : 0.f;
   };
   float gD = 0.f, gbias = 0.f;
   const int n = end > t0 ? (end - t0 + kBlock - 1) / kBlock : 0;   // blocks
@@ -243,10 +250,11 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
       in[t][lane] = float2{d, d * own[j].x};
       gs[t][lane] = g;
     }
-    typename Vectors<T, 2, kBlock>::Set v;
+    typename V::Set v;
     vectors.take(vr, v);
-    float h[kBlock + 1][2], a[kBlock][2];
-    h[0][0] = nh[0], h[0][1] = nh[1];
+    float h[kBlock + 1][NS], a[kBlock][NS];
+#pragma unroll
+    for (int k = 0; k < NS; ++k) h[0][k] = nh[k];
     __syncthreads();
     if (i > 0) load(i - 1);
     // LDS is read a group of tokens ahead; the groups stay apart, else loads of many of
@@ -262,19 +270,25 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
         for (int u = 0; u < 4; ++u) dn[u] = in[t4 + 4 + u][lane];
       }
       each<4>([&](auto ui) {
-        constexpr int u = decltype(ui)::value, t = t4 + u, L = t % 8 * 2;
+        constexpr int u = decltype(ui)::value, t = t4 + u, L = t % V::M * V::W;
         const float2 d = d4[u];
-        const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
-        a[t][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
-        a[t][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
+        const float bv = v.b[0][t / V::M], cv = v.c[0][t / V::M];
+#pragma unroll
+        for (int k = 0; k < NS; ++k) a[t][k] = __builtin_amdgcn_exp2f(d.x * A2[k]);
         h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
-        h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
-        if constexpr (GATE) upart[w][t][lane] = fmaf(row_lane<L + 1>(cv), h[t + 1][1], row_lane<L>(cv) * h[t + 1][0]);
+        float up = row_lane<L>(cv) * h[t + 1][0];
+        if constexpr (NS == 2) {
+          h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
+          up = fmaf(row_lane<L + 1>(cv), h[t + 1][1], up);
+        }
+        if constexpr (GATE) upart[w][t][lane] = up;
       });
       __builtin_amdgcn_sched_barrier(0);
     });
     vectors.forget(v);
-    float r2[2], r4[2], r8[4], gAb[2] = {0.f, 0.f};
+    float r2[2], r4[2], r8[2], r16[4], gAb[NS];
+#pragma unroll
+    for (int k = 0; k < NS; ++k) gAb[k] = 0.f;
     float2 rd[2];
     float rg[2];
 #pragma unroll
@@ -290,48 +304,61 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
           for (int u = 0; u < 2; ++u) rd[u] = in[t2 - 2 + u][lane], rg[u] = gs[t2 - 2 + u][lane];
         }
         each<2>([&](auto ui) {
-          constexpr int u = 1 - decltype(ui)::value, ts = ts2 + u, t = t2 + u, L = t % 8 * 2;
+          constexpr int u = 1 - decltype(ui)::value, ts = ts2 + u, t = t2 + u, L = t % V::M * V::W;
           const float2 d = d2[u];
-          const float g = g2[u], bv = v.b[0][t / 8], cv = v.c[0][t / 8];
-          const float H0 = fmaf(row_lane<L>(cv), g, K[0]), H1 = fmaf(row_lane<L + 1>(cv), g, K[1]);
-          const float vb = swap32_add(H0 * d.y, H1 * d.y), vc = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
-          part[Q & 1][0][w][ts][lane] = fmaf(row_lane<L + 1>(bv), H1, row_lane<L>(bv) * H0);
-          K[0] = H0 * a[t][0];
-          K[1] = H1 * a[t][1];
-          const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];
-          gAb[0] = fmaf(d.x, q0, gAb[0]);
-          gAb[1] = fmaf(d.x, q1, gAb[1]);
-          part[Q & 1][1][w][ts][lane] = fmaf(A[1], q1, A[0] * q0);
-          // tokens 2m + 1 and 2m, then pairs of them, then the four quarters of 16
-          r2[t & 1] = swap16_add(vb, vc);
+          const float g = g2[u], bv = v.b[0][t / V::M], cv = v.c[0][t / V::M];
+          float H[NS], pp, dd;
+          H[0] = fmaf(row_lane<L>(cv), g, K[0]);
+          pp = row_lane<L>(bv) * H[0];
+          if constexpr (NS == 2) {
+            H[1] = fmaf(row_lane<L + 1>(cv), g, K[1]);
+            pp = fmaf(row_lane<L + 1>(bv), H[1], pp);
+            r2[u] = swap16_add(swap32_add(H[0] * d.y, H[1] * d.y), swap32_add(g * h[t + 1][0], g * h[t + 1][1]));
+          } else {
+            r2[u] = swap32_add(H[0] * d.y, g * h[t + 1][0]);
+          }
+#pragma unroll
+          for (int k = 0; k < NS; ++k) {
+            K[k] = H[k] * a[t][k];
+            const float qk = K[k] * h[t][k];
+            gAb[k] = fmaf(d.x, qk, gAb[k]);
+            dd = k == 0 ? A[0] * qk : fmaf(A[k], qk, dd);
+          }
+          part[Q & 1][0][w][ts][lane] = pp;
+          part[Q & 1][1][w][ts][lane] = dd;
         });
-        r4[t2 >> 1 & 1] = half8_add(r2[0], r2[1]);
-        if constexpr ((t2 & 3) == 0) r8[t2 >> 2 & 3] = half4_add(r4[0], r4[1]);
-        if constexpr ((t2 & 15) == 0) vout[(size_t)(i * kBlock + t2) * 4] = quads_add(r8);
+        // the lanes' sums: tokens 2m and 2m + 1 share a register, then pairs of them, ...
+        if constexpr (NS == 2) {
+          r8[t2 >> 1 & 1] = half8_add(r2[0], r2[1]);
+          if constexpr ((t2 & 3) == 0) r16[t2 >> 2 & 3] = half4_add(r8[0], r8[1]);
+          if constexpr ((t2 & 15) == 0) vout[i * kBlock + t2] = quads_add(r16);
+        } else {
+          r4[t2 >> 1 & 1] = swap16_add(r2[0], r2[1]);
+          if constexpr ((t2 & 3) == 0) r8[t2 >> 2 & 1] = half8_add(r4[0], r4[1]);
+          if constexpr ((t2 & 7) == 0) r16[t2 >> 3 & 3] = half4_add(r8[0], r8[1]);
+          if constexpr ((t2 & 31) == 0) vout[i * kBlock + t2] = quads_add(r16);
+        }
         __builtin_amdgcn_sched_barrier(0);
       });
     };
     auto finish = [&](auto qi) {
       constexpr int Q = decltype(qi)::value;
+      const int t = Q * QT + w;
+      float pp = 0.f, dd = 0.f;
 #pragma unroll
-      for (int k = 0; k < JQ; ++k) {
-        const int j = Q * JQ + k, t = j * NW + w, ts = t - Q * QT;
-        float pp = 0.f, dd = 0.f;
+      for (int m = 0; m < NW; ++m) pp += part[Q & 1][0][m][w][lane], dd += part[Q & 1][1][m][w][lane];
+      const float d = in[t][lane].x, g = gs[t][lane], gd = fmaf(pp, own[Q].x, dd) * own[Q].slope;
+      const unsigned at = col + (unsigned)(i * kBlock + t) * row_bytes;
+      gbias += gd;
+      gD = fmaf(g, own[Q].x, gD);
+      Io<T>::store(gx, at, fmaf(pp, d, D * g));
+      Io<T>::store(gdt, at, gd);
+      if (GATE) {
+        float u = D * own[Q].x;
 #pragma unroll
-        for (int m = 0; m < NW; ++m) pp += part[Q & 1][0][m][ts][lane], dd += part[Q & 1][1][m][ts][lane];
-        const float d = in[t][lane].x, g = gs[t][lane], gd = fmaf(pp, own[j].x, dd) * own[j].slope;
-        const unsigned at = col + (unsigned)(i * kBlock + t) * row_bytes;
-        gbias += gd;
-        gD = fmaf(g, own[j].x, gD);
-        Io<T>::store(gx, at, fmaf(pp, d, D * g));
-        Io<T>::store(gdt, at, gd);
-        if (GATE) {
-          float u = D * own[j].x;
-#pragma unroll
-          for (int m = 0; m < NW; ++m) u += upart[GATE ? m : 0][GATE ? t : 0][lane];
-          const float sg = scan::sigmoid(own[j].z);
-          Io<T>::store(gz, at, own[j].gy * u * sg * fmaf(own[j].z, 1.f - sg, 1.f));
-        }
+        for (int m = 0; m < NW; ++m) u += upart[GATE ? m : 0][GATE ? t : 0][lane];
+        const float sg = scan::sigmoid(own[Q].z);
+        Io<T>::store(gz, at, own[Q].gy * u * sg * fmaf(own[Q].z, 1.f - sg, 1.f));
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -348,8 +375,8 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
     __syncthreads();
     // in, gs and own are this wave's own tokens' here, so the next block's may follow
     finish(std::integral_constant<int, 0>());
-    gA[0] += gAb[0];   // block by block: fewer additions behind a sum
-    gA[1] += gAb[1];
+#pragma unroll
+    for (int k = 0; k < NS; ++k) gA[k] += gAb[k];   // block by block: fewer additions behind a sum
   }
   // behind the row's end the gradients are 0
   if (s.on) {
@@ -363,8 +390,8 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
   // parameters' gradients: a row [N + 2][C] of this batch row and segment
   float* out = rows + ((size_t)s.b * q.segs + s.seg) * (q.N + 2) * q.C + s.c;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = w * 2 + i;
+  for (int i = 0; i < NS; ++i) {
+    const int n = w * NS + i;
     if (has[i]) {
       out[(size_t)n * q.C] = gA[i];
       if (p.grad_h0 && s.seg == 0) p.grad_h0[((size_t)s.b * q.C + s.c) * q.N + n] = K[i];
@@ -386,9 +413,9 @@ __global__ __launch_bounds__(NW * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Ge
 // wait in LDS.  Half a block is worked on at a time, the states of its second half from
 // the block's start.
 template <typename T, int NCH>
-__global__ __launch_bounds__(512) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt,
+__global__ __launch_bounds__(kWaves * 64) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt,
                                                           const float* ends, const float* sums, float* vpart, float* rows) {
-  constexpr int NW = 8, SUB = 16, J = SUB / NW;
+  constexpr int NW = kWaves, SUB = 16, J = SUB / NW;
   __shared__ float2 in[kBlock][kLanes];      // d, d x
   __shared__ float gs[kBlock][kLanes];       // g
   __shared__ float part[3][NW][SUB][kLanes]; // each wave's share of p, sum A q, sum C h
@@ -422,7 +449,7 @@ __global__ __launch_bounds__(512) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, G
   const size_t row0 = (size_t)s.b * q.T * q.C + s.c;
   const T *x = (const T*)p.x + row0, *dt = (const T*)p.dt + row0, *z = (const T*)p.z + row0, *gy = (const T*)p.grad_y + row0;
   T *gx = (T*)p.grad_x + row0, *gdt = (T*)p.grad_dt + row0, *gz = (T*)p.grad_z + row0;
-  const int mine = sum_place();
+  const size_t mine = sum_place<2>(q.Tp);
   float gD = 0.f, gbias = 0.f;
 
   for (int tt = t0 + (t1 - 1 - t0) / kBlock * kBlock; tt >= t0; tt -= kBlock) {
@@ -470,7 +497,7 @@ __global__ __launch_bounds__(512) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, G
 #pragma unroll
           for (int i = 0; i < 2; ++i) K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
         }
-        const Vectors<T, 2, SUB> vectors(p.Bv, p.Cv, q, s, t0, end, ch * NW + w);
+        const Vectors<T, 2, SUB> vectors(p.Bv, p.Cv, q, s, t0, end, 2 * (ch * NW + w));
         typename Vectors<T, 2, SUB>::Raw vr;
         typename Vectors<T, 2, SUB>::Set v;
         float h[SUB + 1][2], a[SUB][2];
@@ -506,6 +533,7 @@ __global__ __launch_bounds__(512) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, G
             *at = ch == 0 ? u : *at + u;
           }
         });
+        vectors.forget(v);
         float r2[2], r4[2], r8[4];
         each<SUB>([&](auto back) {
           constexpr int t = SUB - 1 - decltype(back)::value, L = t % 8 * 2;
@@ -529,8 +557,7 @@ __global__ __launch_bounds__(512) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, G
           if constexpr ((t & 1) == 0) r4[t >> 1 & 1] = half8_add(r2[0], r2[1]);
           if constexpr ((t & 3) == 0) r8[t >> 2] = half4_add(r4[0], r4[1]);
         });
-        vpart[((((size_t)s.cb * q.B + s.b) * q.pairs + ch * NW + w) * q.Tp + tt + st) * 4 + mine] =
-            quads_add(r8);
+        vpart[(((size_t)s.cb * q.B + s.b) * q.room + 2 * (ch * NW + w)) * 2 * q.Tp + tt + st + mine] = quads_add(r8);
         {
 #pragma unroll
           for (int i = 0; i < 2; ++i) later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = gA[i];
@@ -594,27 +621,21 @@ __global__ __launch_bounds__(512) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, G
 
 // The vectors' gradients: over the workgroups of a group's channels.
 template <typename T>
-__global__ __launch_bounds__(256) void ssm_vector_join_kernel(const f4* part, Geo q, const int32_t* lens, T* gB, T* gC) {
-  const size_t total = (size_t)q.B * q.G * q.pairs * q.Tp, step = (size_t)q.B * q.pairs * q.Tp;
+__global__ __launch_bounds__(256) void ssm_vector_join_kernel(const float* part, Geo q, const int32_t* lens, T* gB, T* gC) {
+  const size_t total = (size_t)q.B * q.G * q.N * q.Tp, step = (size_t)q.B * q.room * 2 * q.Tp;
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
-    const size_t row = i / q.Tp, gb = row / q.pairs, g = gb / q.B, b = gb - g * q.B;
-    const int t = (int)(i - row * q.Tp), pair = (int)(row - gb * q.pairs), n = pair * 2;
-    if (t >= q.T || n >= q.N) continue;
-    f4 a = {0.f, 0.f, 0.f, 0.f};
+    const size_t row = i / q.Tp, gb = row / q.N, g = gb / q.B, b = gb - g * q.B;
+    const int t = (int)(i - row * q.Tp), n = (int)(row - gb * q.N);
+    if (t >= q.T) continue;
+    float sb = 0.f, sc = 0.f;
     if (t < row_len(lens, (int)b, q.T)) {
-      const f4* at = part + ((g * q.nb * q.B + b) * q.pairs + pair) * q.Tp + t;
-      for (int k = 0; k < q.nb; ++k) {
-        const f4 r = at[k * step];
-        a.x += r.x, a.y += r.y, a.z += r.z, a.w += r.w;
-      }
+      const float* at = part + ((g * q.nb * q.B + b) * q.room + n) * 2 * q.Tp + t;
+#pragma unroll 4
+      for (int k = 0; k < q.nb; ++k) sb += at[k * step], sc += at[k * step + q.Tp];
     }
     const size_t o = ((b * q.T + t) * q.G + g) * q.N + n;
-    chan::st(gB + o, a.x);
-    chan::st(gC + o, a.z);
-    if (n + 1 < q.N) {
-      chan::st(gB + o + 1, a.y);
-      chan::st(gC + o + 1, a.w);
-    }
+    chan::st(gB + o, sb);
+    chan::st(gC + o, sc);
   }
 }
 
@@ -633,23 +654,25 @@ struct ParamGrads {
 struct Parts {
   size_t ends, sums, vpart, rows, ckpt, bytes;
 };
-static Parts parts_of(const Geo& q, bool ckpt) {
+static Parts parts_of(const Geo& q, const Geo& f, bool ckpt) {   // f: of the forward that computes the states again
   Parts w;
   w.ends = 0;
-  w.sums = w.ends + ends_bytes(q);
-  w.vpart = w.sums + sums_bytes(q);
-  w.rows = w.vpart + pad256((size_t)q.G * q.nb * q.B * q.pairs * q.Tp * 16);
+  w.sums = ckpt || ends_bytes(q) > ends_bytes(f) ? ends_bytes(q) : ends_bytes(f);
+  w.vpart = w.sums + (ckpt || sums_bytes(q) > sums_bytes(f) ? sums_bytes(q) : sums_bytes(f));
+  w.rows = w.vpart + pad256((size_t)q.G * q.nb * q.B * q.room * 2 * q.Tp * 4);
   w.ckpt = w.rows + pad256((size_t)q.B * q.segs * (q.N + 2) * q.C * 4);
   w.bytes = w.ckpt + (ckpt ? 0 : pad256((size_t)q.B * (q.Tp / kBlock) * q.N * q.C * 4));
   return w;
 }
 
-size_t bwd_workspace(int B, int T, int C, int N, int G, bool ckpt) { return parts_of(geo_of(B, T, C, N, G), ckpt).bytes; }
+size_t bwd_workspace(int B, int T, int C, int N, int G, bool ckpt) {
+  return parts_of(geo_of(B, T, C, N, G, true), geo_of(B, T, C, N, G, false), ckpt).bytes;
+}
 
 template <typename T>
 static hipError_t bwd(const gdr_ssm_bwd_args& a, hipStream_t s) {
-  const Geo q = geo_of(a.B, a.T, a.C, a.N, a.G);
-  const Parts w = parts_of(q, a.ckpt != nullptr);
+  const Geo q = geo_of(a.B, a.T, a.C, a.N, a.G, true), fq = geo_of(a.B, a.T, a.C, a.N, a.G, false);
+  const Parts w = parts_of(q, fq, a.ckpt != nullptr);
   char* ws = (char*)a.workspace;
   float *ends = (float*)(ws + w.ends), *sums = (float*)(ws + w.sums), *vpart = (float*)(ws + w.vpart),
         *rows = (float*)(ws + w.rows);
@@ -661,29 +684,29 @@ static hipError_t bwd(const gdr_ssm_bwd_args& a, hipStream_t s) {
     f.ckpt = (float*)(ws + w.ckpt);
     ckpt = f.ckpt;
     f.Bv = a.Bv, f.Cv = a.Cv;
-    const hipError_t e = launch_states(f, q, ends, sums, s);
+    const hipError_t e = launch_states(f, fq, ends, sums, s);
     if (e != hipSuccess) return e;
   }
   if (q.segs > 1) {
-    const dim3 grid(q.blocks() / q.segs * (q.segs - 1));
-    if (q.N <= 8) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 4, 2>), grid, dim3(256), 0, s, a, q, ends, sums);
-    else if (q.N <= 16) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 2>), grid, dim3(512), 0, s, a, q, ends, sums);
-    else if (q.N <= 32) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 4>), grid, dim3(512), 0, s, a, q, ends, sums);
-    else hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8, 8>), grid, dim3(512), 0, s, a, q, ends, sums);
+    const dim3 some(q.blocks() / q.segs * (q.segs - 1)), block(kWaves * 64);
+    if (q.N <= 8) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 1>), some, block, 0, s, a, q, ends, sums);
+    else if (q.N <= 16) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 2>), some, block, 0, s, a, q, ends, sums);
+    else if (q.N <= 32) hipLaunchKernelGGL((ssm_adjoint_kernel<T, 4>), some, block, 0, s, a, q, ends, sums);
+    else hipLaunchKernelGGL((ssm_adjoint_kernel<T, 8>), some, block, 0, s, a, q, ends, sums);
   }
   const dim3 grid(q.blocks());
-#define SSM_BWD(KERNEL, THREADS) \
-  hipLaunchKernelGGL((KERNEL), grid, dim3(THREADS), 0, s, a, q, ckpt, ends, sums, vpart, rows)
-  if (q.N <= 8 && a.z) SSM_BWD((ssm_bwd_kernel<T, 4, true>), 256);
-  else if (q.N <= 8) SSM_BWD((ssm_bwd_kernel<T, 4, false>), 256);
-  else if (q.N <= 16 && a.z) SSM_BWD((ssm_bwd_kernel<T, 8, true>), 512);
-  else if (q.N <= 16) SSM_BWD((ssm_bwd_kernel<T, 8, false>), 512);
-  else if (q.N <= 32) SSM_BWD((ssm_bwd_wide_kernel<T, 2>), 512);
-  else SSM_BWD((ssm_bwd_wide_kernel<T, 4>), 512);
+#define SSM_BWD(...) \
+  hipLaunchKernelGGL((__VA_ARGS__), grid, dim3(kWaves * 64), 0, s, a, q, ckpt, ends, sums, vpart, rows)
+  if (q.N <= 8 && a.z) SSM_BWD(ssm_bwd_kernel<T, 1, true>);
+  else if (q.N <= 8) SSM_BWD(ssm_bwd_kernel<T, 1, false>);
+  else if (q.N <= 16 && a.z) SSM_BWD(ssm_bwd_kernel<T, 2, true>);
+  else if (q.N <= 16) SSM_BWD(ssm_bwd_kernel<T, 2, false>);
+  else if (q.N <= 32) SSM_BWD(ssm_bwd_wide_kernel<T, 2>);
+  else SSM_BWD(ssm_bwd_wide_kernel<T, 4>);
 #undef SSM_BWD
-  const size_t blocks = ((size_t)q.B * q.G * q.pairs * q.Tp + 255) / 256;
+  const size_t blocks = ((size_t)q.B * q.G * q.N * q.Tp + 255) / 256;
   hipLaunchKernelGGL(ssm_vector_join_kernel<T>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s,
-                     (const f4*)vpart, q, a.lens, (T*)a.grad_Bv, (T*)a.grad_Cv);
+                     vpart, q, a.lens, (T*)a.grad_Bv, (T*)a.grad_Cv);
   launch_col_join(rows, (size_t)q.B * q.segs, (size_t)(q.N + 2) * q.C, ParamGrads{q.C, q.N, a.grad_A, a.grad_D, a.grad_dt_bias}, s);
   return hipGetLastError();
 }

@@ -20,9 +20,9 @@ constexpr int kTile = 16;
 // ---------------------------------------------------------------- forward
 // MODE 0: y and everything else; 1: states alone (ckpt, h_out); 2: what a segment does to
 // the state: its end from zero (the first one's from h0) and the sum of its time steps.
-template <typename T, int NW, int NS, int MODE>
-__global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q, float* ends, float* sums) {
-  constexpr int J = kTile / NW;   // tokens of a tile that a wave prepares and finishes
+template <typename T, int NS, int MODE>
+__global__ __launch_bounds__(kWaves * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q, float* ends, float* sums) {
+  constexpr int NW = kWaves, J = kTile / NW;   // tokens of a tile that a wave prepares and finishes
   __shared__ float2 in[2][kTile][kLanes];
   __shared__ float part[MODE == 0 ? 2 : 1][MODE == 0 ? NW : 1][kTile][kLanes];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -104,9 +104,10 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
 #pragma unroll
     for (int j = 0; j < J; ++j) Io<T>::store(y, col + (unsigned)(i * kTile + j * NW + w) * row_bytes, u[j]);
   };
-  const Vectors<T, NS, kTile> vectors(p.Bv, p.Cv, q, s, t0, end, w * (NS / 2));
-  typename Vectors<T, NS, kTile>::Raw vr[2];
-  auto run = [&](const typename Vectors<T, NS, kTile>::Set& v, const float2(*from)[kLanes], float(*to)[kTile][kLanes]) {
+  typedef Vectors<T, NS, kTile> V;
+  const V vectors(p.Bv, p.Cv, q, s, t0, end, w * NS);
+  typename V::Raw vr[2];
+  auto run = [&](const typename V::Set& v, const float2(*from)[kLanes], float(*to)[kTile][kLanes]) {
     // four tokens at a time: what does not wait for the state before, then what does
     float2 d[4], dn[4];
 #pragma unroll
@@ -119,28 +120,28 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
       }
       float a[4][NS], b[4][NS];
       each<4>([&](auto uu) {
-        constexpr int u = decltype(uu)::value, L = (t + u) % 8 * 2;
+        constexpr int u = decltype(uu)::value, L = (t + u) % V::M * V::W;
 #pragma unroll
-        for (int i = 0; i < NS; i += 2) {
-          const float bv = v.b[i / 2][t / 8];
-          a[u][i] = __builtin_amdgcn_exp2f(d[u].x * A2[i]);
-          a[u][i + 1] = __builtin_amdgcn_exp2f(d[u].x * A2[i + 1]);
-          b[u][i] = d[u].y * row_lane<L>(bv);
-          b[u][i + 1] = d[u].y * row_lane<L + 1>(bv);
+        for (int i = 0; i < NS; ++i) a[u][i] = __builtin_amdgcn_exp2f(d[u].x * A2[i]);
+#pragma unroll
+        for (int i = 0; i < V::P; ++i) {
+          const float bv = v.b[i][(t + u) / V::M];
+          b[u][V::W * i] = d[u].y * row_lane<L>(bv);
+          if constexpr (V::W == 2) b[u][2 * i + 1] = d[u].y * row_lane<L + 1>(bv);
         }
       });
       __builtin_amdgcn_sched_barrier(0);
       each<4>([&](auto uu) {
-        constexpr int u = decltype(uu)::value, L = (t + u) % 8 * 2;
+        constexpr int u = decltype(uu)::value, L = (t + u) % V::M * V::W;
         float acc = 0.f;
 #pragma unroll
-        for (int i = 0; i < NS; i += 2) {
-          const float cv = v.c[i / 2][t / 8];
-          h[i] = fmaf(a[u][i], h[i], b[u][i]);
-          h[i + 1] = fmaf(a[u][i + 1], h[i + 1], b[u][i + 1]);
-          if (MODE == 0) {
-            acc = i == 0 ? row_lane<L>(cv) * h[0] : fmaf(row_lane<L>(cv), h[i], acc);
-            acc = fmaf(row_lane<L + 1>(cv), h[i + 1], acc);
+        for (int i = 0; i < NS; ++i) h[i] = fmaf(a[u][i], h[i], b[u][i]);
+        if (MODE == 0) {
+#pragma unroll
+          for (int i = 0; i < V::P; ++i) {
+            const float cv = v.c[i][(t + u) / V::M];
+            acc = i == 0 ? row_lane<L>(cv) * h[0] : fmaf(row_lane<L>(cv), h[V::W * i], acc);
+            if constexpr (V::W == 2) acc = fmaf(row_lane<L + 1>(cv), h[2 * i + 1], acc);
           }
         }
         if (MODE == 0) to[w][t + u][lane] = acc;
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
   auto turn = [&](auto parity, int i) {
     constexpr int P = decltype(parity)::value;
     const int tt = t0 + i * kTile;
-    typename Vectors<T, NS, kTile>::Set v;
+    typename V::Set v;
     vectors.take(vr[P], v);
     vectors.load((i + 2) * kTile, vr[P]);
     if (MODE == 0 && i > 0) finish(i - 1, cx[P ^ 1], cz[P ^ 1], part[MODE == 0 ? P ^ 1 : 0]);
@@ -213,10 +214,11 @@ __global__ __launch_bounds__(NW * 64) void ssm_fwd_kernel(gdr_ssm_args p, Geo q,
 template <typename T, int MODE>
 static void launch_fwd(const gdr_ssm_args& a, const Geo& q, float* ends, float* sums, hipStream_t s) {
   const dim3 grid(MODE == 2 ? q.blocks() / q.segs * (q.segs - 1) : q.blocks());   // segments come last
-  if (q.N <= 8) hipLaunchKernelGGL((ssm_fwd_kernel<T, 4, 2, MODE>), grid, dim3(256), 0, s, a, q, ends, sums);
-  else if (q.N <= 16) hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 2, MODE>), grid, dim3(512), 0, s, a, q, ends, sums);
-  else if (q.N <= 32) hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 4, MODE>), grid, dim3(512), 0, s, a, q, ends, sums);
-  else hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, 8, MODE>), grid, dim3(512), 0, s, a, q, ends, sums);
+  const dim3 block(kWaves * 64);
+  if (q.N <= 8) hipLaunchKernelGGL((ssm_fwd_kernel<T, 1, MODE>), grid, block, 0, s, a, q, ends, sums);
+  else if (q.N <= 16) hipLaunchKernelGGL((ssm_fwd_kernel<T, 2, MODE>), grid, block, 0, s, a, q, ends, sums);
+  else if (q.N <= 32) hipLaunchKernelGGL((ssm_fwd_kernel<T, 4, MODE>), grid, block, 0, s, a, q, ends, sums);
+  else hipLaunchKernelGGL((ssm_fwd_kernel<T, 8, MODE>), grid, block, 0, s, a, q, ends, sums);
 }
 
 hipError_t launch_states(const gdr_ssm_args& a, const Geo& q, float* ends, float* sums, hipStream_t s) {
@@ -236,12 +238,12 @@ hipError_t launch_states(const gdr_ssm_args& a, const Geo& q, float* ends, float
 }
 
 size_t fwd_workspace(int B, int T, int C, int N, int G) {
-  const Geo q = geo_of(B, T, C, N, G);
+  const Geo q = geo_of(B, T, C, N, G, false);
   return ends_bytes(q) + sums_bytes(q);
 }
 
 hipError_t launch_ssm_fwd(const gdr_ssm_args& a, hipStream_t s) {
-  const Geo q = geo_of(a.B, a.T, a.C, a.N, a.G);
+  const Geo q = geo_of(a.B, a.T, a.C, a.N, a.G, false);
   float* ends = (float*)a.workspace;
   return launch_states(a, q, ends, (float*)((char*)a.workspace + ends_bytes(q)), s);
 }

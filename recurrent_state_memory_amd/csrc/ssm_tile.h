@@ -26,29 +26,38 @@ constexpr int kBlock = GDR_SSM_BLOCK;
 struct Geo {
   int B, T, C, N, G;
   int each, nb;     // channels of a group, workgroups of them
-  int pairs;        // pairs of states that the waves have room for
+  int room;         // states that the waves have room for
   int Tp;           // T up to a whole block
   int segs, seg;    // segments of the tokens and their length, a multiple of kBlock
   __host__ __device__ unsigned blocks() const { return (unsigned)B * G * nb * segs; }
 };
 
-// Waves and states a wave (NS); waves beyond 8 or more than 8 states a wave serve no N.
-constexpr int waves_of(int N) { return N <= 8 ? 4 : 8; }
-constexpr int states_of(int N) { return N <= 16 ? 2 : N <= 32 ? 4 : 8; }
+constexpr int kWaves = 8;   // of a workgroup
 
-inline Geo geo_of(int B, int T, int C, int N, int G) {
+// The forward's and the backward's.
+inline Geo geo_of(int B, int T, int C, int N, int G, bool backward) {
   Geo q;
   q.B = B, q.T = T, q.C = C, q.N = N, q.G = G;
   q.each = C / G;
   q.nb = lanes_of_group(C, G);
-  q.pairs = waves_of(N) * states_of(N) / 2;
+  q.room = N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64;
   q.Tp = (int)blocks_of(T) * kBlock;
-  // Segments: where the chains of channels are fewer than half the CUs, up to two
-  // workgroups a CU, of 64 tokens at least.
+  // Segments.  Forward: where the chains of channels are no more than half the CUs, two
+  // workgroups a CU of 64 tokens at least (a second one a CU fills the first one's waits).
+  // Backward: one fits a CU, so the number of segments that leaves the fewest rounds of
+  // whole rows, with a fifth of the time of a round for the adjoint's first pass over all
+  // rows but the last segments'.
   const long long chains = chains_of(B, C, G);
-  long long want = chains <= 128 && T >= 256 ? 512 / chains : 1;
-  if (want > T / 64) want = T / 64;
-  if (want < 1) want = 1;
+  long long want = 1;
+  if (!backward) {
+    if (chains <= 128 && T >= 256) want = 512 / chains < T / 64 ? 512 / chains : T / 64;
+  } else {
+    double best = 0;
+    for (int n = 1; n <= 256 && n * kBlock <= T; n = n < 16 ? n + 1 : n * 2) {
+      const double cost = ((chains * n + 255) / 256 + 0.2 * ((double)chains / 256) * (n - 1)) / n;
+      if (n == 1 || cost < 0.97 * best) best = cost, want = n;
+    }
+  }
   // and a segment's rows, and some behind it, stay within a buffer descriptor's 2^31 bytes
   const long long wide = (long long)(C > G * N ? C : G * N) * 4, most = ((1LL << 31) / wide - 128) / kBlock;
   const long long least = ((long long)blocks_of(T) + most - 1) / most;
@@ -127,10 +136,10 @@ __device__ inline Buffer rows_at(const void* base, const Geo& q, int b, int t, i
   return buffer_at((const T*)base + ((size_t)b * q.T + t) * q.C, t < end ? (size_t)(end - t) * q.C * sizeof(T) : 0);
 }
 
-// B_t and C_t of a wave's states, two registers for eight tokens and a pair of states: each
-// row of 16 lanes holds B's (C's) of both states for the eight, lane 2 (t % 8) + i, and the
-// arithmetic takes them from there by DPP (row_newbcast), mostly at no instruction of its
-// own.  (From scalar registers: every scalar load misses its cache, as 64 bytes are four
+// B_t and C_t of a wave's states, two registers for eight tokens and a pair of states (or
+// sixteen tokens and the wave's only state): each row of 16 lanes holds B's (C's) of both
+// states for the eight, lane 2 (t % 8) + i, and the arithmetic takes them from there by DPP
+// (row_newbcast), mostly at no instruction of its own.  (From scalar registers: every scalar load misses its cache, as 64 bytes are four
 // tokens, and returns out of order, so that each wait is for the last one.)
 template <int K>
 __device__ inline float row_lane(float v) {
@@ -138,7 +147,7 @@ __device__ inline float row_lane(float v) {
 }
 template <typename T, int NS, int TILE>
 struct Vectors {
-  static constexpr int P = NS / 2, Q = TILE / 8;
+  static constexpr int W = NS > 1 ? 2 : 1, P = NS / W, M = 16 / W, Q = TILE / M;   // M tokens a register
   struct Raw {
     typename Io<T>::Raw b[P][Q], c[P][Q];
   };
@@ -147,8 +156,8 @@ struct Vectors {
   };
   Buffer Bv, Cv;      // of tokens t0 to end - 1; the last one's row ends with its group's vector
   unsigned step;      // bytes between tokens
-  unsigned at[P];     // the lane's offset behind a multiple of eight tokens
-  // of pairs first, first + 1, ... (state 2 first + 2 i)
+  unsigned at[P];     // the lane's offset behind a multiple of M tokens
+  // of states first ... first + NS - 1
   __device__ inline Vectors(const void* b, const void* c, const Geo& q, const Place& s, int t0, int end, int first) {
     const size_t row = (size_t)q.G * q.N, base = (((size_t)s.b * q.T + t0) * q.G + s.g) * q.N;
     const size_t bytes = t0 < end ? ((size_t)(end - 1 - t0) * row + q.N) * sizeof(T) : 0;
@@ -158,8 +167,8 @@ struct Vectors {
     const int j = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int n = 2 * (first + i) + (j & 1);
-      at[i] = n < q.N ? (j >> 1) * step + n * (unsigned)sizeof(T) : kNowhere;
+      const int n = first + W * i + j % W;
+      at[i] = n < q.N ? j / W * step + n * (unsigned)sizeof(T) : kNowhere;
     }
   }
   // Tokens t ... t + TILE - 1 (counted from t0), zeros behind the last one and where there
@@ -169,7 +178,7 @@ struct Vectors {
     for (int i = 0; i < P; ++i)
 #pragma unroll
       for (int k = 0; k < Q; ++k) {
-        const unsigned o = at[i] + (unsigned)(t + 8 * k) * step;
+        const unsigned o = at[i] + (unsigned)(t + M * k) * step;
         r.b[i][k] = Io<T>::load(Bv, o);
         r.c[i][k] = Io<T>::load(Cv, o);
       }
