@@ -142,16 +142,23 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_ar
 }
 
 // ---------------------------------------------------------------- backward
-// What both kernels below start with: the state's adjoint behind a segment.
-__device__ inline float adjoint_behind(const gdr_ssm_bwd_args& p, const Geo& q, const Place& s, int n, float A2,
-                                       const float* ends, const float* sums) {
-  if (n >= q.N || !s.on) return 0.f;
-  if (s.seg == q.segs - 1) return p.grad_h ? p.grad_h[((size_t)s.b * q.C + s.c) * q.N + n] : 0.f;
-  const size_t nc = (size_t)q.N * q.C, slot = (size_t)s.b * q.segs * nc + (size_t)n * q.C + s.c;
-  float K = ends[slot + (size_t)(q.segs - 1) * nc];
-  for (int k = q.segs - 2; k > s.seg; --k)
-    K = fmaf(__builtin_amdgcn_exp2f(A2 * sums[((size_t)s.b * q.segs + k) * q.C + s.c]), K, ends[slot + k * nc]);
-  return K;
+// What both kernels below start with: the adjoints of states first ... behind a segment.
+template <int NS>
+__device__ inline void adjoint_behind(const gdr_ssm_bwd_args& p, const Geo& q, const Place& s, int first,
+                                      const float (&A2)[NS], const float* ends, const float* sums, float (&K)[NS]) {
+  const bool last = s.seg == q.segs - 1;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int n = first + i;
+    K[i] = 0.f;
+    if (n >= q.N) continue;
+    if (!last) K[i] = ends[(((size_t)s.b * q.segs + q.segs - 1) * q.N + n) * q.C + s.c];
+    else if (p.grad_h) K[i] = p.grad_h[((size_t)s.b * q.C + s.c) * q.N + n];
+  }
+  if (!last) pass_segments<NS>(q, s, first, q.segs - 2, s.seg, -1, A2, ends, sums, K);
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    if (!s.on) K[i] = 0.f;   // lanes without a channel add nothing to the sums
 }
 // The lane's place among the 64 sums of a wave: of 16 tokens and two states' B and C, or
 // of 32 tokens and one state's; from the first state's B of the first token on, in a plane
@@ -194,9 +201,9 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
     has[i] = n < q.N && s.on;
     A[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] : 0.f;
     A2[i] = A[i] * scan::kLog2e;
-    K[i] = adjoint_behind(p, q, s, n, A2[i], ends, sums);
     ck[i] = ckpt + ((size_t)s.b * (q.Tp / kBlock) + t0 / kBlock) * nc + (size_t)(n < q.N ? n : 0) * q.C + s.c;
   }
+  adjoint_behind<NS>(p, q, s, w * NS, A2, ends, sums, K);
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
   const bool softplus = p.softplus != 0;
   const Buffer x = rows_at<T>(p.x, q, s.b, t0, end), dt = rows_at<T>(p.dt, q, s.b, t0, end),
@@ -437,10 +444,9 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_wide_kernel(gdr_ssm_bwd_a
 #pragma unroll
   for (int ch = 0; ch < NCH; ++ch) {
     load_turn(ch);
+    adjoint_behind<2>(p, q, s, (ch * NW + w) * 2, A2, ends, sums, K);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int n = (ch * NW + w) * 2 + i;
-      K[i] = adjoint_behind(p, q, s, n, A2[i], ends, sums);
       later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = 0.f;
     }
   }

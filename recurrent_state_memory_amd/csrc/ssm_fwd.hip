@@ -42,13 +42,11 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_fwd_kernel(gdr_ssm_args p, Ge
         if (p.h0) h[i] = p.h0[((size_t)s.b * q.C + s.c) * q.N + n];
         if (MODE == 2 && s.on) ends[slot + (size_t)(q.segs - 1) * nc] = h[i];   // the last one's end is not needed
       } else if (MODE != 2) {
-        if (s.seg == 0) h[i] = ends[slot + (size_t)(q.segs - 1) * nc];
-        else h[i] = ends[slot];
-        for (int k = 1; k < s.seg; ++k)
-          h[i] = fmaf(__builtin_amdgcn_exp2f(A2[i] * sums[((size_t)s.b * q.segs + k) * q.C + s.c]), h[i], ends[slot + k * nc]);
+        h[i] = ends[s.seg == 0 ? slot + (size_t)(q.segs - 1) * nc : slot];
       }
     }
   }
+  if (MODE != 2 && s.seg > 1) pass_segments<NS>(q, s, w * NS, 1, s.seg, 1, A2, ends, sums, h);
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
   const bool softplus = p.softplus != 0, gate = p.z != nullptr;
   const Buffer x = rows_at<T>(p.x, q, s.b, t0, end), dt = rows_at<T>(p.dt, q, s.b, t0, end),

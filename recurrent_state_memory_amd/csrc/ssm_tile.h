@@ -51,9 +51,10 @@ inline Geo geo_of(int B, int T, int C, int N, int G, bool backward) {
   long long want = 1;
   if (!backward) {
     if (chains <= 128 && T >= 256) want = 512 / chains < T / 64 ? 512 / chains : T / 64;
+    if (want > 128) want = 128;
   } else {
     double best = 0;
-    for (int n = 1; n <= 256 && n * kBlock <= T; n = n < 16 ? n + 1 : n * 2) {
+    for (int n = 1; n <= 128 && n * kBlock <= T; n = n < 16 ? n + 1 : n * 2) {
       const double cost = ((chains * n + 255) / 256 + 0.2 * ((double)chains / 256) * (n - 1)) / n;
       if (n == 1 || cost < 0.97 * best) best = cost, want = n;
     }
@@ -201,6 +202,34 @@ struct Vectors {
 
 // d = softplus(pre) or pre.
 __device__ inline float time_step(float pre, bool softplus) { return softplus ? scan::softplus(pre) : pre; }
+
+// A state (an adjoint) taken through the segments from, from + dir, ... (to excluded): of
+// each one its end and the sum of its time steps.  Several are asked for at once, else
+// each would cost a load's latency.
+template <int NS>
+__device__ inline void pass_segments(const Geo& q, const Place& s, int first, int from, int to, int dir,
+                                     const float (&A2)[NS], const float* ends, const float* sums, float (&h)[NS]) {
+  constexpr int KB = NS <= 2 ? 8 : 2;
+  for (int k0 = from; k0 != to;) {
+    float e[KB][NS], d[KB];
+    const int left = (to - k0) * dir, n = left < KB ? left : KB;
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      const size_t at = (size_t)s.b * q.segs + (k0 + (j < n ? j : 0) * dir);
+      d[j] = sums[at * q.C + s.c];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) e[j][i] = first + i < q.N ? ends[(at * q.N + first + i) * q.C + s.c] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      if (j < n) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(A2[i] * d[j]), h[i], e[j][i]);
+      }
+    }
+    k0 += n * dir;
+  }
+}
 
 // Bytes of the parts of a workspace, each a multiple of 256.
 inline size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
