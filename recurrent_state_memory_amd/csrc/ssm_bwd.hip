@@ -279,17 +279,20 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
       each<4>([&](auto ui) {
         constexpr int u = decltype(ui)::value, t = t4 + u, L = t % V::M * V::W;
         const float2 d = d4[u];
-        const float bv = v.b[0][t / V::M], cv = v.c[0][t / V::M];
+        const float bv = v.b[0][t / V::M];
 #pragma unroll
         for (int k = 0; k < NS; ++k) a[t][k] = __builtin_amdgcn_exp2f(d.x * A2[k]);
         h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
-        float up = row_lane<L>(cv) * h[t + 1][0];
-        if constexpr (NS == 2) {
-          h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
-          up = fmaf(row_lane<L + 1>(cv), h[t + 1][1], up);
-        }
-        if constexpr (GATE) upart[w][t][lane] = up;
+        if constexpr (NS == 2) h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
+        if constexpr (GATE && NS == 1) upart[w][t][lane] = row_lane<L>(v.c[0][t / V::M]) * h[t + 1][0];
       });
+      if constexpr (GATE && NS == 2) {
+        float u[4];
+        row_dots<t4 % V::M * 2, false>(v.c[0][t4 / V::M], h[t4 + 1][0], h[t4 + 2][0], h[t4 + 3][0], h[t4 + 4][0], h[t4 + 1][1],
+                                       h[t4 + 2][1], h[t4 + 3][1], h[t4 + 4][1], u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) upart[w][t4 + k][lane] = u[k];
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
     vectors.forget(v);
@@ -315,13 +318,13 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
           const float2 d = d2[u];
           const float g = g2[u], bv = v.b[0][t / V::M], cv = v.c[0][t / V::M];
           float H[NS], pp, dd;
-          H[0] = fmaf(row_lane<L>(cv), g, K[0]);
-          pp = row_lane<L>(bv) * H[0];
           if constexpr (NS == 2) {
-            H[1] = fmaf(row_lane<L + 1>(cv), g, K[1]);
-            pp = fmaf(row_lane<L + 1>(bv), H[1], pp);
+            H[0] = K[0], H[1] = K[1];
+            pp = row_adjoint<L>(cv, bv, g, H[0], H[1]);
             r2[u] = swap16_add(swap32_add(H[0] * d.y, H[1] * d.y), swap32_add(g * h[t + 1][0], g * h[t + 1][1]));
           } else {
+            H[0] = fmaf(row_lane<L>(cv), g, K[0]);
+            pp = row_lane<L>(bv) * H[0];
             r2[u] = swap32_add(H[0] * d.y, g * h[t + 1][0]);
           }
 #pragma unroll

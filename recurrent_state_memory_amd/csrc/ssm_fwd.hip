@@ -129,22 +129,30 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_fwd_kernel(gdr_ssm_args p, Ge
         }
       });
       __builtin_amdgcn_sched_barrier(0);
-      each<4>([&](auto uu) {
-        constexpr int u = decltype(uu)::value, L = (t + u) % V::M * V::W;
-        float acc = 0.f;
+      float hh[4][NS], acc[4];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) h[i] = fmaf(a[u][i], h[i], b[u][i]);
-        if (MODE == 0) {
+      for (int u = 0; u < 4; ++u) {
 #pragma unroll
-          for (int i = 0; i < V::P; ++i) {
-            const float cv = v.c[i][(t + u) / V::M];
-            acc = i == 0 ? row_lane<L>(cv) * h[0] : fmaf(row_lane<L>(cv), h[V::W * i], acc);
-            if constexpr (V::W == 2) acc = fmaf(row_lane<L + 1>(cv), h[2 * i + 1], acc);
-          }
-        }
-        if (MODE == 0) to[w][t + u][lane] = acc;
+        for (int i = 0; i < NS; ++i) hh[u][i] = h[i] = fmaf(a[u][i], h[i], b[u][i]);
         d[u] = dn[u];
-      });
+      }
+      if constexpr (MODE == 0) {
+        constexpr int L = t % V::M * V::W;
+        if constexpr (NS == 1) {
+          each<4>([&](auto uu) {
+            constexpr int u = decltype(uu)::value;
+            acc[u] = row_lane<L + u>(v.c[0][t / V::M]) * hh[u][0];
+          });
+        } else {
+          each<V::P>([&](auto ii) {
+            constexpr int i = decltype(ii)::value;
+            row_dots<L, (i > 0)>(v.c[i][t / V::M], hh[0][2 * i], hh[1][2 * i], hh[2][2 * i], hh[3][2 * i], hh[0][2 * i + 1],
+                                 hh[1][2 * i + 1], hh[2][2 * i + 1], hh[3][2 * i + 1], acc);
+          });
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) to[w][t + u][lane] = acc[u];
+      }
     });
   };
   auto save = [&](int tt) {

@@ -146,6 +146,44 @@ template <int K>
 __device__ inline float row_lane(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + K, 0xf, 0xf, true));
 }
+// Sums of products with row lanes.  The compiler takes a DPP operand into a multiplication
+// but not into a multiply-add (it moves it first), so these are written out; a register read
+// by DPP must not be one that either of the two instructions before wrote, hence the s_nop.
+// acc_u = c_0 h0_u + c_1 h1_u (MORE: added to acc_u) for four tokens, whose c_0, c_1 are the
+// row lanes L + 2 u and L + 2 u + 1 of cv.
+#define GDR_DPP(OP, DST, SRC, K, B) OP " " DST ", " SRC ", " B " row_newbcast:" K " row_mask:0xf bank_mask:0xf\n\t"
+template <int L, bool MORE>
+__device__ inline void row_dots(float cv, float h00, float h01, float h02, float h03, float h10, float h11, float h12, float h13,
+                                float (&acc)[4]) {
+  if constexpr (MORE)
+    asm("s_nop 1\n\t" GDR_DPP("v_fmac_f32_dpp", "%0", "%4", "%13", "%5") GDR_DPP("v_fmac_f32_dpp", "%1", "%4", "%15", "%6")
+            GDR_DPP("v_fmac_f32_dpp", "%2", "%4", "%17", "%7") GDR_DPP("v_fmac_f32_dpp", "%3", "%4", "%19", "%8")
+                GDR_DPP("v_fmac_f32_dpp", "%0", "%4", "%14", "%9") GDR_DPP("v_fmac_f32_dpp", "%1", "%4", "%16", "%10")
+                    GDR_DPP("v_fmac_f32_dpp", "%2", "%4", "%18", "%11") GDR_DPP("v_fmac_f32_dpp", "%3", "%4", "%20", "%12")
+        : "+&v"(acc[0]), "+&v"(acc[1]), "+&v"(acc[2]), "+&v"(acc[3])
+        : "v"(cv), "v"(h00), "v"(h01), "v"(h02), "v"(h03), "v"(h10), "v"(h11), "v"(h12), "v"(h13), "n"(L), "n"(L + 1),
+          "n"(L + 2), "n"(L + 3), "n"(L + 4), "n"(L + 5), "n"(L + 6), "n"(L + 7));
+  else
+    asm("s_nop 1\n\t" GDR_DPP("v_mul_f32_dpp", "%0", "%4", "%13", "%5") GDR_DPP("v_mul_f32_dpp", "%1", "%4", "%15", "%6")
+            GDR_DPP("v_mul_f32_dpp", "%2", "%4", "%17", "%7") GDR_DPP("v_mul_f32_dpp", "%3", "%4", "%19", "%8")
+                GDR_DPP("v_fmac_f32_dpp", "%0", "%4", "%14", "%9") GDR_DPP("v_fmac_f32_dpp", "%1", "%4", "%16", "%10")
+                    GDR_DPP("v_fmac_f32_dpp", "%2", "%4", "%18", "%11") GDR_DPP("v_fmac_f32_dpp", "%3", "%4", "%20", "%12")
+        : "=&v"(acc[0]), "=&v"(acc[1]), "=&v"(acc[2]), "=&v"(acc[3])
+        : "v"(cv), "v"(h00), "v"(h01), "v"(h02), "v"(h03), "v"(h10), "v"(h11), "v"(h12), "v"(h13), "n"(L), "n"(L + 1),
+          "n"(L + 2), "n"(L + 3), "n"(L + 4), "n"(L + 5), "n"(L + 6), "n"(L + 7));
+}
+// K0, K1 += c_0 g, c_1 g; returns b_0 K0 + b_1 K1 (row lanes L, L + 1 of cv and bv).
+template <int L>
+__device__ inline float row_adjoint(float cv, float bv, float g, float& K0, float& K1) {
+  float p;
+  asm("s_nop 1\n\t" GDR_DPP("v_fmac_f32_dpp", "%0", "%3", "%6", "%5") GDR_DPP("v_fmac_f32_dpp", "%1", "%3", "%7", "%5")
+          GDR_DPP("v_mul_f32_dpp", "%2", "%4", "%6", "%0") GDR_DPP("v_fmac_f32_dpp", "%2", "%4", "%7", "%1")
+      : "+&v"(K0), "+&v"(K1), "=&v"(p)
+      : "v"(cv), "v"(bv), "v"(g), "n"(L), "n"(L + 1));
+  return p;
+}
+#undef GDR_DPP
+
 template <typename T, int NS, int TILE>
 struct Vectors {
   static constexpr int W = NS > 1 ? 2 : 1, P = NS / W, M = 16 / W, Q = TILE / M;   // M tokens a register
