@@ -5,8 +5,15 @@
 // adjoint H runs back through it.  Sums over a channel's states: each wave's parts meet in
 // LDS.  Sums over the channels (grad_Bv, grad_Cv): over the 64 lanes by lane swaps and DPP, 64
 // values at a time, then over the workgroups through partial results that
-// ssm_vector_join_kernel adds up.  Bound by the vector units: about 20 issue slots a state
-// and token.
+// ssm_vector_join_kernel adds up.
+//
+// Bound by the issue of instructions, two waves a SIMD as in the forward: 16 slots a state and
+// token cannot be done without (6 again, 10 for the adjoint and the two sums), 518 us of the
+// 931 on 8 x 4096 x 2048 with 16 states, gated; 25 are issued, 6 of them for the sums over
+// lanes.  LDS and registers allow one workgroup a CU.  Half of a block's decays computed
+// twice instead of kept: 1060; LDS read where it is used: 1006; row lanes moved to
+// registers of their own before a multiply-add: 980 us.  (The same for all of a block makes
+// the compiler spill: 2880.)
 #include "col_join.h"
 #include "ssm_tile.h"
 
