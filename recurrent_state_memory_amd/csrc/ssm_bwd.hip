@@ -14,6 +14,10 @@
 // twice instead of kept: 1060; LDS read where it is used: 1006; row lanes moved to
 // registers of their own before a multiply-add: 980 us.  (The same for all of a block makes
 // the compiler spill: 2880.)
+// More than 16 states go through each block in turns of 16 (8 x 2048 x 2048 bf16, gated, with
+// 32: 1070 us, 64: 2040), at the same rate as 16 do (476); two states at a time with half a
+// block's tokens in registers took 1570 and 2790.  Waves without a state skip the recurrence
+// (4 states: 330 -> 284 us).
 #include "col_join.h"
 #include "ssm_tile.h"
 
@@ -121,6 +125,7 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_ar
     total += tile;
     if (i > 0) load(i - 1);
     __syncthreads();   // the tile before last is read no more
+    if (w * NS >= q.N) continue;
     each<kTile>([&](auto back) {
       constexpr int t = kTile - 1 - decltype(back)::value, L = t % V::M * V::W;
       const float2 d = to[t][lane];
@@ -149,7 +154,7 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_ar
 }
 
 // ---------------------------------------------------------------- backward
-// What both kernels below start with: the adjoints of states first ... behind a segment.
+// What the kernel below starts with: the adjoints of states first ... behind a segment.
 template <int NS>
 __device__ inline void adjoint_behind(const gdr_ssm_bwd_args& p, const Geo& q, const Place& s, int first,
                                       const float (&A2)[NS], const float* ends, const float* sums, float (&K)[NS]) {
@@ -176,20 +181,37 @@ __device__ inline size_t sum_place(int Tp) {
   if (NS == 2) return (size_t)(b5 * 2 + b4) * Tp + (b3 | b2 << 1 | b1 << 2 | b0 << 3);
   return (size_t)b5 * Tp + (b4 | b3 << 1 | b2 << 2 | b1 << 3 | b0 << 4);
 }
+// A turn's values among all turns', which are registers.
+template <int NCH, int NS>
+__device__ inline void pick(int ch, const float (&all)[NCH][NS], float (&v)[NS]) {
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int k = 0; k < NS; ++k) v[k] = c == 0 || c == ch ? all[c][k] : v[k];
+}
+template <int NCH, int NS>
+__device__ inline void put(int ch, const float (&v)[NS], float (&all)[NCH][NS]) {
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int k = 0; k < NS; ++k) all[c][k] = NCH == 1 || c == ch ? v[k] : all[c][k];
+}
 // What a channel's token is prepared to.
 struct Token {
   float x, z, gy, slope;   // slope of softplus
 };
 
-// Up to 16 states: eight waves of one or two each.  A block's 32 states and decays stay in registers.
+// Eight waves of one or two states each; more than 16 are taken 16 at a time, NCH turns at
+// the most, through each block.  A turn's 32 states and decays of a block stay in registers.
 // The adjoint passes through it in four quarters; while one is worked on, the one before
 // is finished (the waves' parts added, gradients written), and the next block's inputs are
-// on their way.
-template <typename T, int NS, bool GATE>
+// on their way (with several turns, from the third quarter on: they take registers).
+template <typename T, int NS, bool GATE, int NCH>
 __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt, const float* ends,
                                                           const float* sums, float* vpart, float* rows) {
   constexpr int NW = kWaves, J = kBlock / NW, QT = 8;
   static_assert(NW == QT && (NS == 1 || NS == 2), "a token of a quarter for every wave");
+  static_assert(NCH == 1 || NS == 2, "a turn has 16 states");
   __shared__ float2 in[kBlock][kLanes];                        // d, d x
   __shared__ float gs[kBlock][kLanes];                         // g
   __shared__ float part[2][2][NW][QT][kLanes];                 // each wave's share of p and sum A q, two quarters
@@ -198,19 +220,28 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
   const Place s = place_of(q);
   const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T), end = min(t1, len);
   const size_t nc = (size_t)q.N * q.C;
-  float A[NS], A2[NS], K[NS], gA[NS];
-  const float* ck[NS];   // the states' checkpoints
+  const int turns = NCH == 1 ? 1 : (q.N + NW * NS - 1) / (NW * NS);
+  auto state = [&](int ch, int k) { return (ch * NW + w) * NS + k; };
+  auto load_A = [&](int ch, float(&A)[NS]) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) A[k] = state(ch, k) < q.N ? p.A[(size_t)s.c * q.N + state(ch, k)] : 0.f;
+  };
+  float A[NS], A2[NS], Ks[NCH][NS], gA[NCH][NS];
+#pragma unroll
+  for (int ch = NCH - 1; ch >= 0; --ch) {
+    load_A(ch, A);
+#pragma unroll
+    for (int k = 0; k < NS; ++k) A2[k] = A[k] * scan::kLog2e, gA[ch][k] = 0.f;
+    adjoint_behind<NS>(p, q, s, state(ch, 0), A2, ends, sums, Ks[ch]);
+  }
+  const float* const ck = ckpt + ((size_t)s.b * (q.Tp / kBlock) + t0 / kBlock) * nc + s.c;   // the states' checkpoints
+  const float* ck1[NS];   // the only turn's
   bool has[NS];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int n = w * NS + i;
-    gA[i] = 0.f;
-    has[i] = n < q.N && s.on;
-    A[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] : 0.f;
-    A2[i] = A[i] * scan::kLog2e;
-    ck[i] = ckpt + ((size_t)s.b * (q.Tp / kBlock) + t0 / kBlock) * nc + (size_t)(n < q.N ? n : 0) * q.C + s.c;
+  for (int k = 0; k < NS; ++k) {
+    has[k] = state(0, k) < q.N && s.on;
+    ck1[k] = ck + (size_t)(has[k] ? state(0, k) : 0) * q.C;
   }
-  adjoint_behind<NS>(p, q, s, w * NS, A2, ends, sums, K);
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
   const bool softplus = p.softplus != 0;
   const Buffer x = rows_at<T>(p.x, q, s.b, t0, end), dt = rows_at<T>(p.dt, q, s.b, t0, end),
@@ -219,15 +250,36 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
                gz = rows_at<T>(p.grad_z, q, s.b, t0, GATE ? end : t0);
   const unsigned row_bytes = (unsigned)(q.C * sizeof(T)), col = s.on ? (unsigned)(s.c * sizeof(T)) : kNowhere;
   typedef Vectors<T, NS, kBlock> V;
-  const V vectors(p.Bv, p.Cv, q, s, t0, end, w * NS);
-  float* vout = vpart + (((size_t)s.cb * q.B + s.b) * q.room + w * NS) * 2 * q.Tp + t0 + sum_place<NS>(q.Tp);
+  V vectors(p.Bv, p.Cv, q, s, t0, end, w * NS);
+  float* const vout0 = vpart + (((size_t)s.cb * q.B + s.b) * q.room + w * NS) * 2 * q.Tp + t0 + sum_place<NS>(q.Tp);
+
+  auto clear = [&]() {   // an idle wave's parts
+#pragma unroll
+    for (int t = 0; t < 2 * QT; ++t) part[t & 1][0][w][t >> 1][lane] = part[t & 1][1][w][t >> 1][lane] = 0.f;
+    if (GATE) {
+#pragma unroll
+      for (int t = 0; t < kBlock; ++t) upart[GATE ? w : 0][GATE ? t : 0][lane] = 0.f;
+    }
+  };
+  if (NS == 1 && state(0, 0) >= q.N) clear();
 
   // the next block's inputs as they come
   typedef typename Io<T>::Raw Raw;
   Raw nx[J], nd[J], ng[J], nz[J];
   typename V::Raw vr;
-  float nh[NS];
-  auto load = [&](int i) {
+  float nh[NS], nA[NS];
+  auto load_states = [&](int i, int ch) {   // and what a turn starts with
+    if constexpr (NCH > 1) {
+      vectors.states(q, state(ch, 0));
+      load_A(ch, nA);
+    }
+    vectors.load(i * kBlock, vr);
+#pragma unroll
+    for (int k = 0; k < NS; ++k)
+      if constexpr (NCH == 1) nh[k] = has[k] ? ck1[k][i * nc] : 0.f;
+      else nh[k] = state(ch, k) < q.N && s.on ? ck[i * nc + (size_t)state(ch, k) * q.C] : 0.f;
+  };
+  auto load_inputs = [&](int i, unsigned col) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const unsigned at = col + (unsigned)(i * kBlock + j * NW + w) * row_bytes;
@@ -236,13 +288,10 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
       ng[j] = Io<T>::load(gy, at);
       if (GATE) nz[j] = Io<T>::load(z, at);
     }
-    vectors.load(i * kBlock, vr);
-#pragma unroll
-    for (int k = 0; k < NS; ++k) nh[k] = has[k] ? ck[k][i * nc] : 0.f;
   };
   float gD = 0.f, gbias = 0.f;
   const int n = end > t0 ? (end - t0 + kBlock - 1) / kBlock : 0;   // blocks
-  if (n > 0) load(n - 1);
+  if (n > 0) load_inputs(n - 1, col), load_states(n - 1, 0);
 #pragma unroll 1
   for (int i = n - 1; i >= 0; --i) {
     const int tt = t0 + i * kBlock;
@@ -264,136 +313,180 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
       in[t][lane] = float2{d, d * own[j].x};
       gs[t][lane] = g;
     }
-    typename V::Set v;
-    vectors.take(vr, v);
-    float h[kBlock + 1][NS], a[kBlock][NS];
+    float sp[NCH > 1 ? J : 1], sd[NCH > 1 ? J : 1], su[NCH > 1 ? J : 1];   // the turns' sums
+    if constexpr (NCH > 1) {
 #pragma unroll
-    for (int k = 0; k < NS; ++k) h[0][k] = nh[k];
-    __syncthreads();
-    if (i > 0) load(i - 1);
-    // LDS is read a group of tokens ahead; the groups stay apart, else loads of many of
-    // them take the registers
-    float2 dn[4];
+      for (int j = 0; j < J; ++j) sp[j] = sd[j] = su[j] = 0.f;
+    }
+    auto turn = [&](int ch) {
+      const bool last = ch == turns - 1;
+      float K[NS];
+      pick(ch, Ks, K);
+      typename V::Set v;
+      vectors.take(vr, v);
+      float h[kBlock + 1][NS], a[kBlock][NS];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) dn[u] = in[u][lane];
-    each<kBlock / 4>([&](auto gi) {
-      constexpr int t4 = decltype(gi)::value * 4;
-      const float2 d4[4] = {dn[0], dn[1], dn[2], dn[3]};
-      if constexpr (t4 + 4 < kBlock) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) dn[u] = in[t4 + 4 + u][lane];
+      for (int k = 0; k < NS; ++k) {
+        h[0][k] = nh[k];
+        if constexpr (NCH > 1) A[k] = nA[k], A2[k] = A[k] * scan::kLog2e;
       }
-      each<4>([&](auto ui) {
-        constexpr int u = decltype(ui)::value, t = t4 + u, L = t % V::M * V::W;
-        const float2 d = d4[u];
-        const float bv = v.b[0][t / V::M];
-#pragma unroll
-        for (int k = 0; k < NS; ++k) a[t][k] = __builtin_amdgcn_exp2f(d.x * A2[k]);
-        h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
-        if constexpr (NS == 2) h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
-        if constexpr (GATE && NS == 1) upart[w][t][lane] = row_lane<L>(v.c[0][t / V::M]) * h[t + 1][0];
-      });
-      if constexpr (GATE && NS == 2) {
-        float u[4];
-        row_dots<t4 % V::M * 2, false>(v.c[0][t4 / V::M], h[t4 + 1][0], h[t4 + 2][0], h[t4 + 3][0], h[t4 + 4][0], h[t4 + 1][1],
-                                       h[t4 + 2][1], h[t4 + 3][1], h[t4 + 4][1], u);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) upart[w][t4 + k][lane] = u[k];
+      float* const vout = vout0 + (size_t)ch * (NW * NS) * 2 * q.Tp;
+      // a wave without a state leaves the others its SIMD
+      const bool idle = (NS == 1 || NCH > 1) && state(ch, 0) >= q.N;
+      __syncthreads();
+      if (NCH > 1 && idle) clear();
+      if constexpr (NCH == 1) {
+        if (i > 0) load_inputs(i - 1, col), load_states(i - 1, 0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    vectors.forget(v);
-    float r2[2], r4[2], r8[2], r16[4], gAb[NS];
+      float r2[2], r4[2], r8[2], r16[4], gAb[NS];
 #pragma unroll
-    for (int k = 0; k < NS; ++k) gAb[k] = 0.f;
-    float2 rd[2];
-    float rg[2];
+      for (int k = 0; k < NS; ++k) gAb[k] = 0.f;
+      float2 rd[2];
+      float rg[2];
+      if (!idle) {
+        // LDS is read a group of tokens ahead; the groups stay apart, else loads of many of
+        // them take the registers
+        float2 dn[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) rd[u] = in[kBlock - 2 + u][lane], rg[u] = gs[kBlock - 2 + u][lane];
-    auto quarter = [&](auto qi) {
-      constexpr int Q = decltype(qi)::value;
-      each<QT / 2>([&](auto back) {
-        constexpr int ts2 = QT - 2 - 2 * decltype(back)::value, t2 = Q * QT + ts2;
-        const float2 d2[2] = {rd[0], rd[1]};
-        const float g2[2] = {rg[0], rg[1]};
-        if constexpr (t2 > 0) {
+        for (int u = 0; u < 4; ++u) dn[u] = in[u][lane];
+        each<kBlock / 4>([&](auto gi) {
+          constexpr int t4 = decltype(gi)::value * 4;
+          const float2 d4[4] = {dn[0], dn[1], dn[2], dn[3]};
+          if constexpr (t4 + 4 < kBlock) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) rd[u] = in[t2 - 2 + u][lane], rg[u] = gs[t2 - 2 + u][lane];
-        }
-        each<2>([&](auto ui) {
-          constexpr int u = 1 - decltype(ui)::value, ts = ts2 + u, t = t2 + u, L = t % V::M * V::W;
-          const float2 d = d2[u];
-          const float g = g2[u], bv = v.b[0][t / V::M], cv = v.c[0][t / V::M];
-          float H[NS], pp, dd;
-          if constexpr (NS == 2) {
-            H[0] = K[0], H[1] = K[1];
-            pp = row_adjoint<L>(cv, bv, g, H[0], H[1]);
-            r2[u] = swap16_add(swap32_add(H[0] * d.y, H[1] * d.y), swap32_add(g * h[t + 1][0], g * h[t + 1][1]));
-          } else {
-            H[0] = fmaf(row_lane<L>(cv), g, K[0]);
-            pp = row_lane<L>(bv) * H[0];
-            r2[u] = swap32_add(H[0] * d.y, g * h[t + 1][0]);
+            for (int u = 0; u < 4; ++u) dn[u] = in[t4 + 4 + u][lane];
           }
+          each<4>([&](auto ui) {
+            constexpr int u = decltype(ui)::value, t = t4 + u, L = t % V::M * V::W;
+            const float2 d = d4[u];
+            const float bv = v.b[0][t / V::M];
 #pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            K[k] = H[k] * a[t][k];
-            const float qk = K[k] * h[t][k];
-            gAb[k] = fmaf(d.x, qk, gAb[k]);
-            dd = k == 0 ? A[0] * qk : fmaf(A[k], qk, dd);
+            for (int k = 0; k < NS; ++k) a[t][k] = __builtin_amdgcn_exp2f(d.x * A2[k]);
+            h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
+            if constexpr (NS == 2) h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
+            if constexpr (GATE && NS == 1) upart[w][t][lane] = row_lane<L>(v.c[0][t / V::M]) * h[t + 1][0];
+          });
+          if constexpr (GATE && NS == 2) {
+            float u[4];
+            row_dots<t4 % V::M * 2, false>(v.c[0][t4 / V::M], h[t4 + 1][0], h[t4 + 2][0], h[t4 + 3][0], h[t4 + 4][0], h[t4 + 1][1],
+                                           h[t4 + 2][1], h[t4 + 3][1], h[t4 + 4][1], u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) upart[w][t4 + k][lane] = u[k];
           }
-          part[Q & 1][0][w][ts][lane] = pp;
-          part[Q & 1][1][w][ts][lane] = dd;
+          __builtin_amdgcn_sched_barrier(0);
         });
-        // the lanes' sums: tokens 2m and 2m + 1 share a register, then pairs of them, ...
-        if constexpr (NS == 2) {
-          r8[t2 >> 1 & 1] = half8_add(r2[0], r2[1]);
-          if constexpr ((t2 & 3) == 0) r16[t2 >> 2 & 3] = half4_add(r8[0], r8[1]);
-          if constexpr ((t2 & 15) == 0) vout[i * kBlock + t2] = quads_add(r16);
-        } else {
-          r4[t2 >> 1 & 1] = swap16_add(r2[0], r2[1]);
-          if constexpr ((t2 & 3) == 0) r8[t2 >> 2 & 1] = half8_add(r4[0], r4[1]);
-          if constexpr ((t2 & 7) == 0) r16[t2 >> 3 & 3] = half4_add(r8[0], r8[1]);
-          if constexpr ((t2 & 31) == 0) vout[i * kBlock + t2] = quads_add(r16);
+        vectors.forget(v);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) rd[u] = in[kBlock - 2 + u][lane], rg[u] = gs[kBlock - 2 + u][lane];
+      }
+      auto quarter = [&](auto qi) {
+        constexpr int Q = decltype(qi)::value;
+        if (!idle) each<QT / 2>([&](auto back) {
+          constexpr int ts2 = QT - 2 - 2 * decltype(back)::value, t2 = Q * QT + ts2;
+          const float2 d2[2] = {rd[0], rd[1]};
+          const float g2[2] = {rg[0], rg[1]};
+          if constexpr (t2 > 0) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) rd[u] = in[t2 - 2 + u][lane], rg[u] = gs[t2 - 2 + u][lane];
+          }
+          each<2>([&](auto ui) {
+            constexpr int u = 1 - decltype(ui)::value, ts = ts2 + u, t = t2 + u, L = t % V::M * V::W;
+            const float2 d = d2[u];
+            const float g = g2[u], bv = v.b[0][t / V::M], cv = v.c[0][t / V::M];
+            float H[NS], pp, dd;
+            if constexpr (NS == 2) {
+              H[0] = K[0], H[1] = K[1];
+              pp = row_adjoint<L>(cv, bv, g, H[0], H[1]);
+              r2[u] = swap16_add(swap32_add(H[0] * d.y, H[1] * d.y), swap32_add(g * h[t + 1][0], g * h[t + 1][1]));
+            } else {
+              H[0] = fmaf(row_lane<L>(cv), g, K[0]);
+              pp = row_lane<L>(bv) * H[0];
+              r2[u] = swap32_add(H[0] * d.y, g * h[t + 1][0]);
+            }
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+              K[k] = H[k] * a[t][k];
+              const float qk = K[k] * h[t][k];
+              gAb[k] = fmaf(d.x, qk, gAb[k]);
+              dd = k == 0 ? A[0] * qk : fmaf(A[k], qk, dd);
+            }
+            part[Q & 1][0][w][ts][lane] = pp;
+            part[Q & 1][1][w][ts][lane] = dd;
+          });
+          // the lanes' sums: tokens 2m and 2m + 1 share a register, then pairs of them, ...
+          if constexpr (NS == 2) {
+            r8[t2 >> 1 & 1] = half8_add(r2[0], r2[1]);
+            if constexpr ((t2 & 3) == 0) r16[t2 >> 2 & 3] = half4_add(r8[0], r8[1]);
+            if constexpr ((t2 & 15) == 0) vout[i * kBlock + t2] = quads_add(r16);
+          } else {
+            r4[t2 >> 1 & 1] = swap16_add(r2[0], r2[1]);
+            if constexpr ((t2 & 3) == 0) r8[t2 >> 2 & 1] = half8_add(r4[0], r4[1]);
+            if constexpr ((t2 & 7) == 0) r16[t2 >> 3 & 3] = half4_add(r8[0], r8[1]);
+            if constexpr ((t2 & 31) == 0) vout[i * kBlock + t2] = quads_add(r16);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      auto finish = [&](auto qi) {
+        constexpr int Q = decltype(qi)::value;
+        const int t = Q * QT + w;
+        float pp = 0.f, dd = 0.f;
+#pragma unroll
+        for (int m = 0; m < NW; ++m) pp += part[Q & 1][0][m][w][lane], dd += part[Q & 1][1][m][w][lane];
+        auto sum_u = [&](float u) {
+#pragma unroll
+          for (int m = 0; m < NW; ++m) u += upart[GATE ? m : 0][GATE ? t : 0][lane];
+          return u;
+        };
+        if constexpr (NCH > 1) {
+          pp = sp[Q] += pp, dd = sd[Q] += dd;
+          if (GATE) su[Q] = sum_u(su[Q]);
+          if (!last) return;
+        }
+        const float d = in[t][lane].x, g = gs[t][lane], gd = fmaf(pp, own[Q].x, dd) * own[Q].slope;
+        const unsigned at = col + (unsigned)(i * kBlock + t) * row_bytes;
+        gbias += gd;
+        gD = fmaf(g, own[Q].x, gD);
+        Io<T>::store(gx, at, fmaf(pp, d, D * g));
+        Io<T>::store(gdt, at, gd);
+        if (GATE) {
+          const float u = NCH > 1 ? fmaf(D, own[Q].x, su[NCH > 1 ? Q : 0]) : sum_u(D * own[Q].x);
+          const float sg = scan::sigmoid(own[Q].z);
+          Io<T>::store(gz, at, own[Q].gy * u * sg * fmaf(own[Q].z, 1.f - sg, 1.f));
         }
         __builtin_amdgcn_sched_barrier(0);
-      });
-    };
-    auto finish = [&](auto qi) {
-      constexpr int Q = decltype(qi)::value;
-      const int t = Q * QT + w;
-      float pp = 0.f, dd = 0.f;
-#pragma unroll
-      for (int m = 0; m < NW; ++m) pp += part[Q & 1][0][m][w][lane], dd += part[Q & 1][1][m][w][lane];
-      const float d = in[t][lane].x, g = gs[t][lane], gd = fmaf(pp, own[Q].x, dd) * own[Q].slope;
-      const unsigned at = col + (unsigned)(i * kBlock + t) * row_bytes;
-      gbias += gd;
-      gD = fmaf(g, own[Q].x, gD);
-      Io<T>::store(gx, at, fmaf(pp, d, D * g));
-      Io<T>::store(gdt, at, gd);
-      if (GATE) {
-        float u = D * own[Q].x;
-#pragma unroll
-        for (int m = 0; m < NW; ++m) u += upart[GATE ? m : 0][GATE ? t : 0][lane];
-        const float sg = scan::sigmoid(own[Q].z);
-        Io<T>::store(gz, at, own[Q].gy * u * sg * fmaf(own[Q].z, 1.f - sg, 1.f));
+      };
+      quarter(std::integral_constant<int, 3>());
+      __syncthreads();
+      finish(std::integral_constant<int, 3>());
+      quarter(std::integral_constant<int, 2>());
+      __syncthreads();
+      finish(std::integral_constant<int, 2>());
+      if constexpr (NCH > 1) {
+        // Into the registers of the quarters that are done; in every turn, else those that do
+        // not load keep the registers.
+        load_inputs(i - 1, last && i > 0 ? col : kNowhere);
+        load_states(last && i > 0 ? i - 1 : i, last ? 0 : ch + 1);
       }
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    quarter(std::integral_constant<int, 3>());
-    __syncthreads();
-    finish(std::integral_constant<int, 3>());
-    quarter(std::integral_constant<int, 2>());
-    __syncthreads();
-    finish(std::integral_constant<int, 2>());
-    quarter(std::integral_constant<int, 1>());
-    __syncthreads();
-    finish(std::integral_constant<int, 1>());
-    quarter(std::integral_constant<int, 0>());
-    __syncthreads();
-    // in, gs and own are this wave's own tokens' here, so the next block's may follow
-    finish(std::integral_constant<int, 0>());
+      quarter(std::integral_constant<int, 1>());
+      __syncthreads();
+      finish(std::integral_constant<int, 1>());
+      quarter(std::integral_constant<int, 0>());
+      __syncthreads();
+      // in, gs and own are this wave's own tokens' here, so the next block's may follow
+      finish(std::integral_constant<int, 0>());
+      put(ch, K, Ks);
 #pragma unroll
-    for (int k = 0; k < NS; ++k) gA[k] += gAb[k];   // block by block: fewer additions behind a sum
+      for (int c = 0; c < NCH; ++c)   // block by block: fewer additions behind a sum
+#pragma unroll
+        for (int k = 0; k < NS; ++k) gA[c][k] += NCH == 1 || c == ch ? gAb[k] : 0.f;
+    };
+    if constexpr (NCH == 1) {
+      turn(0);
+    } else {
+#pragma unroll 1
+      for (int ch = 0; ch < turns; ++ch) turn(ch);
+    }
   }
   // behind the row's end the gradients are 0
   if (s.on) {
@@ -407,223 +500,16 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
   // parameters' gradients: a row [N + 2][C] of this batch row and segment
   float* out = rows + ((size_t)s.b * q.segs + s.seg) * (q.N + 2) * q.C + s.c;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int n = w * NS + i;
-    if (has[i]) {
-      out[(size_t)n * q.C] = gA[i];
-      if (p.grad_h0 && s.seg == 0) p.grad_h0[((size_t)s.b * q.C + s.c) * q.N + n] = K[i];
-    }
-  }
-  __syncthreads();
-  in[w][lane] = float2{gD, gbias};
-  __syncthreads();
-  if (w == 0 && s.on) {
-    gD = gbias = 0.f;
+  for (int ch = 0; ch < NCH; ++ch)
 #pragma unroll
-    for (int k = 0; k < NW; ++k) gD += in[k][lane].x, gbias += in[k][lane].y;
-    out[(size_t)q.N * q.C] = gD;
-    out[(size_t)(q.N + 1) * q.C] = gbias;
-  }
-}
-
-// More states: eight waves take them two at a time in NCH turns, whose adjoints and grad_A
-// wait in LDS.  Half a block is worked on at a time, the states of its second half from
-// the block's start.
-template <typename T, int NCH>
-__global__ __launch_bounds__(kWaves * 64) void ssm_bwd_wide_kernel(gdr_ssm_bwd_args p, Geo q, const float* ckpt,
-                                                          const float* ends, const float* sums, float* vpart, float* rows) {
-  constexpr int NW = kWaves, SUB = 16, J = SUB / NW;
-  __shared__ float2 in[kBlock][kLanes];      // d, d x
-  __shared__ float gs[kBlock][kLanes];       // g
-  __shared__ float part[3][NW][SUB][kLanes]; // each wave's share of p, sum A q, sum C h
-  __shared__ float later[NCH * 4][NW][kLanes];   // K0, K1, grad_A0, grad_A1 of each turn
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place s = place_of(q);
-  const int len = row_len(p.lens, s.b, q.T), t0 = s.seg * q.seg, t1 = min(t0 + q.seg, q.T), end = min(t1, len);
-  const size_t nc = (size_t)q.N * q.C;
-  const int blocks = q.Tp / kBlock;
-  float A[2], A2[2], K[2], gA[2];
-  auto load_turn = [&](int ch) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int n = (ch * NW + w) * 2 + i;
-      A[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] : 0.f;
-      A2[i] = A[i] * scan::kLog2e;
-    }
-  };
-#pragma unroll
-  for (int ch = 0; ch < NCH; ++ch) {
-    load_turn(ch);
-    adjoint_behind<2>(p, q, s, (ch * NW + w) * 2, A2, ends, sums, K);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = 0.f;
-    }
-  }
-  const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f, D = p.D ? p.D[s.c] : 0.f;
-  const bool softplus = p.softplus != 0, gate = p.z != nullptr;
-  const size_t row0 = (size_t)s.b * q.T * q.C + s.c;
-  const T *x = (const T*)p.x + row0, *dt = (const T*)p.dt + row0, *z = (const T*)p.z + row0, *gy = (const T*)p.grad_y + row0;
-  T *gx = (T*)p.grad_x + row0, *gdt = (T*)p.grad_dt + row0, *gz = (T*)p.grad_z + row0;
-  const size_t mine = sum_place<2>(q.Tp);
-  float gD = 0.f, gbias = 0.f;
-
-  for (int tt = t0 + (t1 - 1 - t0) / kBlock * kBlock; tt >= t0; tt -= kBlock) {
-    if (tt >= len) {   // behind the row's end
-#pragma unroll
-      for (int j = 0; j < kBlock / NW; ++j) {
-        const int t = tt + j * NW + w;
-        if (t < t1 && s.on) {
-          chan::st(gx + (size_t)t * q.C, 0.f);
-          chan::st(gdt + (size_t)t * q.C, 0.f);
-          if (gate) chan::st(gz + (size_t)t * q.C, 0.f);
-        }
-      }
-      continue;
-    }
-    float xs[2 * J], slope[2 * J], zs[2 * J], gys[2 * J];
-#pragma unroll
-    for (int j = 0; j < 2 * J; ++j) {
-      const int t = j * NW + w;
-      const bool live = tt + t < min(t1, len) && s.on;   // lanes without a channel add nothing to the sums
-      float d = 0.f, g = 0.f;
-      xs[j] = zs[j] = gys[j] = 0.f;
-      slope[j] = 1.f;
-      if (live) {
-        const size_t at = (size_t)(tt + t) * q.C;
-        xs[j] = ld(x + at);
-        gys[j] = g = ld(gy + at);
-        d = ld(dt + at) + bias;
-        if (softplus) d = scan::softplus(d, slope[j]);
-        if (gate) {
-          zs[j] = ld(z + at);
-          g *= zs[j] * scan::sigmoid(zs[j]);
-        }
-      }
-      in[t][lane] = float2{d, d * xs[j]};
-      gs[t][lane] = g;
-    }
-    __syncthreads();
-    for (int sub = 1; sub >= 0; --sub) {
-      const int st = sub * SUB;
-#pragma unroll
-      for (int ch = 0; ch < NCH; ++ch) {
-        {
-          load_turn(ch);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
-        }
-        const Vectors<T, 2, SUB> vectors(p.Bv, p.Cv, q, s, t0, end, 2 * (ch * NW + w));
-        typename Vectors<T, 2, SUB>::Raw vr;
-        typename Vectors<T, 2, SUB>::Set v;
-        float h[SUB + 1][2], a[SUB][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int n = (ch * NW + w) * 2 + i;
-          h[0][i] = n < q.N && s.on ? ckpt[((size_t)s.b * blocks + tt / kBlock) * nc + (size_t)n * q.C + s.c] : 0.f;
-        }
-        if (sub == 1) {
-          vectors.load(tt - t0, vr);
-          vectors.take(vr, v);
-          each<SUB>([&](auto ti) {
-            constexpr int t = decltype(ti)::value, L = t % 8 * 2;
-            const float2 d = in[t][lane];
-            const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
-            h[0][0] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[0]), h[0][0], d.y * row_lane<L>(bv));
-            h[0][1] = fmaf(__builtin_amdgcn_exp2f(d.x * A2[1]), h[0][1], d.y * row_lane<L + 1>(bv));
-          });
-        }
-        vectors.load(tt + st - t0, vr);
-        vectors.take(vr, v);
-        each<SUB>([&](auto ti) {
-          constexpr int t = decltype(ti)::value, L = t % 8 * 2;
-          const float2 d = in[st + t][lane];
-          const float bv = v.b[0][t / 8], cv = v.c[0][t / 8];
-          a[t][0] = __builtin_amdgcn_exp2f(d.x * A2[0]);
-          a[t][1] = __builtin_amdgcn_exp2f(d.x * A2[1]);
-          h[t + 1][0] = fmaf(a[t][0], h[t][0], d.y * row_lane<L>(bv));
-          h[t + 1][1] = fmaf(a[t][1], h[t][1], d.y * row_lane<L + 1>(bv));
-          if (gate) {
-            const float u = fmaf(row_lane<L + 1>(cv), h[t + 1][1], row_lane<L>(cv) * h[t + 1][0]);
-            float* at = &part[2][w][t][lane];
-            *at = ch == 0 ? u : *at + u;
-          }
-        });
-        vectors.forget(v);
-        float r2[2], r4[2], r8[4];
-        each<SUB>([&](auto back) {
-          constexpr int t = SUB - 1 - decltype(back)::value, L = t % 8 * 2;
-          const float2 d = in[st + t][lane];
-          const float g = gs[st + t][lane], bv = v.b[0][t / 8], cv = v.c[0][t / 8];
-          const float H0 = fmaf(row_lane<L>(cv), g, K[0]), H1 = fmaf(row_lane<L + 1>(cv), g, K[1]);
-          const float b = swap32_add(H0 * d.y, H1 * d.y), c = swap32_add(g * h[t + 1][0], g * h[t + 1][1]);
-          const float bc4 = swap16_add(b, c);
-          const float pp = fmaf(row_lane<L + 1>(bv), H1, row_lane<L>(bv) * H0);
-          K[0] = H0 * a[t][0];
-          K[1] = H1 * a[t][1];
-          const float q0 = K[0] * h[t][0], q1 = K[1] * h[t][1];
-          gA[0] = fmaf(d.x, q0, gA[0]);
-          gA[1] = fmaf(d.x, q1, gA[1]);
-          const float dd = fmaf(A[1], q1, A[0] * q0);
-          float *pp_at = &part[0][w][t][lane], *dd_at = &part[1][w][t][lane];
-          *pp_at = ch == 0 ? pp : *pp_at + pp;
-          *dd_at = ch == 0 ? dd : *dd_at + dd;
-          // tokens 2m + 1 and 2m, then pairs of them, then the four quarters
-          r2[t & 1] = bc4;
-          if constexpr ((t & 1) == 0) r4[t >> 1 & 1] = half8_add(r2[0], r2[1]);
-          if constexpr ((t & 3) == 0) r8[t >> 2] = half4_add(r4[0], r4[1]);
-        });
-        vpart[(((size_t)s.cb * q.B + s.b) * q.room + 2 * (ch * NW + w)) * 2 * q.Tp + tt + st + mine] = quads_add(r8);
-        {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) later[ch * 4 + i][w][lane] = K[i], later[ch * 4 + 2 + i][w][lane] = gA[i];
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int jj = 0; jj < 2 * J; ++jj) {
-        if (jj / J != sub) continue;
-        const int t = jj * NW + w, ts = t - st;
-        float pp = 0.f, dd = 0.f, u = 0.f;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-          pp += part[0][k][ts][lane];
-          dd += part[1][k][ts][lane];
-          if (gate) u += part[2][k][ts][lane];
-        }
-        const float d = in[t][lane].x, g = gs[t][lane];
-        const bool live = tt + t < len;
-        const float gd = live ? fmaf(pp, xs[jj], dd) * slope[jj] : 0.f;
-        gbias += gd;
-        gD = fmaf(g, xs[jj], gD);
-        if (tt + t < t1 && s.on) {
-          const size_t at = (size_t)(tt + t) * q.C;
-          chan::st(gx + at, live ? fmaf(pp, d, D * g) : 0.f);
-          chan::st(gdt + at, gd);
-          if (gate) {
-            const float sg = scan::sigmoid(zs[jj]);
-            u = fmaf(D, xs[jj], u);
-            chan::st(gz + at, live ? gys[jj] * u * sg * fmaf(zs[jj], 1.f - sg, 1.f) : 0.f);
-          }
-        }
-      }
-      __syncthreads();
-    }
-  }
-  // parameters' gradients: a row [N + 2][C] of this batch row and segment
-  float* out = rows + ((size_t)s.b * q.segs + s.seg) * (q.N + 2) * q.C + s.c;
-#pragma unroll
-  for (int ch = 0; ch < NCH; ++ch) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int n = (ch * NW + w) * 2 + i;
-      K[i] = later[ch * 4 + i][w][lane], gA[i] = later[ch * 4 + 2 + i][w][lane];
+    for (int k = 0; k < NS; ++k) {
+      const int n = state(ch, k);
       if (n < q.N && s.on) {
-        out[(size_t)n * q.C] = gA[i];
-        if (p.grad_h0 && s.seg == 0) p.grad_h0[((size_t)s.b * q.C + s.c) * q.N + n] = K[i];
+        out[(size_t)n * q.C] = gA[ch][k];
+        if (p.grad_h0 && s.seg == 0) p.grad_h0[((size_t)s.b * q.C + s.c) * q.N + n] = Ks[ch][k];
       }
     }
-  }
+  __syncthreads();
   in[w][lane] = float2{gD, gbias};
   __syncthreads();
   if (w == 0 && s.on) {
@@ -713,12 +599,12 @@ static hipError_t bwd(const gdr_ssm_bwd_args& a, hipStream_t s) {
   const dim3 grid(q.blocks());
 #define SSM_BWD(...) \
   hipLaunchKernelGGL((__VA_ARGS__), grid, dim3(kWaves * 64), 0, s, a, q, ckpt, ends, sums, vpart, rows)
-  if (q.N <= 8 && a.z) SSM_BWD(ssm_bwd_kernel<T, 1, true>);
-  else if (q.N <= 8) SSM_BWD(ssm_bwd_kernel<T, 1, false>);
-  else if (q.N <= 16 && a.z) SSM_BWD(ssm_bwd_kernel<T, 2, true>);
-  else if (q.N <= 16) SSM_BWD(ssm_bwd_kernel<T, 2, false>);
-  else if (q.N <= 32) SSM_BWD(ssm_bwd_wide_kernel<T, 2>);
-  else SSM_BWD(ssm_bwd_wide_kernel<T, 4>);
+  if (q.N <= 8 && a.z) SSM_BWD(ssm_bwd_kernel<T, 1, true, 1>);
+  else if (q.N <= 8) SSM_BWD(ssm_bwd_kernel<T, 1, false, 1>);
+  else if (q.N <= 16 && a.z) SSM_BWD(ssm_bwd_kernel<T, 2, true, 1>);
+  else if (q.N <= 16) SSM_BWD(ssm_bwd_kernel<T, 2, false, 1>);
+  else if (a.z) SSM_BWD(ssm_bwd_kernel<T, 2, true, 4>);
+  else SSM_BWD(ssm_bwd_kernel<T, 2, false, 4>);
 #undef SSM_BWD
   const size_t blocks = ((size_t)q.B * q.G * q.N * q.Tp + 255) / 256;
   hipLaunchKernelGGL(ssm_vector_join_kernel<T>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s,

@@ -205,6 +205,9 @@ struct Vectors {
     step = (unsigned)(row * sizeof(T));
     Bv = buffer_at((const T*)b + base, bytes);
     Cv = buffer_at((const T*)c + base, bytes);
+    states(q, first);
+  }
+  __device__ inline void states(const Geo& q, int first) {
     const int j = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < P; ++i) {

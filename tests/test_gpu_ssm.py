@@ -11,6 +11,7 @@ SHAPES = [  # B, T, C, N, G, padded
     (1, 1, 1, 1, 1, False), (2, 1, 70, 16, 1, False), (1, 31, 3, 5, 1, False), (3, 33, 64, 16, 1, True),
     (2, 64, 65, 8, 1, False), (1, 97, 130, 16, 2, False), (4, 50, 12, 3, 4, True), (1, 200, 64, 4, 1, False),
     (2, 70, 40, 32, 1, True), (1, 65, 66, 64, 1, False), (2, 40, 20, 17, 2, True), (1, 33, 9, 63, 3, False),
+    (1, 300, 66, 48, 1, True), (2, 130, 30, 40, 1, True), (1, 600, 64, 2, 1, False), (1, 1500, 20, 33, 2, True),
     (1, 1100, 64, 16, 1, False), (2, 700, 10, 8, 1, True), (7, 130, 96, 16, 1, True),
 ]
 
