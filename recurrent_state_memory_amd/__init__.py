@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from typing import Optional
 
@@ -1532,7 +1533,7 @@ def gdr_gnorm_fwd(x, groups, weight=None, bias=None, *, z=None, silu=False, cent
     if x.dim() < 1:
         raise ValueError("gdr: x must be [...,C]")
     shape, io, f32, dev = x.shape, x.dtype, torch.float32, x.device
-    lead, chans, G = shape[:-1], shape[-1], int(groups)
+    lead, chans, G = shape[:-1], shape[-1], operator.index(groups)
     R, code_io = math.prod(lead), _io(x)
     xp = _in(x, "x", shape, io, dev)
     zp = _opt(z, "z", shape, io, dev)
@@ -1572,7 +1573,7 @@ def gdr_gnorm_bwd(grad_y, x, mean, rstd, groups, weight=None, bias=None, *, z=No
     if grad_y.dim() < 1:
         raise ValueError("gdr: grad_y must be [...,C]")
     shape, io, f32, dev = grad_y.shape, grad_y.dtype, torch.float32, grad_y.device
-    lead, chans, G = shape[:-1], shape[-1], int(groups)
+    lead, chans, G = shape[:-1], shape[-1], operator.index(groups)
     R, code_io = math.prod(lead), _io(grad_y)
     if G < 1 or chans % G:
         raise ValueError(f"gdr: {chans} channels do not fall into {groups} groups")

@@ -1,8 +1,8 @@
 // conv.hip -- short causal convolution, its backward and its single-token step, gfx950.
 //
 // A thread holds one 16-byte run of channels (four channels in the backward) and walks a
-// stretch of tokens with the last K rows in registers, so x is read once (the K - 1 rows ahead of a stretch come from the
-// caches).  LX threads of a workgroup share a row, the other 256 / LX take further
+// stretch of tokens with the last K rows in registers, so x is read once (the K - 1 rows
+// ahead of a stretch come from the caches).  LX threads of a workgroup share a row, the other 256 / LX take further
 // stretches.  On 8 x 4096 x 2048 bf16 with 4 taps and silu the forward takes 50 us, HBM's
 // rate (5.4 TB/s); the backward 91 us (4.4 TB/s): its arithmetic, some 30 instructions an
 // element, takes about 60 of them.  Backward with eight channels a thread (two waves a SIMD):

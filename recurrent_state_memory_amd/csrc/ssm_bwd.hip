@@ -9,7 +9,7 @@
 //
 // Bound by the issue of instructions, two waves a SIMD as in the forward: 16 slots a state and
 // token cannot be done without (6 again, 10 for the adjoint and the two sums), 518 us of the
-// 931 on 8 x 4096 x 2048 with 16 states, gated; 25 are issued, 6 of them for the sums over
+// 917 on 8 x 4096 x 2048 with 16 states, gated; 25 are issued, 6 of them for the sums over
 // lanes.  LDS and registers allow one workgroup a CU.  Half of a block's decays computed
 // twice instead of kept: 1060; LDS read where it is used: 1006; row lanes moved to
 // registers of their own before a multiply-add: 980 us.  (The same for all of a block makes
@@ -23,8 +23,6 @@
 
 namespace gdr {
 namespace ssm {
-
-using chan::ld;
 
 // ---------------------------------------------------------------- sums over lanes
 // 64 values of every lane in, lane_value(v)'s sum over the 64 lanes out, by halves: each
@@ -125,7 +123,7 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_ar
     total += tile;
     if (i > 0) load(i - 1);
     __syncthreads();   // the tile before last is read no more
-    if (w * NS >= q.N) continue;
+    if (NS == 1 && w >= q.N) continue;   // a wave without a state
     each<kTile>([&](auto back) {
       constexpr int t = kTile - 1 - decltype(back)::value, L = t % V::M * V::W;
       const float2 d = to[t][lane];

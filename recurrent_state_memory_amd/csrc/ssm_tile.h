@@ -142,8 +142,9 @@ __device__ inline Buffer rows_at(const void* base, const Geo& q, int b, int t, i
 // B_t and C_t of a wave's states, two registers for eight tokens and a pair of states (or
 // sixteen tokens and the wave's only state): each row of 16 lanes holds B's (C's) of both
 // states for the eight, lane 2 (t % 8) + i, and the arithmetic takes them from there by DPP
-// (row_newbcast), mostly at no instruction of its own.  (From scalar registers: every scalar load misses its cache, as 64 bytes are four
-// tokens, and returns out of order, so that each wait is for the last one.)
+// (row_newbcast), mostly at no instruction of its own.  (From scalar registers: every scalar
+// load misses its cache, as 64 bytes are four tokens, and returns out of order, so that each
+// wait is for the last one.)
 template <int K>
 __device__ inline float row_lane(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + K, 0xf, 0xf, true));

@@ -189,6 +189,16 @@ def test_binding_checks():
             call()
 
 
+@pytest.mark.parametrize("groups", [2.5, 2.0, "2", None])
+def test_groups_are_whole(groups):
+    import torch
+    x, r = torch.zeros(3, 8), torch.zeros(3, 2)
+    with pytest.raises(TypeError):
+        gdr.gdr_gnorm_fwd(x, groups)
+    with pytest.raises(TypeError):
+        gdr.gdr_gnorm_bwd(x, x, r, r, groups)
+
+
 def test_host_half_under_sanitizers(tmp_path):
     import shutil
     gxx = shutil.which("g++")
