@@ -268,7 +268,12 @@ __device__ inline void pass_segments(const Geo& q, const Place& s, int first, in
     for (int j = 0; j < KB; ++j) {
       if (j < n) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(A2[i] * d[j]), h[i], e[j][i]);
+        for (int i = 0; i < NS; ++i) {
+          // the factor's root, twice, and finite: a growing segment's may pass fp32 where
+          // what it multiplies is 0 or small
+          const float root = __builtin_amdgcn_exp2f(fminf(0.5f * A2[i] * d[j], 127.f));
+          h[i] = fmaf(root, root * h[i], e[j][i]);
+        }
       }
     }
     k0 += n * dir;

@@ -170,3 +170,27 @@ def test_long_rows_in_place():
     g = gdr.gdr_ssm_bwd(t["dy"], *args, ckpt=ck, grad_h=m.dev(d["dh"]), **kw)
     g1 = gdr.gdr_ssm_bwd(t["dy"], *args, h0=hin, grad_h=m.dev(d["dh"]), **kw)
     assert all(torch.equal(g[k], g1[k]) for k in g)
+
+
+@pytest.mark.parametrize("saved", [True, False])
+def test_growing_states_that_are_zero(saved):
+    """Over 64 steps of e^2 a factor passes fp32, but a state (an adjoint) of zero stays zero
+    however many such steps run side by side.  The inputs lie at one end, the gradients at
+    the other; all numbers are positive, so a result's error is that of its factors: 8 steps
+    of (|A| d log2(e) + 3) 2^-24 and 16 terms, twice at most: less than 2^-16."""
+    import torch
+    import recurrent_state_memory_amd as gdr
+    T, C, N = 1000, 64, 16
+    rng = np.random.default_rng(3)
+    x, gy = np.zeros((1, T, C), np.float32), np.zeros((1, T, C), np.float32)
+    x[:, -8:], gy[:, :8] = rng.uniform(0.5, 1, (2, 1, 8, C))
+    dt, A = np.ones((1, T, C), np.float32), np.full((C, N), 2, np.float32)
+    Bv, Cv = rng.uniform(0.5, 1, (2, 1, T, 1, N)).astype(np.float32)
+    t = [m.dev(v) for v in (x, dt, A, Bv, Cv)]
+    y, h, ck = gdr.gdr_ssm_fwd(*t, softplus=False, return_ckpt=True)
+    g = gdr.gdr_ssm_bwd(m.dev(gy), *t, softplus=False, ckpt=ck if saved else None)
+    torch.cuda.synchronize()
+    y_r, h_r, _ = ssm.forward(x, dt, A, Bv, Cv, softplus=False)
+    g_r = ssm.backward(gy, x, dt, A, Bv, Cv, softplus=False)
+    for a, r in [(y, y_r), (h, h_r), *((g[k], g_r["d" + k]) for k in ("x", "dt", "A", "B", "C", "h0"))]:
+        np.testing.assert_allclose(a.double().cpu().numpy(), r, rtol=2.0 ** -16, atol=0)
