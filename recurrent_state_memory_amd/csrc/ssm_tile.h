@@ -269,9 +269,11 @@ __device__ inline void pass_segments(const Geo& q, const Place& s, int first, in
       if (j < n) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          // the factor's root, twice, and finite: a growing segment's may pass fp32 where
-          // what it multiplies is 0 or small
-          const float root = __builtin_amdgcn_exp2f(fminf(0.5f * A2[i] * d[j], 127.f));
+          // The factor's root, twice, and finite: a growing segment's may pass fp32 where what
+          // it multiplies is 0 or small.  Without decay, or where the steps sum to 0 (behind
+          // a row's end), it is 1 whatever the other one is; a NaN stays one.
+          const float half = A2[i] == 0.f || d[j] == 0.f ? 0.f : 0.5f * A2[i] * d[j];
+          const float root = __builtin_amdgcn_exp2f(half > 127.f ? 127.f : half);
           h[i] = fmaf(root, root * h[i], e[j][i]);
         }
       }
