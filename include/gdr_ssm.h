@@ -13,7 +13,8 @@
  *     y_t = u_t z_t sigmoid(z_t) with z, else u_t
  *
  * Channels of a group are neighbours: channel c belongs to group c / (C / G).  A <= 0
- * is the stable case and not checked.
+ * is the stable case and not checked; its values are held to [-2^64, 2^64], so that -Inf,
+ * or fp32's lowest value, is a state that every time step from 2^-56 on resets.
  *
  * A batch may be padded: row b has lens[b] tokens (its value is held to [0, T]), NULL
  * means T.  Tokens behind them are not read; their y and gradients are 0, the state

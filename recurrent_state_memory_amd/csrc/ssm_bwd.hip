@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_adjoint_kernel(gdr_ssm_bwd_ar
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     const int n = w * NS + i;
-    A2[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] * scan::kLog2e : 0.f;
+    A2[i] = n < q.N ? held(p.A[(size_t)s.c * q.N + n]) * scan::kLog2e : 0.f;
     K[i] = n < q.N && p.grad_h && s.seg == q.segs - 1 ? p.grad_h[((size_t)s.b * q.C + s.c) * q.N + n] : 0.f;
   }
   const float bias = p.dt_bias ? p.dt_bias[s.c] : 0.f;
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
   auto state = [&](int ch, int k) { return (ch * NW + w) * NS + k; };
   auto load_A = [&](int ch, float(&A)[NS]) {
 #pragma unroll
-    for (int k = 0; k < NS; ++k) A[k] = state(ch, k) < q.N ? p.A[(size_t)s.c * q.N + state(ch, k)] : 0.f;
+    for (int k = 0; k < NS; ++k) A[k] = state(ch, k) < q.N ? held(p.A[(size_t)s.c * q.N + state(ch, k)]) : 0.f;
   };
   float A[NS], A2[NS], Ks[NCH][NS], gA[NCH][NS];
 #pragma unroll

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_fwd_kernel(gdr_ssm_args p, Ge
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     const int n = w * NS + i;
-    A2[i] = n < q.N ? p.A[(size_t)s.c * q.N + n] * scan::kLog2e : 0.f;
+    A2[i] = n < q.N ? held(p.A[(size_t)s.c * q.N + n]) * scan::kLog2e : 0.f;
     h[i] = 0.f;
     if (n < q.N) {
       // h_out may be h0, so where segments run side by side only the first pass reads h0
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(gdr_ssm_step_args p, int 
   float u = 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    h[k] = fmaf(__builtin_amdgcn_exp2f(d * (A[k] * scan::kLog2e)), h[k], dx * Bv[k]);
+    h[k] = fmaf(__builtin_amdgcn_exp2f(d * (held(A[k]) * scan::kLog2e)), h[k], dx * Bv[k]);
     u = k < n ? fmaf(Cv[k], h[k], u) : u;
   }
   Run<float>::store(p.h_out + rc * p.N + n0, n, h);

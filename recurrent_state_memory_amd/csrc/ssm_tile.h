@@ -22,6 +22,7 @@ namespace gdr {
 namespace ssm {
 
 constexpr int kBlock = GDR_SSM_BLOCK;
+constexpr float kRate = 0x1p64f;   // decay rates are held to +-kRate
 
 struct Geo {
   int B, T, C, N, G;
@@ -246,6 +247,10 @@ struct Vectors {
 
 // d = softplus(pre) or pre.
 __device__ inline float time_step(float pre, bool softplus) { return softplus ? scan::softplus(pre) : pre; }
+
+// A rate as the kernels use it (a NaN stays one).  Behind a row's end the time step is 0 and
+// the slope of softplus too, and neither 0 A log2 e nor 0 A h H may be 0 times an Inf.
+__device__ inline float held(float A) { return __builtin_fabsf(A) > kRate ? __builtin_copysignf(kRate, A) : A; }
 
 // A state (an adjoint) taken through the segments from, from + dir, ... (to excluded): of
 // each one its end and the sum of its time steps.  Several are asked for at once, else
