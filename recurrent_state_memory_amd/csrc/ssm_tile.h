@@ -27,7 +27,7 @@ constexpr float kRate = 0x1p64f;   // decay rates are held to +-kRate
 struct Geo {
   int B, T, C, N, G;
   int each, nb;     // channels of a group, workgroups of them
-  int room;         // states that the waves have room for
+  int room;         // states that the backward's waves write partial sums of
   int Tp;           // T up to a whole block
   int segs, seg;    // segments of the tokens and their length, a multiple of kBlock
   __host__ __device__ unsigned blocks() const { return (unsigned)B * G * nb * segs; }
@@ -41,7 +41,8 @@ inline Geo geo_of(int B, int T, int C, int N, int G, bool backward) {
   q.B = B, q.T = T, q.C = C, q.N = N, q.G = G;
   q.each = C / G;
   q.nb = lanes_of_group(C, G);
-  q.room = N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64;
+  // waves of one state or two; those without one write nothing, but for 9 to 16 states
+  q.room = N <= 8 ? N : N <= 16 ? 16 : N + N % 2;
   q.Tp = (int)blocks_of(T) * kBlock;
   // Segments.  Forward: where the chains of channels are no more than half the CUs, two
   // workgroups a CU of 64 tokens at least (a second one a CU fills the first one's waits):
