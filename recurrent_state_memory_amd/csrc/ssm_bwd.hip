@@ -222,14 +222,14 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
   auto state = [&](int ch, int k) { return (ch * NW + w) * NS + k; };
   auto load_A = [&](int ch, float(&A)[NS]) {
 #pragma unroll
-    for (int k = 0; k < NS; ++k) A[k] = state(ch, k) < q.N ? held(p.A[(size_t)s.c * q.N + state(ch, k)]) : 0.f;
+    for (int k = 0; k < NS; ++k) A[k] = state(ch, k) < q.N ? p.A[(size_t)s.c * q.N + state(ch, k)] : 0.f;
   };
   float A[NS], A2[NS], Ks[NCH][NS], gA[NCH][NS];
 #pragma unroll
   for (int ch = NCH - 1; ch >= 0; --ch) {
     load_A(ch, A);
 #pragma unroll
-    for (int k = 0; k < NS; ++k) A2[k] = A[k] * scan::kLog2e, gA[ch][k] = 0.f;
+    for (int k = 0; k < NS; ++k) A[k] = held(A[k]), A2[k] = A[k] * scan::kLog2e, gA[ch][k] = 0.f;
     adjoint_behind<NS>(p, q, s, state(ch, 0), A2, ends, sums, Ks[ch]);
   }
   const float* const ck = ckpt + ((size_t)s.b * (q.Tp / kBlock) + t0 / kBlock) * nc + s.c;   // the states' checkpoints
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kWaves * 64) void ssm_bwd_kernel(gdr_ssm_bwd_args p
 #pragma unroll
       for (int k = 0; k < NS; ++k) {
         h[0][k] = nh[k];
-        if constexpr (NCH > 1) A[k] = nA[k], A2[k] = A[k] * scan::kLog2e;
+        if constexpr (NCH > 1) A[k] = held(nA[k]), A2[k] = A[k] * scan::kLog2e;
       }
       float* const vout = vout0 + (size_t)ch * (NW * NS) * 2 * q.Tp;
       // a wave without a state leaves the others its SIMD
