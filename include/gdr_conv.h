@@ -18,11 +18,13 @@
  *
  * Sizes: 2 <= K <= 8, 1 <= C <= 2^18, any B and T >= 1 with B * T < 2^30, B * T * C < 2^40
  * and B * ceil(C/256) * ceil(T/256) < 2^22.  Every pointer is aligned to its element;
- * channels move 16 bytes at a time, fastest where rows begin at multiples of 16 bytes.  Outputs overlap neither inputs nor each other
- * (GDR_ERR_ARG), except that state_out may equal state.  All arithmetic is fp32; y,
- * grad_x and grad_state are rounded once (RNE) to io_dtype, states are copied.  The sums
- * of grad_weight and grad_bias run in an order that the sizes fix.  NaN and Inf stay
- * within the K tokens of their channel that they reach (and grad_weight, grad_bias).
+ * channels move 16 bytes at a time, fastest where rows begin at multiples of 16 bytes.
+ * Outputs overlap neither inputs nor each other (GDR_ERR_ARG), except that state_out may
+ * equal state.  All arithmetic is fp32; y, grad_x and grad_state are rounded once (RNE) to
+ * io_dtype, states are copied.  The sums of grad_weight and grad_bias run in an order that
+ * the sizes fix.  NaN and Inf stay within the K tokens of their channel that they reach
+ * (backward: x through silu's slope reaches grad_x of K - 1 tokens on either side), and
+ * grad_weight and grad_bias of that channel.
  */
 #ifndef GDR_CONV_H
 #define GDR_CONV_H

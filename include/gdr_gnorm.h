@@ -20,7 +20,8 @@
  * R * G < 2^31, R * C < 2^40.  Every pointer is aligned to its element; rows move 16
  * bytes at a time, fastest where groups begin at multiples of 16 bytes.  Outputs
  * overlap neither inputs nor each other (GDR_ERR_ARG).  Sums are fp32, in an order
- * that depends on the sizes alone; y, grad_x and grad_z are rounded once (RNE) to
+ * that depends on the sizes alone (where the squares of a group pass fp32, its values
+ * being some 2^60, rstd is 0); y, grad_x and grad_z are rounded once (RNE) to
  * io_dtype.  NaN and Inf stay within their group of their row (and reach grad_weight
  * and grad_bias).
  */

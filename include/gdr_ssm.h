@@ -23,9 +23,9 @@
  * Sizes: 1 <= N <= 64, C a multiple of G, C <= 2^18, G * N <= 2^16, any B and T >= 1
  * with B * T < 2^30, B * T * C < 2^40 and B * G * ceil(C/G/64) < 2^22.  Every pointer is
  * aligned to its element.  Outputs overlap neither inputs nor each other (GDR_ERR_ARG),
- * except that h_out may equal h0 (and the step's h_out its h).  All arithmetic and states are fp32;
- * y and the gradients of io_dtype are rounded once (RNE); exponentials below fp32's
- * least normal number count as 0.  Sums run in an order that the sizes fix: no atomics
+ * except that h_out may equal h0 (and the step's h_out its h).  All arithmetic and states
+ * are fp32; y and the gradients of io_dtype are rounded once (RNE); exponentials below
+ * fp32's least normal number count as 0.  Sums run in an order that the sizes fix: no atomics
  * add numbers.  NaN propagates along its channel (in the backward also to the gradients
  * of the vectors and of A, D and dt_bias that it enters); an Inf may come out as NaN.
  */

@@ -2,10 +2,11 @@
 //
 // A thread holds one 16-byte run of channels (four channels in the backward) and walks a
 // stretch of tokens with the last K rows in registers, so x is read once (the K - 1 rows
-// ahead of a stretch come from the caches).  LX threads of a workgroup share a row, the other 256 / LX take further
-// stretches.  On 8 x 4096 x 2048 bf16 with 4 taps and silu the forward takes 50 us, HBM's
-// rate (5.4 TB/s); the backward 91 us (4.4 TB/s): its arithmetic, some 30 instructions an
-// element, takes about 60 of them.  Backward with eight channels a thread (two waves a SIMD):
+// ahead of a stretch come from the caches).  LX threads of a workgroup share a row, the
+// other 256 / LX take further stretches.  On 8 x 4096 x 2048 bf16 with 4 taps and silu the
+// forward takes 52 us, the rate of a large copy (5.2 TB/s; fp32 104 us with the launch); the
+// backward 91 us (4.4 TB/s; fp32 182): its arithmetic, some 30 instructions an element, takes
+// about 60 of them.  Backward with eight channels a thread (two waves a SIMD):
 // 99 us; rows asked for one step ahead, or runs that are known to be whole, cost the fourth
 // wave's registers: 111 and 100 us.
 #include <type_traits>
@@ -73,8 +74,8 @@ static Plan plan_of(int B, int T, int C, int n, int longest) {
   while (q.lx < 6 && (1 << q.lx) < runs) ++q.lx;
   const int LX = 1 << q.lx, LY = kThreads / LX;
   q.cols = (unsigned)((runs + LX - 1) / LX);
-  // 128 Ki threads fill the card (8 waves a SIMD); shorter stretches than 8 tokens read
-  // mostly rows of their neighbours
+  // 128 Ki threads are two waves a SIMD; shorter stretches than 8 tokens read mostly rows
+  // of their neighbours
   const long long threads = (long long)B * q.cols * LX;
   q.len = 8;
   while (q.len < longest && threads * ((T + q.len - 1) / q.len) > 131072) q.len *= 2;

@@ -11,7 +11,9 @@ namespace conv {
 
 constexpr int kMinK = 2, kMaxK = 8;
 
-// Workgroups of a launch stay below 2^22 (plan_of never makes more than this counts).
+// Workgroups of a launch stay below 2^22: with stretches of 64 tokens there are no more than
+// this counts, and shorter ones are taken only while all stretches together need at most
+// 128 Ki threads.
 constexpr bool too_many_tiles(int B, int T, int C) {
   return (long long)B * ((C + 255) / 256) * ((T + 255) / 256) >= (1LL << 22);
 }

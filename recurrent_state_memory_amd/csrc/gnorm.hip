@@ -1,11 +1,12 @@
 // gnorm.hip -- gated group norm forward and backward, gfx950.
 //
 // A group of a row is held in registers by L threads of NV 16-byte runs each (thread l has
-// runs l, l + L, ...; the forward asks for the next row ahead), so everything is read once: the mean, then the squares about it,
-// then the outputs.  L is a part of a wave for short groups (several groups side by side in
+// runs l, l + L, ...; the forward asks for the next row ahead), so everything is read once:
+// the mean, then the squares about it, then the outputs.  L is a part of a wave for short groups (several groups side by side in
 // a wave, no barrier) or up to 1024 threads.  Bound by HBM: 32768 x 2048 bf16 in 16 groups,
-// gated, forward 81 us (5.0 TB/s), backward 126 us (5.3 TB/s).  Of fp32 and bf16 groups of
-// more than 8192 values the backward spills up to 36 registers.
+// gated, forward 83 us (4.9 TB/s), backward 129 us (5.2 TB/s).  Of groups of more than 8192
+// values the backward spills up to 36 registers: 4096 rows of one group of 16384, gated, 298 us
+// in bf16 (2.3 TB/s; 8192 rows of 8192 149) and 383 in fp32 (3.5 TB/s), the forward 91 and 155.
 #include "chan_device.h"
 #include "col_join.h"
 #include "gnorm_kernels.h"

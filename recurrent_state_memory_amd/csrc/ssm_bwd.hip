@@ -9,14 +9,14 @@
 //
 // Bound by the issue of instructions, two waves a SIMD as in the forward: 16 slots a state and
 // token cannot be done without (6 again, 10 for the adjoint and the two sums), 518 us of the
-// 917 on 8 x 4096 x 2048 with 16 states, gated; 25 are issued, 6 of them for the sums over
+// 923 on 8 x 4096 x 2048 with 16 states, gated; 25 are issued, 6 of them for the sums over
 // lanes.  LDS and registers allow one workgroup a CU.  Half of a block's decays computed
 // twice instead of kept: 1060; LDS read where it is used: 1006; row lanes moved to
 // registers of their own before a multiply-add: 980 us.  (The same for all of a block makes
 // the compiler spill: 2880.)
 // More than 16 states go through each block in turns of 16 (8 x 2048 x 2048 bf16, gated, with
-// 32: 1070 us, 64: 2040), at the same rate as 16 do (476); two states at a time with half a
-// block's tokens in registers took 1570 and 2790.  Waves without a state skip the recurrence
+// 32: 1087 us, 64: 2072), a state at 7 to 13 % more than where there are 16 (482); two states
+// at a time with half a block's tokens in registers took 1570 and 2790.  Waves without a state skip the recurrence
 // (4 states: 330 -> 284 us).
 #include "col_join.h"
 #include "ssm_tile.h"
